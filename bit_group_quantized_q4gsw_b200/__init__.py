@@ -8,3 +8,7 @@ from .binding import (  # noqa: F401
     q4gsw_layout_version, q4gsw_linear_bwd_input,
     q4gsw_linear_fwd, q4gsw_packed_bytes, q4gsw_prepack, q4gsw_prepack_f32s, q4gsw_qkv_fwd, q4gsw_status_str, q4gsw_unpack,
 )
+from .layer import (  # noqa: F401
+    q4gsw_distill_bwd, q4gsw_distill_fwd, q4gsw_distill_step, q4gsw_gated_bwd, q4gsw_gated_fwd, q4gsw_linear_act_bwd,
+    q4gsw_linear_act_fwd, q4gsw_prepack_gated,
+)

@@ -56,6 +56,27 @@ SIGNATURES = [
     ("q4gsw_status_str", ctypes.c_char_p, [_I]),
 ]
 
+# the same for include/q4gsw_layer.h (called from layer.py)
+_F = ctypes.c_float
+_GATED_BWD = [_VP, _I, _I, _I, _VP, _VP, _I, _I, _VP, _VP, _VP]
+_ACT_FWD = [_VP, _I, _I, _I, _VP, _I, _VP, _I, _VP, _VP, _VP, _VP]
+_ACT_BWD = [_VP, _I, _I, _I, _VP, _VP, _I, _I, _VP, _VP, _VP, _VP]
+LAYER_SIGNATURES = [
+    ("q4gsw_prepack_gated", _I, [_VP, _VP, _VP, _VP, _I, _I, _I, _VP, _SZ, _VP]),
+    ("q4gsw_prepack_gated_f32s", _I, [_VP, _VP, _VP, _VP, _I, _I, _I, _VP, _SZ, _VP]),
+    ("q4gsw_gated_fwd", _I, [_VP, _I, _I, _I, _VP, _I, _I, _VP, _VP, _VP]),
+    ("q4gsw_gated_fwd_f32s", _I, [_VP, _I, _I, _I, _VP, _I, _I, _VP, _VP, _VP]),
+    ("q4gsw_gated_bwd", _I, _GATED_BWD),
+    ("q4gsw_gated_bwd_f32s", _I, _GATED_BWD),
+    ("q4gsw_linear_act_fwd", _I, _ACT_FWD),
+    ("q4gsw_linear_act_fwd_f32s", _I, _ACT_FWD),
+    ("q4gsw_linear_act_bwd", _I, _ACT_BWD),
+    ("q4gsw_linear_act_bwd_f32s", _I, _ACT_BWD),
+    ("q4gsw_distill_fwd", _I, [_VP, _I, _I, _I, _VP, _VP, _I, _I, _F, _VP, _VP, _VP]),
+    ("q4gsw_distill_bwd", _I, [_VP, _I, _I, _I, _VP, _VP, _VP, _I, _I, _F, _VP, _VP, _VP]),
+    ("q4gsw_distill_step", _I, [_VP, _I, _I, _I, _VP, _VP, _I, _I, _F, _VP, _VP, _VP, _VP, _VP]),
+]
+
 _lib = None
 
 
@@ -82,7 +103,7 @@ def library(path: str | None = None) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"q4gsw CUDA library not found at {path}; run `python -m bit_group_quantized_q4gsw_b200.build`")
     lib = ctypes.CDLL(path)
-    for name, res, args in SIGNATURES:
+    for name, res, args in SIGNATURES + LAYER_SIGNATURES:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

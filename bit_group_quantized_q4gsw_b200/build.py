@@ -45,7 +45,7 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
-    cmd = [nvcc_path(), "-std=c++17", "-O3", "-lineinfo", *ARCH_FLAGS, "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc_path(), "-std=c++17", "-O3", "-lineinfo", "--threads", "0", *ARCH_FLAGS, "-shared", "-Xcompiler", "-fPIC",
            "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"),
            "-o", LIB_PATH + ".tmp", *sources()]
     if verbose:

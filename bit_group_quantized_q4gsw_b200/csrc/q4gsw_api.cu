@@ -15,6 +15,7 @@
 #include <cstring>
 
 #include "../../include/q4gsw.h"
+#include "q4gsw_api_common.h"
 #include "q4gsw_common.cuh"
 #include "q4gsw_internal.h"
 
@@ -44,22 +45,17 @@ int sm_count(int dev) {
 
 }  // namespace q4gsw
 
-using namespace q4gsw;
+namespace q4gsw {
 
-namespace {
-
-thread_local char g_route[160] = "none";
+static thread_local char g_route[160] = "none";
 
 void set_route(const char* s) {
   std::strncpy(g_route, s, sizeof(g_route) - 1);
   g_route[sizeof(g_route) - 1] = 0;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+static bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
-bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
-
-// Shape rules shared by every entry point.
 q4gsw_status check_weight_shape(int N, int K, int gs) {
   if (N <= 0 || K <= 0 || gs <= 0) return Q4GSW_ERR_SHAPE;
   if (N % 4 || K % 4 || gs % 4) return Q4GSW_ERR_SHAPE;        // the page's constraints
@@ -68,13 +64,9 @@ q4gsw_status check_weight_shape(int N, int K, int gs) {
   return Q4GSW_OK;
 }
 
-q4gsw_status from_cuda(cudaError_t e) { return e == cudaSuccess ? Q4GSW_OK : Q4GSW_ERR_CUDA; }
+}  // namespace q4gsw
 
-// Token counts up to this run the tensor-core GEMV (weight streaming); above
-// it the tcgen05 GEMM.
-constexpr int kGemvMaxM = 16;
-
-}  // namespace
+using namespace q4gsw;
 
 namespace {
 
@@ -230,7 +222,7 @@ const char* q4gsw_status_str(q4gsw_status s) {
     case Q4GSW_ERR_CUDA: return "CUDA runtime error";
     case Q4GSW_ERR_SIZE: return "buffer too small";
     case Q4GSW_ERR_TIMEOUT: return "a kernel wait ran out (results of the calls since the last check are invalid)";
-    case Q4GSW_ERR_INDEX: return "an embedding index was outside [0, N) (its row was written as zeros)";
+    case Q4GSW_ERR_INDEX: return "an embedding index was outside [0, N) (its row was written as zeros), or a teacher's token id outside [0, V) (taken as padding)";
   }
   return "unknown status";
 }

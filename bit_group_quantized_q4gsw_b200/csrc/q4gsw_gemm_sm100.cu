@@ -32,9 +32,12 @@
 
 #include <cmath>
 #include <cstdio>
+#include <cstring>
 #include <cstdlib>
+#include <type_traits>
 
 #include "q4gsw_common.cuh"
+#include "q4gsw_epilogue.cuh"
 #include "q4gsw_internal.h"
 #include "q4gsw_sm100.cuh"
 
@@ -83,8 +86,9 @@ struct Smem {
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
+template <typename Out>
 struct Args {
-  OutSplit out;
+  Out out;
   int M, N, K, gs;
   int out_cols;       // forward: N, backward: K
   int stages_total;   // contraction / TK
@@ -120,10 +124,10 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
-template <bool BWD, int ST, int SCB, int MSUB, bool F32S>
+template <bool BWD, int ST, int SCB, int MSUB, bool F32S, typename Out>
 __global__ void __launch_bounds__(kThreads, 1)
 q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_constant__ CUtensorMap map_pk,
-                  const __grid_constant__ CUtensorMap map_sc, const Args args) {
+                  const __grid_constant__ CUtensorMap map_sc, const Args<Out> args) {
   using namespace sm100;
   using SM = Smem<ST, SCB, MSUB>;
   constexpr int SB = F32S ? 4 : 2;   // bytes per scale
@@ -342,12 +346,7 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
   if (epi) have_acc = mbar_wait(&ctl->accfull, 0, abort_flag, &g_device_error, 16u);
   if (epi && have_acc) tc_fence_after();
   auto store4 = [&](int m, int n, float4 val) {
-    const OutSplit& o = args.out;
-    float* dst;
-    if (n < o.n1) dst = o.y0 + (size_t)m * o.n1 + n;
-    else if (n < o.n2) dst = o.y1 + (size_t)m * (o.n2 - o.n1) + (n - o.n1);
-    else dst = o.y2 + (size_t)m * (o.N - o.n2) + (n - o.n2);
-    *reinterpret_cast<float4*>(dst) = val;
+    epi_store4(args.out, (size_t)m, n, val, epi_load4(args.out, (size_t)m, n));
   };
 #pragma unroll 1
   for (int ms = 0; ms < MSUB; ++ms) {
@@ -467,12 +466,12 @@ static double stage_time(int msub) { return msub == 2 ? 1.6 : 1.0; }
 // (stages / S * stage time + fixed overhead: 2 stage times per accumulator, or
 // 8 with the cluster reduction), where waves(S) uses how many S-CTA clusters
 // the device can hold at once (a GPC must host a whole cluster).
-template <bool BWD, int ST, int SCB, int MSUB, bool F32S>
+template <bool BWD, int ST, int SCB, int MSUB, bool F32S, typename Out>
 static cudaError_t gemm_variant(const CUtensorMap& map_act, const CUtensorMap& map_pk, const CUtensorMap& map_sc,
-                                const gemm::Args& a, int tiles_n, cudaStream_t stream, bool launch, int* S_out,
+                                const gemm::Args<Out>& a, int tiles_n, cudaStream_t stream, bool launch, int* S_out,
                                 double* cost_out) {
   using namespace gemm;
-  auto kern = q4gsw_gemm_kernel<BWD, ST, SCB, MSUB, F32S>;
+  auto kern = q4gsw_gemm_kernel<BWD, ST, SCB, MSUB, F32S, Out>;
   constexpr int smem = Smem<ST, SCB, MSUB>::BYTES;
   static PerDeviceOnce attr_once;
   static std::atomic<int> max_clusters[kMaxDevices][9];
@@ -534,9 +533,9 @@ static int forced_msub() {
   return g == kGemmSs1 ? 1 : g == kGemmSs2 ? 2 : 0;
 }
 
-template <bool BWD, bool F32S>
+template <bool BWD, bool F32S, typename Out>
 static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, const uint16_t* act, int M,
-                                    OutSplit out, cudaStream_t stream, char* route, int route_len) {
+                                    Out out, cudaStream_t stream, char* route, int route_len) {
   using namespace gemm;
   constexpr int SB = F32S ? 4 : 2;
   const CUtensorMapDataType sdt = F32S ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -561,7 +560,7 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
   }
   if (!ok || sc_bytes > (F32S ? 4096 : 2048)) return cudaErrorInvalidValue;
 
-  Args a;
+  Args<Out> a;
   a.sc_bytes = sc_bytes;
   a.out = out;
   a.M = M;
@@ -583,12 +582,12 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
                      CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
     if (sc_bytes <= 1024)
-      return msub == 2 ? gemm_variant<BWD, 3, 1024, 2, F32S>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost)
-                       : gemm_variant<BWD, 5, 1024, 1, F32S>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost);
+      return msub == 2 ? gemm_variant<BWD, 3, 1024, 2, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost)
+                       : gemm_variant<BWD, 5, 1024, 1, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost);
     if (sc_bytes <= 2048)
-      return msub == 2 ? gemm_variant<BWD, 3, 2048, 2, F32S>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost)
-                       : gemm_variant<BWD, 4, 2048, 1, F32S>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost);
-    return gemm_variant<BWD, 4, 4096, 1, F32S>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost);
+      return msub == 2 ? gemm_variant<BWD, 3, 2048, 2, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost)
+                       : gemm_variant<BWD, 4, 2048, 1, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost);
+    return gemm_variant<BWD, 4, 4096, 1, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost);
   };
   int msub = one_acc_only ? 1 : forced_msub();
   int S = 1;
@@ -607,6 +606,10 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
   if (route)
     snprintf(route, route_len, "tcgen05_gemm_%s launches=1 tile=%dx%dx%d stages=%d+%d grid=%dx%dx%d",
              BWD ? "bwd" : "fwd", BM * msub, BN, TK, st, WST, tiles_n, (M + BM * msub - 1) / (BM * msub), S);
+  if (route && std::is_same_v<Out, Epi>) {
+    const size_t len = strlen(route);
+    snprintf(route + len, route_len - len, " out=epi");
+  }
   return e;
 }
 
@@ -616,6 +619,7 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
 #include "q4gsw_gemm_ts.cuh"
 #include "q4gsw_gemv_tma.cuh"
 #include "q4gsw_dq8ca_tma.cuh"
+#include "q4gsw_distill.cuh"
 
 namespace q4gsw {
 
@@ -658,6 +662,27 @@ cudaError_t launch_gemm_bwd(const void* packed, int N, int K, int gs, bool f32s,
                 : launch_gemm_impl<true, false>(packed, N, K, gs, d_out, M, o, stream, route, route_len);
   return f32s ? launch_gemm_ts_impl<true, true>(packed, N, K, gs, d_out, M, o, stream, route, route_len)
               : launch_gemm_ts_impl<true, false>(packed, N, K, gs, d_out, M, o, stream, route, route_len);
+}
+
+// The products with fp16 outputs through an epilogue (any M): the same routes.
+template <bool BWD, bool F32S>
+static cudaError_t product_epi(const void* packed, int N, int K, int gs, const uint16_t* act, int M, const Epi& out,
+                               cudaStream_t stream, char* route, int route_len) {
+  if (M <= kGemvMaxM) {
+    return BWD ? gemv_tma_bwd_impl(packed, N, K, gs, F32S, act, M, out, stream, route, route_len)
+               : gemv_tma_fwd_impl(packed, N, K, gs, F32S, act, M, out, stream, route, route_len);
+  }
+  return use_ss_route(M) ? launch_gemm_impl<BWD, F32S>(packed, N, K, gs, act, M, out, stream, route, route_len)
+                         : launch_gemm_ts_impl<BWD, F32S>(packed, N, K, gs, act, M, out, stream, route, route_len);
+}
+
+cudaError_t launch_product_epi(bool bwd, const void* packed, int N, int K, int gs, bool f32s, const uint16_t* act,
+                               int M, const Epi& out, cudaStream_t stream, char* route, int route_len) {
+  if (bwd)
+    return f32s ? product_epi<true, true>(packed, N, K, gs, act, M, out, stream, route, route_len)
+                : product_epi<true, false>(packed, N, K, gs, act, M, out, stream, route, route_len);
+  return f32s ? product_epi<false, true>(packed, N, K, gs, act, M, out, stream, route, route_len)
+              : product_epi<false, false>(packed, N, K, gs, act, M, out, stream, route, route_len);
 }
 
 __global__ void q4gsw_error_exchange_kernel(unsigned int slot) {

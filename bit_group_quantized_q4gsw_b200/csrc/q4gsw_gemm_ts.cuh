@@ -65,8 +65,9 @@ struct Smem {
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
+template <typename Out>
 struct Args {
-  OutSplit out;
+  Out out;
   int M, N, K, gs;
   int rows_out;       // weight-side extent of the output: N (forward) or K (backward)
   int stages_total;
@@ -125,12 +126,12 @@ __device__ __forceinline__ uint32_t nibbles_minus8(uint32_t v) {
 // thread first issues the loads of up to kPer items (S each), then adds and
 // stores: remote loads are latency-bound, and one item at a time left ~4 of
 // those latencies in a row per thread.
-template <int S>
+template <int S, typename Out>
 __device__ __forceinline__ void copy_out(const float* stage_f32, bool pushed, int slot_floats, int row_b, int row_e,
-                                         int t0, int f0, const Args& args) {
+                                         int t0, int f0, const Args<Out>& args) {
   using namespace sm100;
   constexpr int kPer = S == 1 ? 8 : (12 / S > 0 ? 12 / S : 1);   // at most 12 float4 in flight
-  const OutSplit& o = args.out;
+  using Operand = decltype(epi_load4(args.out, size_t(0), 0));   // what the epilogue reads (nothing for fp32 rows)
   uint32_t src[S];   // rank qq's partial rows, in the cluster's shared window
 #pragma unroll
   for (int qq = 0; qq < S; ++qq)
@@ -140,6 +141,7 @@ __device__ __forceinline__ void copy_out(const float* stage_f32, bool pushed, in
   const int total = (row_e - row_b) * (BW / 4);
   for (int base = threadIdx.x; base < total; base += kThreads * kPer) {
     float4 part[kPer][S];
+    Operand opd[kPer];
     bool ok[kPer];
     int offs[kPer];
 #pragma unroll
@@ -150,6 +152,7 @@ __device__ __forceinline__ void copy_out(const float* stage_f32, bool pushed, in
       ok[u] = idx < total && t0 + row_b + row < args.M && f0 + 4 * c4 < args.rows_out;
       if (ok[u]) {
         const uint32_t o4 = 4u * (uint32_t)((r0 + row) * BW + 4 * c4);
+        opd[u] = epi_load4(args.out, (size_t)(t0 + row_b + row), f0 + 4 * c4);
 #pragma unroll
         for (int qq = 0; qq < S; ++qq)
           part[u][qq] = S == 1 ? *reinterpret_cast<const float4*>(stage_f32 + (r0 + row) * BW + 4 * c4)
@@ -168,21 +171,17 @@ __device__ __forceinline__ void copy_out(const float* stage_f32, bool pushed, in
         acc.w += part[u][qq].w;
       }
       const int m = t0 + row_b + offs[u] / BW, f = f0 + offs[u] % BW;
-      float* dst;
-      if (f < o.n1) dst = o.y0 + (size_t)m * o.n1 + f;
-      else if (f < o.n2) dst = o.y1 + (size_t)m * (o.n2 - o.n1) + (f - o.n1);
-      else dst = o.y2 + (size_t)m * (o.N - o.n2) + (f - o.n2);
-      *reinterpret_cast<float4*>(dst) = acc;
+      epi_store4(args.out, (size_t)m, f, acc, opd[u]);
     }
   }
 }
 
-template <bool BWD, int ST, bool F32S>
+template <bool BWD, int ST, bool F32S, typename Out>
 __global__ void __launch_bounds__(kThreads, 1)
 q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_constant__ CUtensorMap map_pk,
                      const __grid_constant__ CUtensorMap map_sc, const __grid_constant__ CUtensorMap map_y0,
                      const __grid_constant__ CUtensorMap map_y1, const __grid_constant__ CUtensorMap map_y2,
-                     const __grid_constant__ CUtensorMap map_ad, const Args args) {
+                     const __grid_constant__ CUtensorMap map_ad, const Args<Out> args) {
   using namespace sm100;
   static_assert(ST <= kMaxST, "barrier arrays and TMEM slots");
   using SM = Smem<ST, F32S ? 2048 : 1024>;
@@ -478,7 +477,6 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
     have_acc = __all_sync(0xffffffffu, have_acc);
     if (have_acc) tc_fence_after();
   }
-  const OutSplit& o = args.out;
   float* stage_f32 = reinterpret_cast<float*>(smem);   // the operand ring, idle by now
   // Park the tile in this CTA's shared memory as [token][128 features].
   auto park = [&] {
@@ -500,7 +498,10 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
     // One tensor store of the [bt][128] fp32 tile (rows past M and features
     // past the output clipped by the map), or the threads' copy-out.
     park();
-    if (args.tma_out) {
+    bool stored = false;
+    if constexpr (std::is_same_v<Out, OutSplit>) {
+      if (args.tma_out) {
+      const OutSplit& o = args.out;
       const CUtensorMap* my = f0 < o.n1 ? &map_y0 : (f0 < o.n2 ? &map_y1 : &map_y2);
       const int c0 = f0 < o.n1 ? f0 : (f0 < o.n2 ? f0 - o.n1 : f0 - o.n2);
       fence_proxy_async_smem();
@@ -510,7 +511,10 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
         bulk_commit();
         bulk_wait_read_all();
       }
-    } else {
+      stored = true;
+      }
+    }
+    if (!stored) {
       __syncthreads();
       if (!*abort_flag) copy_out<1>(stage_f32, false, 0, 0, args.bt, t0, f0, args);
     }
@@ -597,9 +601,9 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-template <bool BWD, bool F32S>
+template <bool BWD, bool F32S, typename Out>
 static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs, const uint16_t* act, int M,
-                                       OutSplit out, cudaStream_t stream, char* route, int route_len,
+                                       Out out, cudaStream_t stream, char* route, int route_len,
                                        const AdapterRef* ad = nullptr) {
   using namespace ts;
   constexpr int ST = F32S ? 5 : 6;
@@ -610,7 +614,7 @@ static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs,
   const Layout L = layout_of(N, K, gs, SB);
   const void* scales = pk + L.scales_offset;
   const int G = K / gs;
-  Args a;
+  Args<Out> a;
   a.out = out;
   a.M = M;
   a.N = N;
@@ -648,6 +652,10 @@ static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs,
   // them; otherwise the threads write the outputs.
   CUtensorMap map_y[3];
   auto make_out_maps = [&](int bt) -> bool {
+    if constexpr (!std::is_same_v<Out, OutSplit>) {
+      map_y[0] = map_y[1] = map_y[2] = map_act;   // never read: an epilogue is applied by the threads
+      return false;
+    } else {
     const int nb[3] = {0, out.n1, out.n2};
     const int ne[3] = {out.n1, out.n2, out.N};
     float* const yb[3] = {out.y0, out.y1, out.y2};
@@ -664,6 +672,7 @@ static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs,
     }
     if (!tma_out) map_y[0] = map_y[1] = map_y[2] = map_act;   // never read
     return tma_out;
+    }
   };
   a.tma_out = make_out_maps(a.bt) ? 1 : 0;
 
@@ -680,7 +689,7 @@ static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs,
     a.ad_r = ad->r;
     a.ad_ld = BWD ? K : ad->r;
   }
-  auto kern = q4gsw_gemm_ts_kernel<BWD, ST, F32S>;
+  auto kern = q4gsw_gemm_ts_kernel<BWD, ST, F32S, Out>;
   constexpr int smem = Smem<ST, SC_BYTES>::BYTES;
   static PerDeviceOnce attr_once;
   static std::atomic<int> max_clusters[kMaxDevices][9];
@@ -758,7 +767,7 @@ static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs,
   cfg.gridDim = dim3(tiles_f, tiles_t, best_S);
   if (route)
     snprintf(route, route_len, "tcgen05_ts_gemm_%s launches=1 tile=%dx%dx%d stages=%d+%d grid=%dx%dx%d out=%s%s",
-             BWD ? "bwd" : "fwd", BW, a.bt, TK, ST, ST, tiles_f, tiles_t, best_S, a.tma_out ? "tma" : "st",
+             BWD ? "bwd" : "fwd", BW, a.bt, TK, ST, ST, tiles_f, tiles_t, best_S, std::is_same_v<Out, Epi> ? "epi" : a.tma_out ? "tma" : "st",
              ad ? " adapter_stage=1" : "");
   return cudaLaunchKernelEx(&cfg, kern, map_act, map_pk, map_sc, map_y[0], map_y[1], map_y[2], map_ad, a);
 }

@@ -104,10 +104,10 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 // slices), cluster = (1, S, 1).  SPG = 16-column steps per scale group
 // (1: gs 16, 2: gs 32, 4: gs 64 or 128, where a warp's 64-column block is one
 // group; 8: gs >= 256, where a group spans the warp's blocks of several stages).
-template <int NT, int SPG, bool F32S, bool XS>
+template <int NT, int SPG, bool F32S, bool XS, typename Out>
 __global__ void __launch_bounds__(FwdCfg<NT, SPG, F32S, XS>::THREADS, FwdCfg<NT, SPG, F32S, XS>::MINB)
 q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __grid_constant__ CUtensorMap map_sc,
-                          const __grid_constant__ CUtensorMap map_x, const __half* __restrict__ x, OutSplit out,
+                          const __grid_constant__ CUtensorMap map_x, const __half* __restrict__ x, Out out,
                           int M, int N, int K, int gs, int stages_total) {
   using namespace sm100;
   using C = FwdCfg<NT, SPG, F32S, XS>;
@@ -388,16 +388,31 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
   if (!(S > 1 ? cluster_any_abort(cluster, &ctl->abort, S) : *abort_flag)) {
     const int rk = S > 1 ? (int)cluster.block_rank() : 0;
     const int tb = rk * Mz / S, te = (rk + 1) * Mz / S;
-    for (int e = threadIdx.x; e < (te - tb) * 64; e += C::THREADS) {
-      const int tok = tb + (e >> 6), nl = e & 63;
-      const int n = n0 + nl;
-      if (n >= N) continue;
-      float v = 0.f;
-      for (int q = 0; q < S; ++q) v += (q == rk ? red : cluster.map_shared_rank(red, q))[tok * 64 + nl];
-      const size_t m = (size_t)(tok0 + tok);
-      if (n < out.n1) out.y0[m * out.n1 + n] = v;
-      else if (n < out.n2) out.y1[m * (out.n2 - out.n1) + (n - out.n1)] = v;
-      else out.y2[m * (out.N - out.n2) + (n - out.n2)] = v;
+    if constexpr (std::is_same_v<Out, OutSplit>) {
+      for (int e = threadIdx.x; e < (te - tb) * 64; e += C::THREADS) {
+        const int tok = tb + (e >> 6), nl = e & 63;
+        const int n = n0 + nl;
+        if (n >= N) continue;
+        float v = 0.f;
+        for (int q = 0; q < S; ++q) v += (q == rk ? red : cluster.map_shared_rank(red, q))[tok * 64 + nl];
+        const size_t m = (size_t)(tok0 + tok);
+        if (n < out.n1) out.y0[m * out.n1 + n] = v;
+        else if (n < out.n2) out.y1[m * (out.n2 - out.n1) + (n - out.n1)] = v;
+        else out.y2[m * (out.N - out.n2) + (n - out.n2)] = v;
+      }
+    } else {
+      // pairs of features (N % 8 == 0: a pair is wholly inside or outside)
+      for (int e = threadIdx.x; e < (te - tb) * 32; e += C::THREADS) {
+        const int tok = tb + (e >> 5), nl = 2 * (e & 31);
+        if (n0 + nl >= N) continue;
+        float2 v = make_float2(0.f, 0.f);
+        for (int q = 0; q < S; ++q) {
+          const float2 p = *reinterpret_cast<const float2*>((q == rk ? red : cluster.map_shared_rank(red, q)) + tok * 64 + nl);
+          v.x += p.x;
+          v.y += p.y;
+        }
+        epi_store2(out, (size_t)(tok0 + tok), n0 + nl, v.x, v.y);
+      }
     }
   }
   if (S > 1) cluster.sync();
@@ -438,10 +453,10 @@ struct BwdCfg {
   static_assert(BYTES <= 113 * 1024, "two CTAs per SM");
 };
 
-template <int NT, int SPB, bool F32S>  // SPB scale groups per 64-column block: 1 (gs >= 64), 2 (gs 32), 4 (gs 16)
+template <int NT, int SPB, bool F32S, typename Out>  // SPB scale groups per 64-column block: 1 (gs >= 64), 2 (gs 32), 4 (gs 16)
 __global__ void __launch_bounds__(kBwdThreads, 2)
 q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __grid_constant__ CUtensorMap map_sc,
-                    const __grid_constant__ CUtensorMap map_d, float* __restrict__ dx, int M, int N, int K,
+                    const __grid_constant__ CUtensorMap map_d, Out dx, int M, int N, int K,
                     int gs, int stages_total) {
   using namespace sm100;
   using C = BwdCfg<NT, F32S>;
@@ -635,12 +650,26 @@ q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
     const int rk = S > 1 ? (int)cluster.block_rank() : 0;
     const int tb = rk * Mz / S, te = (rk + 1) * Mz / S;
     const int kw = min(128, K - kbase);
-    for (int e = tb * 128 + threadIdx.x; e < te * 128; e += kBwdThreads) {
-      const int tok = e >> 7, kl = e & 127;
-      if (kl >= kw) continue;
-      float v = 0.f;
-      for (int q = 0; q < S; ++q) v += (q == rk ? cta_part : cluster.map_shared_rank(cta_part, q))[e];
-      dx[(size_t)(tok0 + tok) * K + kbase + kl] = v;
+    if constexpr (std::is_same_v<Out, float*>) {
+      for (int e = tb * 128 + threadIdx.x; e < te * 128; e += kBwdThreads) {
+        const int tok = e >> 7, kl = e & 127;
+        if (kl >= kw) continue;
+        float v = 0.f;
+        for (int q = 0; q < S; ++q) v += (q == rk ? cta_part : cluster.map_shared_rank(cta_part, q))[e];
+        dx[(size_t)(tok0 + tok) * K + kbase + kl] = v;
+      }
+    } else {
+      for (int e = tb * 128 + 2 * threadIdx.x; e < te * 128; e += 2 * kBwdThreads) {
+        const int tok = e >> 7, kl = e & 127;
+        if (kl >= kw) continue;   // kw is a multiple of 64
+        float2 v = make_float2(0.f, 0.f);
+        for (int q = 0; q < S; ++q) {
+          const float2 p = *reinterpret_cast<const float2*>((q == rk ? cta_part : cluster.map_shared_rank(cta_part, q)) + e);
+          v.x += p.x;
+          v.y += p.y;
+        }
+        epi_store2(dx, (size_t)(tok0 + tok), kbase + kl, v.x, v.y);
+      }
     }
   }
   if (S > 1) cluster.sync();
@@ -651,12 +680,12 @@ q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-template <int NT, int SPG, bool F32S, bool XS>
+template <int NT, int SPG, bool F32S, bool XS, typename Out>
 static cudaError_t launch_gemv_tma_variant(const CUtensorMap& map_pk, const CUtensorMap& map_sc,
-                                           const CUtensorMap& map_x, const __half* x, OutSplit out, int M, int N,
+                                           const CUtensorMap& map_x, const __half* x, Out out, int M, int N,
                                            int K, int gs, int stages_total, dim3 grid, cudaStream_t stream) {
   using C = gv::FwdCfg<NT, SPG, F32S, XS>;
-  auto kern = gv::q4gsw_gemv_fwd_tma_kernel<NT, SPG, F32S, XS>;
+  auto kern = gv::q4gsw_gemv_fwd_tma_kernel<NT, SPG, F32S, XS, Out>;
   static PerDeviceOnce attr_once;
   {
     cudaError_t e = once_per_device(attr_once, current_device(), [&] {
@@ -681,8 +710,9 @@ static cudaError_t launch_gemv_tma_variant(const CUtensorMap& map_pk, const CUte
   return cudaLaunchKernelEx(&cfg, kern, map_pk, map_sc, map_x, x, out, M, N, K, gs, stages_total);
 }
 
-cudaError_t launch_gemv_tma_fwd(const void* packed, int N, int K, int gs, bool f32s, const uint16_t* x, int M,
-                                OutSplit out, cudaStream_t stream, char* route, int route_len) {
+template <typename Out>
+static cudaError_t gemv_tma_fwd_impl(const void* packed, int N, int K, int gs, bool f32s, const uint16_t* x, int M,
+                                     Out out, cudaStream_t stream, char* route, int route_len) {
   const uint8_t* pk = static_cast<const uint8_t*>(packed);
   const int sb = f32s ? 4 : 2;
   const Layout L = layout_of(N, K, gs, sb);
@@ -733,13 +763,20 @@ cudaError_t launch_gemv_tma_fwd(const void* packed, int N, int K, int gs, bool f
 #undef Q4_TMA_FWD
 #undef Q4_TMA_FWD_X
   if (route)
-    snprintf(route, route_len, "gemv_tma_fwd launches=1 nt=%d tiles=%d splits=%d zslices=%d stages=%d%s", NT, tiles,
-             S, zs, stages_total, xs ? " x=staged" : "");
+    snprintf(route, route_len, "gemv_tma_fwd launches=1 nt=%d tiles=%d splits=%d zslices=%d stages=%d%s%s", NT, tiles,
+             S, zs, stages_total, xs ? " x=staged" : "", std::is_same_v<Out, Epi> ? " out=epi" : "");
   return e;
 }
 
-cudaError_t launch_gemv_tma_bwd(const void* packed, int N, int K, int gs, bool f32s, const uint16_t* d_out, int M,
-                                float* d_x, cudaStream_t stream, char* route, int route_len) {
+cudaError_t launch_gemv_tma_fwd(const void* packed, int N, int K, int gs, bool f32s, const uint16_t* x, int M,
+                                OutSplit out, cudaStream_t stream, char* route, int route_len) {
+  return gemv_tma_fwd_impl(packed, N, K, gs, f32s, x, M, out, stream, route, route_len);
+}
+
+// Out: float* (fp32 rows) or Epi (fp16 rows)
+template <typename Out>
+static cudaError_t gemv_tma_bwd_impl(const void* packed, int N, int K, int gs, bool f32s, const uint16_t* d_out, int M,
+                                     Out d_x, cudaStream_t stream, char* route, int route_len) {
   const uint8_t* pk = static_cast<const uint8_t*>(packed);
   const int sb = f32s ? 4 : 2;
   const Layout L = layout_of(N, K, gs, sb);
@@ -786,17 +823,22 @@ cudaError_t launch_gemv_tma_bwd(const void* packed, int N, int K, int gs, bool f
   };
   cudaError_t e;
 #define Q4_TMA_BWD(NT_, SPB_)                                                                        \
-  (f32s ? launch(gv::q4gsw_gemv_bwd_tma_kernel<NT_, SPB_, true>, gv::BwdCfg<NT_, true>::BYTES)       \
-        : launch(gv::q4gsw_gemv_bwd_tma_kernel<NT_, SPB_, false>, gv::BwdCfg<NT_, false>::BYTES))
+  (f32s ? launch(gv::q4gsw_gemv_bwd_tma_kernel<NT_, SPB_, true, Out>, gv::BwdCfg<NT_, true>::BYTES)       \
+        : launch(gv::q4gsw_gemv_bwd_tma_kernel<NT_, SPB_, false, Out>, gv::BwdCfg<NT_, false>::BYTES))
   if (NT == 1)
     e = spb == 1 ? Q4_TMA_BWD(1, 1) : spb == 2 ? Q4_TMA_BWD(1, 2) : Q4_TMA_BWD(1, 4);
   else
     e = spb == 1 ? Q4_TMA_BWD(2, 1) : spb == 2 ? Q4_TMA_BWD(2, 2) : Q4_TMA_BWD(2, 4);
 #undef Q4_TMA_BWD
   if (route)
-    snprintf(route, route_len, "gemv_tma_bwd launches=1 nt=%d tiles=%d splits=%d zslices=%d stages=%d", NT, tiles, S,
-             zs, stages_total);
+    snprintf(route, route_len, "gemv_tma_bwd launches=1 nt=%d tiles=%d splits=%d zslices=%d stages=%d%s", NT, tiles, S,
+             zs, stages_total, std::is_same_v<Out, Epi> ? " out=epi" : "");
   return e;
+}
+
+cudaError_t launch_gemv_tma_bwd(const void* packed, int N, int K, int gs, bool f32s, const uint16_t* d_out, int M,
+                                float* d_x, cudaStream_t stream, char* route, int route_len) {
+  return gemv_tma_bwd_impl(packed, N, K, gs, f32s, d_out, M, d_x, stream, route, route_len);
 }
 
 }  // namespace q4gsw

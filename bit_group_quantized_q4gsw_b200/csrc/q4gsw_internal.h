@@ -5,9 +5,14 @@
 #include <atomic>
 #include <cstdint>
 #include <mutex>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 namespace q4gsw {
+
+// Token counts up to this run the tensor-core GEMV (weight streaming); above
+// it the tcgen05 GEMM.
+constexpr int kGemvMaxM = 16;
 
 // Route pins of the calling host thread (set by q4gsw_debug_pin_routes; 0
 // everywhere means the launchers choose).  Thread-local, like the route string.
@@ -41,6 +46,10 @@ int sm_count(int dev);
 // f32s: the blob holds fp32 scales (packed layout version 2) instead of fp16.
 cudaError_t launch_prepack(const uint8_t* codes, const void* scales, int N, int K, int gs, bool f32s, void* packed,
                            cudaStream_t stream, uint32_t* host_flag);
+// The gated block's blob: N = 2 F rows, gate row j and up row j as rows 2 j and 2 j + 1.
+cudaError_t launch_prepack_gated(const uint8_t* codes_gate, const void* scales_gate, const uint8_t* codes_up,
+                                 const void* scales_up, int F, int K, int gs, bool f32s, void* packed,
+                                 cudaStream_t stream, uint32_t* host_flag);
 cudaError_t launch_unpack(const void* packed, int N, int K, uint8_t* codes, cudaStream_t stream);
 cudaError_t launch_dequant(const void* packed, int N, int K, int gs, bool f32s, float* w32, uint16_t* w16,
                            cudaStream_t stream);
@@ -57,6 +66,22 @@ struct OutSplit {
 
 __host__ __device__ inline OutSplit single_output(float* y, int N) { return OutSplit{y, y, y, N, N, N}; }
 
+// fp16 outputs with an epilogue (q4gsw_epilogue.cuh) over N output columns:
+//   gated   v = (g, u) pairs (weight rows interleaved): y[m, j] = act(g_j) u_j,
+//           z[m, 2 j] = g_j, z[m, 2 j + 1] = u_j
+//   else    z[m, n] = v + bias[n],  y[m, n] = act(z) + res[m, n]
+// bias, res and z may be null; y may be res.
+enum ActKind { kActNone = 0, kActSilu = 1, kActGelu = 2 };
+struct Epi {
+  __half* y;
+  __half* z;
+  const __half* bias;
+  const __half* res;
+  int N;
+  int act;
+  int gated;
+};
+
 // The compute launchers take f32s = the packed blob has fp32 scales (layout
 // version 2) instead of fp16 (version 1).
 // Tensor-core GEMV routes for small token counts.  `M` may exceed 16: token
@@ -65,6 +90,11 @@ cudaError_t launch_gemv_fwd(const void* packed, int N, int K, int gs, bool f32s,
                             OutSplit out, cudaStream_t stream, char* route, int route_len);
 cudaError_t launch_gemv_bwd(const void* packed, int N, int K, int gs, bool f32s, const uint16_t* d_out, int M,
                             float* d_x, cudaStream_t stream, char* route, int route_len);
+
+// The same products with fp16 outputs through an epilogue: any M >= 1, the
+// GEMV up to kGemvMaxM tokens, the GEMMs above.
+cudaError_t launch_product_epi(bool bwd, const void* packed, int N, int K, int gs, bool f32s, const uint16_t* act,
+                               int M, const Epi& out, cudaStream_t stream, char* route, int route_len);
 
 // Forward GEMV that streams the packed weight through a TMA ring (M <= 16
 // per z-slice).
@@ -109,6 +139,33 @@ size_t dq8ca_zero_offset(int M, int K);
 cudaError_t launch_dq8ca_quantize(const uint16_t* x, int M, int K, void* workspace, cudaStream_t stream);
 cudaError_t launch_dq8ca_gemv(const void* packed, int N, int K, int gs, int M, const void* workspace, OutSplit out,
                               cudaStream_t stream, char* route, int route_len);
+
+// Gradients through the activations (q4gsw_layer.cu): d_gu from gu and d_h
+// (fp16, [M][2 F] and [M][F]); d_z = d_y act'(z) and its column sums (fp16
+// [M][N]; z and d_z null without an activation, d_bias may be null).
+cudaError_t launch_gated_grad(const __half* gu, const __half* d_h, int M, int F, int act, __half* d_gu,
+                              cudaStream_t stream);
+cudaError_t launch_act_grad(const __half* z, const __half* d_y, int M, int N, int act, __half* d_z, float* d_bias,
+                            cudaStream_t stream);
+
+// Distillation loss, log-sum-exp and gradient (q4gsw_distill.cuh).
+struct DistillArgs {
+  const void* logits;
+  const int32_t* indices;
+  const void* teacher;
+  const float* d_loss;    // null: no gradient
+  const float* lse_in;    // backward only: the forward's log-sum-exp
+  float* loss;
+  float* lse;
+  __half* grad;
+  int M, V, k;
+  int half_teacher;
+  float temperature;
+};
+cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
+                                int route_len);
+cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
+                               int route_len);
 
 // Embedding rows out[t] = dequant(W)[indices[t]] (fp32); an index outside
 // [0, N) gives a zero row and sets kIndexErrorBit in the device error word.

@@ -18,7 +18,11 @@ namespace pk {
 // One thread per 16-byte output chunk of the codes region: pair p, 64-byte
 // block b, quarter t of the block.  The chunk holds word slots 4t .. 4t+3, i.e.
 // columns 64b + 16 i + 4 t + e for i, e in 0..3.
-__global__ void q4gsw_prepack_codes_kernel(const uint8_t* __restrict__ codes, uint8_t* __restrict__ packed,
+// Pair p's even and odd rows start at even_rows + p row_stride and odd_rows +
+// p row_stride (one matrix: its rows 2p and 2p + 1; the gated block: row p of
+// the gate and of the up projection).
+__global__ void q4gsw_prepack_codes_kernel(const uint8_t* __restrict__ even_rows, const uint8_t* __restrict__ odd_rows,
+                                     size_t row_stride, uint8_t* __restrict__ packed,
                                      int N, int K, uint32_t* __restrict__ range_flag) {
   const int blocks_per_row = K / 64;
   const long long chunks = (long long)(N / 2) * blocks_per_row * 4;
@@ -29,8 +33,8 @@ __global__ void q4gsw_prepack_codes_kernel(const uint8_t* __restrict__ codes, ui
     const long long pb = c >> 2;
     const int b = int(pb % blocks_per_row);
     const int p = int(pb / blocks_per_row);
-    const uint8_t* even = codes + (size_t)(2 * p) * K + 64 * b + 4 * t;
-    const uint8_t* odd = even + K;
+    const uint8_t* even = even_rows + (size_t)p * row_stride + 64 * b + 4 * t;
+    const uint8_t* odd = odd_rows + (size_t)p * row_stride + 64 * b + 4 * t;
     uint32_t out[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -53,7 +57,7 @@ __global__ void q4gsw_prepack_tail_kernel(const void* __restrict__ scales, uint8
   const Layout L = layout_of(N, K, gs, sbytes);
   const size_t tid = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
   const size_t stride = (size_t)gridDim.x * blockDim.x;
-  const size_t n16 = L.scales_bytes / 16;  // N % 8 == 0 -> a whole number of 16-byte vectors
+  const size_t n16 = scales ? L.scales_bytes / 16 : 0;   // null: written by q4gsw_interleave_scales_kernel  // N % 8 == 0 -> a whole number of 16-byte vectors
   const uint4* src = reinterpret_cast<const uint4*>(scales);
   uint4* dst = reinterpret_cast<uint4*>(packed + L.scales_offset);
   for (size_t i = tid; i < n16; i += stride) dst[i] = src[i];
@@ -66,6 +70,19 @@ __global__ void q4gsw_prepack_tail_kernel(const void* __restrict__ scales, uint8
     tr[2] = uint32_t(N);
     tr[3] = uint32_t(K);
     tr[4] = uint32_t(gs);
+  }
+}
+
+// Scales of the gated block: [G][F] of the gate and of the up projection ->
+// [G][2 F], column 2 j from the gate and 2 j + 1 from the up projection (one
+// thread per pair; S = uint16_t or uint32_t).
+template <typename S>
+__global__ void q4gsw_interleave_scales_kernel(const S* __restrict__ gate, const S* __restrict__ up,
+                                               S* __restrict__ out, size_t pairs) {
+  const size_t stride = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < pairs; i += stride) {
+    out[2 * i] = gate[i];
+    out[2 * i + 1] = up[i];
   }
 }
 
@@ -160,8 +177,9 @@ static int grid_for(long long work, int threads) {
   return int(g);
 }
 
-cudaError_t launch_prepack(const uint8_t* codes, const void* scales, int N, int K, int gs, bool f32s, void* packed,
-                           cudaStream_t stream, uint32_t* host_flag) {
+static cudaError_t prepack_rows(const uint8_t* even_rows, const uint8_t* odd_rows, size_t row_stride,
+                                const void* scales, const void* scales_gate, const void* scales_up, int N, int K,
+                                int gs, bool f32s, void* packed, cudaStream_t stream, uint32_t* host_flag) {
   const int sbytes = f32s ? 4 : 2;
   const Layout L = layout_of(N, K, gs, sbytes);
   uint8_t* out = static_cast<uint8_t*>(packed);
@@ -169,14 +187,39 @@ cudaError_t launch_prepack(const uint8_t* codes, const void* scales, int N, int 
   cudaError_t err = cudaMemsetAsync(out + L.trailer_offset, 0, kTrailerBytes, stream);
   if (err != cudaSuccess) return err;
   const long long chunks = (long long)(N / 2) * (K / 64) * 4;
-  pk::q4gsw_prepack_codes_kernel<<<grid_for(chunks, 256), 256, 0, stream>>>(codes, out, N, K, flag);
+  pk::q4gsw_prepack_codes_kernel<<<grid_for(chunks, 256), 256, 0, stream>>>(even_rows, odd_rows, row_stride, out, N, K,
+                                                                            flag);
   pk::q4gsw_prepack_tail_kernel<<<grid_for((long long)(L.scales_bytes / 16) + 256, 256), 256, 0, stream>>>(
       scales, out, N, K, gs, sbytes);
+  if (!scales) {
+    const size_t pairs = (size_t)(K / gs) * (size_t)(N / 2);
+    if (f32s)
+      pk::q4gsw_interleave_scales_kernel<uint32_t><<<grid_for((long long)pairs, 256), 256, 0, stream>>>(
+          static_cast<const uint32_t*>(scales_gate), static_cast<const uint32_t*>(scales_up),
+          reinterpret_cast<uint32_t*>(out + L.scales_offset), pairs);
+    else
+      pk::q4gsw_interleave_scales_kernel<uint16_t><<<grid_for((long long)pairs, 256), 256, 0, stream>>>(
+          static_cast<const uint16_t*>(scales_gate), static_cast<const uint16_t*>(scales_up),
+          reinterpret_cast<uint16_t*>(out + L.scales_offset), pairs);
+  }
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   err = cudaMemcpyAsync(host_flag, flag, sizeof(uint32_t), cudaMemcpyDeviceToHost, stream);
   if (err != cudaSuccess) return err;
   return cudaStreamSynchronize(stream);
+}
+
+cudaError_t launch_prepack(const uint8_t* codes, const void* scales, int N, int K, int gs, bool f32s, void* packed,
+                           cudaStream_t stream, uint32_t* host_flag) {
+  return prepack_rows(codes, codes + K, 2 * (size_t)K, scales, nullptr, nullptr, N, K, gs, f32s, packed, stream,
+                      host_flag);
+}
+
+cudaError_t launch_prepack_gated(const uint8_t* codes_gate, const void* scales_gate, const uint8_t* codes_up,
+                                 const void* scales_up, int F, int K, int gs, bool f32s, void* packed,
+                                 cudaStream_t stream, uint32_t* host_flag) {
+  return prepack_rows(codes_gate, codes_up, (size_t)K, nullptr, scales_gate, scales_up, 2 * F, K, gs, f32s, packed,
+                      stream, host_flag);
 }
 
 cudaError_t launch_unpack(const void* packed, int N, int K, uint8_t* codes, cudaStream_t stream) {

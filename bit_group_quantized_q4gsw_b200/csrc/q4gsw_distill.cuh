@@ -9,14 +9,25 @@
 //
 // The rows are long (V tokens) and each logit is used for one exponential or
 // two, so the kernels are streams: what they cost is the bytes of the logits
-// and of the gradient.  A cluster of C CTAs shares a row.  Each thread issues
-// the 16-byte loads of 32 logits at once, the CTA's (max, sum of exp) pairs are
-// combined through shuffles and shared memory, and the C pairs of a row through
-// distributed shared memory, in rank order.  Where a CTA's slice of the row
-// fits its registers (V <= 8 x 8192), the gradient is computed from the
-// registers that the sum was computed from: the logits cross the memory system
-// once.  Longer rows are read a second time, shortly after the first, from L2.
-//
+// and of the gradient, provided enough of them are always in flight and little
+// is issued per logit.  Hence:
+//  - a CTA of 128 threads keeps 64 logits of its part of a row in each thread's
+//    registers from the sum to the gradient, so the logits cross the memory
+//    system once; a cluster of up to eight CTAs holds a row of 65536 tokens
+//    (longer rows are read a second time, shortly after the first, from L2);
+//  - the launch holds as many CTAs as fit the SMs (five each) and each walks its
+//    rows.  While a row is reduced and its gradient written, the next row's
+//    logits, teacher entries and scalars are already on their way (cp.async
+//    into shared memory, and registers that nothing touches before the next
+//    row);
+//  - the (max, sum of exp) pairs of a row's CTAs are exchanged by asynchronous
+//    stores into each other's shared memory that count on a barrier there (a
+//    cluster barrier would first wait for the gradient's stores), and added in
+//    a fixed order; the buffers alternate between two rows, so nothing waits to
+//    free them;
+//  - the teacher's softmax is spread over the threads, one entry each, while the
+//    row's logits arrive (in one warp, for all entries, it held up the row: 64
+//    entries 54 us instead of 45 for the gradient of 2048 x 32000).
 // The gradient is first written as coef p for every token; the k teacher
 // tokens are then written again as coef (p - q), in fp32 until the one
 // rounding.  Every CTA does that for the tokens of its own slice, after a
@@ -26,15 +37,15 @@
 namespace q4gsw {
 namespace distill {
 
-constexpr int kThreads = 256;
-constexpr int kPer = 32;                     // logits per thread and tile
-constexpr int kTile = kThreads * kPer;       // 8192 logits
-constexpr int kMaxK = 1024;                  // teacher entries per row
 constexpr int kMaxCluster = 8;
+constexpr int kThreads = 128, kWarps = 4;
+constexpr int kPer = 64;                     // logits per thread and tile
+constexpr int kTile = kThreads * kPer;       // 8192 logits
+constexpr int kPerSm = 5;                    // resident CTAs per SM
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-
-enum Mode { kResident = 0, kStream = 1, kGradOnly = 2 };
+constexpr float kHuge = 1e37f;   // |m c| beyond this: exponents from (x - m) c, which does not overflow to NaN
 
 __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error 2^-22
   float y;
@@ -42,15 +53,120 @@ __device__ __forceinline__ float ex2(float x) {   // 2^x, relative error 2^-22
   return y;
 }
 
-// (maximum, sum of 2^((x - maximum) c)) of a set of logits; an empty set (or
-// one of -infinity alone) is (-infinity, 0).
-struct MaxSum {
+// (maximum m, sum of the weights of x against m) of a set of logits; an empty
+// set (or one of -infinity alone) is (-infinity, 0).
+struct alignas(8) MaxSum {
   float m, s;
 };
-__device__ __forceinline__ float finite_ref(float m) { return m == -INFINITY ? 0.f : m; }
-__device__ __forceinline__ MaxSum combine(MaxSum a, MaxSum b, float c) {
-  const float m = fmaxf(a.m, b.m), r = finite_ref(m);
-  return {m, a.s * ex2((a.m - r) * c) + b.s * ex2((b.m - r) * c)};
+// Weight of x against a maximum m: 2^(x c - base), base = m c rounded.  The
+// exponent is one fused multiply-add, exact but for its own rounding, and what
+// rounding m c changed is the same factor for all of a row.  Where m c is near
+// the end of the fp32 range (a row masked with the type's lowest value) it is
+// (x - m) c; an m of -infinity stands for a base of 0.
+__device__ __forceinline__ bool is_huge(float m, float c) { return !(fabsf(m) * c < kHuge); }
+__device__ __forceinline__ float base_of(float m, float c) { return m == -INFINITY ? 0.f : m * c; }
+__device__ __forceinline__ float far_exponent(float x, float m, float c) {
+  return (x - (m == -INFINITY ? 0.f : m)) * c;
+}
+__device__ __forceinline__ float exponent_of(float x, float m, float c) {
+  return is_huge(m, c) ? far_exponent(x, m, c) : fmaf(x, c, -base_of(m, c));
+}
+// A sum against v.m, brought to a maximum m >= v.m.
+__device__ __forceinline__ float rebased(MaxSum v, float m, float c) {
+  const float e = is_huge(m, c) ? far_exponent(v.m, m, c) : v.m * c - base_of(m, c);
+  return v.s * ex2(e);
+}
+
+// The maximum over the lanes of a warp, in all of them (a NaN is passed over;
+// the sum of exponentials then carries it).
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+// Sums over groups of W lanes, the same bits in all of them (each step adds the same two values).
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// The pairs of W lanes (repeated over the warp) as one.
+template <int W>
+__device__ __forceinline__ MaxSum lanes_total(MaxSum v, float c) {
+  const float m = warp_max(v.m);
+  return {m, lanes_sum<W>(rebased(v, m, c))};
+}
+
+// Copies and stores under a predicate, at fixed offsets from one address: as
+// `if` statements each of them became a branch with its own address arithmetic,
+// together a third of the instructions of a row.
+template <int OFF>
+__device__ __forceinline__ void cp_async_16_if(bool p, uint32_t smem, const void* src) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+      "@p cp.async.cg.shared.global [%1 + %3], [%2 + %3], 16;\n\t}" ::"r"((int)p),
+      "r"(smem), "l"(src), "n"(OFF)
+      : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void st_v2_if(bool p, void* dst, uint32_t a, uint32_t b) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.v2.b32 [%1 + %4], {%2, %3};\n\t}" ::"r"(
+                   (int)p),
+               "l"(dst), "r"(a), "r"(b), "n"(OFF)
+               : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void st_v4_if(bool p, void* dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.v4.b32 [%1 + %6], {%2, %3, %4, %5};\n\t}" ::"r"(
+          (int)p),
+      "l"(dst), "r"(a), "r"(b), "r"(c), "r"(d), "n"(OFF)
+      : "memory");
+}
+// f(integral_constant<0>), f(integral_constant<1>), ...: a loop whose index is a constant
+template <typename F, int... I>
+__device__ __forceinline__ void unrolled(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+
+// A pair into another CTA's shared memory, counted (8 bytes) on a barrier there.
+__device__ __forceinline__ void st_async_pair(uint32_t dst, MaxSum v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(dst), "f"(v.m),
+               "f"(v.s), "r"(bar)
+               : "memory");
+}
+
+// Two fp32 operations in one instruction: the kernels are bound by what they
+// issue per logit.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ uint64_t ex2_2(uint64_t e) {
+  const float2 f = unpair(e);
+  return pair(ex2(f.x), ex2(f.y));
 }
 
 // One 16-byte vector of logits -> fp32 values.
@@ -77,257 +193,457 @@ __device__ __forceinline__ float logit_at(const void* row, int i) {
   return HALF ? __half2float(static_cast<const __half*>(row)[i]) : static_cast<const float*>(row)[i];
 }
 
-// grid = M * C CTAs, cluster = (C, 1, 1) (kGradOnly: no cluster).  CTA `rank`
-// of row m owns the 16-byte vectors [rank VV / C, (rank + 1) VV / C) of the row
-// (VV = V / E; kGradOnly: one tile of kTile logits).
-template <int MODE, bool HALF>
-__global__ void __launch_bounds__(kThreads, 4) q4gsw_distill_kernel(const DistillArgs a, int C) {
+// A teacher entry: token id (-1: padding, its logit then -infinity) and logit.
+struct Entry {
+  int id;
+  float t;
+};
+// As loaded: nothing waits for the loads before the entry is used, a row later.
+struct RawEntry {
+  int id;
+  uint32_t bits;
+};
+__device__ __forceinline__ RawEntry load_entry(const DistillArgs& a, int m, int j) {
+  const size_t at = (size_t)m * a.k + j;
+  RawEntry e;
+  e.id = a.indices[at];
+  if (a.half_teacher) e.bits = static_cast<const unsigned short*>(a.teacher)[at];
+  else e.bits = static_cast<const uint32_t*>(a.teacher)[at];
+  return e;
+}
+__device__ __forceinline__ Entry entry_of(const DistillArgs& a, const RawEntry& e) {
+  return {e.id, a.half_teacher ? __half2float(__ushort_as_half((unsigned short)e.bits)) : __uint_as_float(e.bits)};
+}
+
+// Rows (ROWS): grid = clusters of C CTAs (a power of two); cluster q takes rows
+// q, q + clusters, ...; CTA `rank` owns the vectors [rank VV / C, (rank + 1) VV
+// / C) of each (VV = V / E), in `tiles` tiles (1: they stay in registers).
+// Gradient alone (!ROWS): no clusters; CTA b takes items b, b + grid, ... of the
+// M x C tiles.  Dynamic shared memory: the next tile and two sets of k teacher
+// entries.
+template <bool ROWS, bool HALF>
+__global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const DistillArgs a, int C, int tiles) {
   constexpr int E = HALF ? 8 : 4;         // logits per vector
   constexpr int NV = kPer / E;            // vectors per thread and tile
-  __shared__ int s_idx[kMaxK];            // token id, -1: padding
-  __shared__ float s_q[kMaxK];            // teacher logit, then q
-  __shared__ MaxSum s_warp[kThreads / 32];
-  __shared__ MaxSum s_cta;
-  __shared__ float s_top, s_log_total;    // teacher: maximum; log of the sum of exponentials
-  __shared__ int s_has;
+  constexpr int TV = kTile / E;           // vectors per tile
+  extern __shared__ uint4 s_next[];       // [NV][kThreads]
+  __shared__ MaxSum s_warp[kWarps];       // the warps' pairs
+  __shared__ MaxSum s_row[2][kMaxCluster];   // the row's CTAs' pairs
+  __shared__ MaxSum s_teach[2][kWarps];   // of the warps with entries; (-infinity, 0) from the others
+  __shared__ float s_loss[kWarps];
+  __shared__ uint64_t s_bar[2];
+  __shared__ int s_abort;
+  const int k = a.k, V = a.V;
+  const int k4 = (k + 3) & ~3;                                         // ids in groups of four
+  int* s_id = reinterpret_cast<int*>(s_next + NV * kThreads);          // [2][k4], -1: padding
+  float* s_t = reinterpret_cast<float*>(s_id + 2 * k4);                // [2][k4]
 
   griddep_launch_dependents();
-  const int m = blockIdx.x / C, rank = blockIdx.x % C;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int V = a.V, k = a.k;
-  const float inv_t = 1.f / a.temperature, c = kLog2e / a.temperature;
+  const float inv_t = a.inv_t, c = a.inv_t * kLog2e;
   const int VV = V / E;
-  const int v_begin = MODE == kGradOnly ? rank * (kTile / E) : (int)((long long)rank * VV / C);
-  const int v_end = MODE == kGradOnly ? min(VV, v_begin + kTile / E) : (int)((long long)(rank + 1) * VV / C);
-  const char* row = static_cast<const char*>(a.logits) + (size_t)m * V * (HALF ? 2 : 4);
-  const uint4* rowv = reinterpret_cast<const uint4*>(row);
-  const bool want_grad = MODE == kGradOnly || a.grad != nullptr;
-  griddep_wait();
+  const bool want_grad = !ROWS || a.grad != nullptr;
+  const int c_log = __ffs(C) - 1;
+  const int rank = ROWS ? blockIdx.x & (C - 1) : 0;
+  const int first = ROWS ? blockIdx.x >> c_log : blockIdx.x, step = ROWS ? gridDim.x >> c_log : gridDim.x;
+  const int items = ROWS ? a.M : a.M * C;   // rows, or tiles of rows
+  // loads per item: the slice's tiles, and again for the gradient of a slice longer than one
+  const int loads = ROWS ? (tiles > 1 && want_grad ? 2 * tiles : tiles) : 1;
+  const bool entry_warp = 32 * warp < k;   // a warp whose threads have teacher entries
 
+  // Vectors [begin, end) of load `l` of item `it` (a slice's tile).
+  struct Span {
+    int m, begin, end;
+  };
+  const int v_begin = ROWS ? (int)(((long long)rank * VV) >> c_log) : 0;
+  const int v_end = ROWS ? (int)(((long long)(rank + 1) * VV) >> c_log) : 0;
+  auto slice_of = [&](int it) -> Span {
+    if (ROWS) return {it, v_begin, v_end};
+    const int m = it / C, t = it - m * C;
+    return {m, t * TV, min(VV, (t + 1) * TV)};
+  };
+  auto span_of = [&](int it, int l) -> Span {
+    Span s = slice_of(it);
+    if (ROWS && tiles > 1) {
+      s.begin += (l < tiles ? l : l - tiles) * TV;
+      s.end = min(s.end, s.begin + TV);
+    }
+    return s;
+  };
+  auto row_of = [&](int m) { return static_cast<const char*>(a.logits) + (size_t)m * V * (HALF ? 2 : 4); };
   // logits past the end of the slice: -infinity, which adds nothing
   const uint4 fill = HALF ? make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u)
                           : make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
-  auto load_tile = [&](int base, uint4 (&x)[NV]) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = base + i * kThreads + threadIdx.x;
-      x[i] = at < v_end ? ldg_stream_v4(rowv + at) : fill;
+  // Each thread copies, and later reads, its own vectors: no barrier.  They
+  // are issued after the tile before has been consumed from registers.  Slots
+  // past the end of a slice are filled once where all slices are alike.
+  uint4* const slots = s_next + threadIdx.x;
+  const uint32_t slots_addr = sm100::smem_u32(slots);
+  auto issue = [&](const Span& s) {
+    const uint4* src = reinterpret_cast<const uint4*>(row_of(s.m)) + s.begin + threadIdx.x;
+    const int n = s.end - s.begin - (int)threadIdx.x;
+    unrolled(
+        [&](auto index) {
+          constexpr int i = decltype(index)::value;
+          cp_async_16_if<i * kThreads * 16>(i * kThreads < n, slots_addr, src);
+        },
+        std::make_integer_sequence<int, NV>{});
+    cp_async_commit();
+    if (!ROWS || tiles > 1) {
+#pragma unroll 1
+      for (int i = NV - 1; i >= 0 && i * kThreads >= n; --i) slots[i * kThreads] = fill;
     }
   };
-  uint4 x[NV];
-  if (MODE != kStream) load_tile(v_begin, x);
+  auto take = [&](uint4 (&x)[NV]) {
+    cp_async_wait<0>();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = lds128_u32addr(slots_addr + i * kThreads * 16);
+  };
 
-  // ---- teacher softmax (warp 0), while the logits are on their way
-  if (warp == 0) {
-    const int32_t* idx = a.indices + (size_t)m * k;
-    const size_t t0 = (size_t)m * k;
-    float top = -INFINITY;
-    bool some = false, bad = false;
-    for (int j = lane; j < k; j += 32) {
-      int id = idx[j];
-      float t = a.half_teacher ? __half2float(static_cast<const __half*>(a.teacher)[t0 + j])
-                               : static_cast<const float*>(a.teacher)[t0 + j];
-      if (id < 0 || id >= V) {
-        bad |= id != -1;
-        id = -1;
-        t = -INFINITY;
-      }
-      s_idx[j] = id;
-      s_q[j] = t;
-      some |= t != -INFINITY;
-      top = fmaxf(top, t);
-    }
-    some = __any_sync(0xffffffffu, some);
-    if (__any_sync(0xffffffffu, bad) && lane == 0 && rank == 0) atomicOr(&g_device_error, kIndexErrorBit);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float total = 0.f;
-    for (int j = lane; j < k; j += 32) total += ex2((s_q[j] - top) * c);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) {
-      s_has = some;
-      s_top = top;
-      s_log_total = logf(total);
-    }
-    // the teacher's logits stay for the loss (rank 0); q is ex2((t - top) c) / total
-    s_cta.s = total;
-    __syncwarp();
+  if (ROWS && tiles == 1) {
+#pragma unroll 1
+    for (int i = 0; i < NV; ++i)
+      if (i * kThreads + (int)threadIdx.x >= v_end - v_begin) slots[i * kThreads] = fill;
   }
+  if (threadIdx.x < 2 * kWarps) s_teach[threadIdx.x / kWarps][threadIdx.x % kWarps] = {-INFINITY, 0.f};
+  if (threadIdx.x < kWarps) s_loss[threadIdx.x] = 0.f;
   __syncthreads();
-  const bool has = s_has != 0;
-  const float top = s_top, inv_total = 1.f / s_cta.s;
-  const float coef = want_grad ? a.d_loss[m] * a.temperature : 0.f;
-  __syncthreads();   // s_cta is written again below
-
-  // ---- (max, sum of exponentials) of the row
-  float ref = 0.f, scale = 0.f;   // p_i = 2^((z_i - ref) c) scale
-  if (MODE == kGradOnly) {
-    ref = a.lse_in[m] * a.temperature;   // z_i / T - lse = (z_i - lse T) / T
-    scale = 1.f;
-  } else {
-    MaxSum mine{-INFINITY, 0.f};
-    auto add_tile = [&](const uint4 (&t)[NV]) {
-      float top_t = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float f[E];
-        unpack<HALF>(t[i], f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) top_t = fmaxf(top_t, f[e]);
-      }
-      const float mx = fmaxf(mine.m, top_t), r = finite_ref(mx);
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float f[E];
-        unpack<HALF>(t[i], f);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          s0 += ex2((f[e] - r) * c);
-          s1 += ex2((f[e + 1] - r) * c);
-        }
-      }
-      mine = {mx, mine.s * ex2((mine.m - r) * c) + (s0 + s1)};
-    };
-    if (MODE == kResident) {
-      add_tile(x);
-    } else {
-      for (int base = v_begin; base < v_end; base += kTile / E) {
-        load_tile(base, x);
-        add_tile(x);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      mine = combine(mine, {__shfl_xor_sync(0xffffffffu, mine.m, o), __shfl_xor_sync(0xffffffffu, mine.s, o)}, c);
-    if (lane == 0) s_warp[warp] = mine;
-    __syncthreads();
+  if (ROWS && C > 1) {
     if (threadIdx.x == 0) {
-      MaxSum t = s_warp[0];
-      for (int w = 1; w < kThreads / 32; ++w) t = combine(t, s_warp[w], c);
-      s_cta = t;
+      sm100::mbar_init(&s_bar[0], 1);
+      sm100::mbar_init(&s_bar[1], 1);
+      s_abort = 0;
+      sm100::fence_mbar_init();
     }
-    cg::cluster_group cluster = cg::this_cluster();
-    if (C > 1) cluster.sync();
-    else __syncthreads();
-    MaxSum all{-INFINITY, 0.f};
-    for (int q = 0; q < C; ++q) all = combine(all, C > 1 ? *cluster.map_shared_rank(&s_cta, q) : s_cta, c);
-    if (C > 1) cluster.sync();   // no CTA leaves while another reads its pair
-    ref = all.m;
-    scale = 1.f / all.s;
-    if (rank == 0 && warp == 0) {
-      // (all.m - all.m) is 0, or NaN where the row's maximum is not finite
-      const float lse = fmaf(all.m, inv_t, logf(all.s)) + (all.m - all.m);
-      float part = 0.f;
-      if (has) {
-        for (int j = lane; j < k; j += 32) {
-          const float lt = (s_q[j] - top) * inv_t - s_log_total;   // log q_j
-          const float q = ex2((s_q[j] - top) * c) * inv_total;
-          // a weight of zero adds nothing, whatever its token's logit (a NaN
-          // weight, from a NaN of the teacher, is added)
-          if (s_idx[j] >= 0 && !(q == 0.f)) part += q * (lt - logit_at<HALF>(row, s_idx[j]) * inv_t + lse);
+  }
+
+  griddep_wait();
+  RawEntry ahead{-1, 0u};      // entry threadIdx.x of the next item
+  float d_loss_ahead = 0.f, lse_ahead = 0.f;
+  auto fetch = [&](int m) {
+    if ((int)threadIdx.x < k) ahead = load_entry(a, m, threadIdx.x);
+    if (want_grad) d_loss_ahead = a.d_loss[m];
+    if (!ROWS) lse_ahead = a.lse_in[m];
+  };
+  if (first < items) {
+    const Span s = span_of(first, 0);
+    issue(s);
+    fetch(s.m);
+  }
+  if (ROWS && C > 1) sm100::cluster_barrier();   // every CTA's barriers are set up
+
+  int turn = 0;   // items done
+  for (int it = first; it < items; it += step, ++turn) {
+    const int par = turn & 1;
+    const Span slice = slice_of(it);
+    const int m = slice.m;
+    const char* row = row_of(m);
+    const float coef = d_loss_ahead * a.temperature, lse_saved = lse_ahead;
+    int* ids = s_id + par * k4;
+    float* ts = s_t + par * k4;
+
+    // ---- teacher entries -> shared memory; the (max, sum) of the warp's
+    bool some = false;            // an entry with a weight (a NaN counts as one)
+    float z_own = 0.f;            // the student's logit at entry threadIdx.x, where this CTA needs it
+    if (entry_warp) {
+      float t_max = -INFINITY, t_sum = 0.f;
+      for (int j = threadIdx.x; j < k4; j += kThreads) {
+        Entry e{-1, -INFINITY};
+        if (j < k) e = entry_of(a, j == (int)threadIdx.x ? ahead : load_entry(a, m, j));
+        if (e.id < 0 || e.id >= V) {
+          if (e.id != -1 && rank == 0) atomicOr(&g_device_error, kIndexErrorBit);
+          e = {-1, -INFINITY};
+        }
+        ids[j] = e.id;
+        ts[j] = e.t;
+        some |= !(e.t == -INFINITY);
+        if (j == (int)threadIdx.x && e.id >= 0 &&
+            ((ROWS && rank == 0) || (e.id >= slice.begin * E && e.id < slice.end * E)))
+          z_own = logit_at<HALF>(row, e.id);
+        t_max = fmaxf(t_max, e.t);
+      }
+      t_max = warp_max(t_max);
+      for (int j = threadIdx.x; j < k4; j += kThreads) t_sum += ex2(exponent_of(ts[j], t_max, c));   // its own entries
+      t_sum = lanes_sum<32>(t_sum);
+      if (lane == 0) s_teach[par][warp] = {t_max, t_sum};
+    }
+
+    // ---- (max, sum of exponentials) of the slice; run_m is the same in a warp
+    uint4 x[NV];
+    float run_m = -INFINITY, run_s = 0.f;
+    if (ROWS) {
+      for (int l = 0; l < tiles; ++l) {
+        take(x);
+        float top_t = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float f[E];
+          unpack<HALF>(x[i], f);
+#pragma unroll
+          for (int e = 0; e < E; ++e) top_t = fmaxf(top_t, f[e]);
+        }
+        // every vector is in registers (the maximum depends on it): its slots take the next load
+        const float mx = fmaxf(run_m, warp_max(top_t)), base = base_of(mx, c);
+        if (l + 1 < loads) issue(span_of(it, l + 1));
+        else if (loads == 1 && it + step < items) issue(span_of(it + step, 0));
+        uint64_t sum[2] = {pair(rebased({run_m, run_s}, mx, c), 0.f), 0ull};
+        const uint64_t c2 = pair(c, c), minus_base = pair(-base, -base);
+        auto add = [&](auto weights) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            float f[E];
+            unpack<HALF>(x[i], f);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], weights(f[e], f[e + 1]));
+          }
+        };
+        if (!is_huge(mx, c)) add([&](float z0, float z1) { return ex2_2(fma2(pair(z0, z1), c2, minus_base)); });
+        else add([&](float z0, float z1) { return ex2_2(pair(far_exponent(z0, mx, c), far_exponent(z1, mx, c))); });
+        const float2 total = unpair(add2(sum[0], sum[1]));
+        run_m = mx;
+        run_s = total.x + total.y;
+      }
+      run_s = lanes_sum<32>(run_s);
+      if (lane == 0) s_warp[warp] = {run_m, run_s};
+    } else {
+      take(x);
+      if (it + step < items) issue(span_of(it + step, 0));
+    }
+    if (it + step < items) fetch(slice_of(it + step).m);
+    const bool has = __syncthreads_or(some);
+
+    // ---- the row's pair: every CTA's to every CTA of the cluster
+    MaxSum mine{0.f, 0.f};
+    if (ROWS) {
+      mine = lanes_total<kWarps>(s_warp[lane % kWarps], c);
+      if (C > 1 && warp == kWarps - 1) {
+        if (lane == 0) sm100::mbar_arrive_expect_tx(&s_bar[par], (uint32_t)sizeof(MaxSum) * C);
+        __syncwarp();
+        if (lane < C)
+          st_async_pair(sm100::mapa_u32(sm100::smem_u32(&s_row[par][rank]), lane), mine,
+                        sm100::mapa_u32(sm100::smem_u32(&s_bar[par]), lane));
+      }
+    }
+    MaxSum teach{0.f, 0.f};   // in the warps with entries
+    float inv_total = 0.f;    // q_j = 2^exponent_of(t_j, teach.m) / teach.s
+    if (entry_warp) {
+      teach = lanes_total<kWarps>(s_teach[par][lane % kWarps], c);
+      inv_total = 1.f / teach.s;
+    }
+    float ref, base, scale;   // p_i = 2^(z_i c - base) scale, base for ref
+    if (ROWS) {
+      if (C > 1) {
+        if (!sm100::mbar_wait(&s_bar[par], (turn >> 1) & 1, &s_abort, &g_device_error, 0x400u)) break;
+        mine = lane % kMaxCluster < C ? s_row[par][lane % kMaxCluster] : MaxSum{-INFINITY, 0.f};
+        mine = lanes_total<kMaxCluster>(mine, c);
+      }
+      ref = mine.m;
+      base = base_of(ref, c);
+      scale = 1.f / mine.s;
+      if (rank == 0 && entry_warp) {
+        // log of the sum against the maximum itself (its base was rounded); (ref -
+        // ref) is 0, or NaN where the row's maximum is not finite
+        auto log_of = [&](const MaxSum& v) {
+          return logf(v.s) - (is_huge(v.m, c) ? 0.f : fmaf(v.m, c, -base_of(v.m, c)) * kLn2);
+        };
+        const float lse = fmaf(ref, inv_t, log_of(mine)) + (ref - ref);
+        float part = 0.f;
+        if (has) {
+          const float log_total = log_of(teach);
+          for (int j = threadIdx.x; j < k; j += kThreads) {
+            const Entry e{ids[j], ts[j]};
+            const float q = ex2(exponent_of(e.t, teach.m, c)) * inv_total;
+            // a weight of zero adds nothing, whatever its token's logit (a NaN weight is added)
+            if (e.id >= 0 && !(q == 0.f)) {
+              const float z = j == (int)threadIdx.x ? z_own : logit_at<HALF>(row, e.id);
+              part += q * ((e.t - teach.m) * inv_t - log_total - z * inv_t + lse);
+            }
+          }
+        }
+        part = lanes_sum<32>(part);
+        if (lane == 0) s_loss[warp] = part;
+        if (threadIdx.x == 0) a.lse[m] = lse;
+      }
+    } else {
+      ref = lse_saved * a.temperature;   // z / T - lse = (z - lse T) / T
+      base = lse_saved * kLog2e;
+      scale = 1.f;
+    }
+
+    // ---- gradient: coef p for every token of the slice, then the teacher's tokens again
+    __half* grow = a.grad + (size_t)m * V;
+    if (want_grad) {
+      const float by = coef * scale;
+      const uint64_t c2 = pair(c, c), minus_base = pair(-base, -base), by2 = pair(by, by);
+      for (int l = 0; l < (ROWS ? tiles : 1); ++l) {
+        const Span s = span_of(it, l);
+        if (ROWS && tiles > 1) take(x);
+        __half* dst = grow + ((size_t)s.begin + threadIdx.x) * E;
+        const int n = s.end - s.begin - (int)threadIdx.x;
+        auto store = [&](auto values) {
+          unrolled(
+              [&](auto index) {
+                constexpr int i = decltype(index)::value;
+                float f[E];
+                unpack<HALF>(x[i], f);
+                uint32_t h[E / 2];
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                  const float2 g = unpair(values(f[e], f[e + 1]));
+                  h[e / 2] = h2_as_u32(__floats2half2_rn(g.x, g.y));
+                }
+                constexpr int kOff = i * kThreads * E * 2;
+                if constexpr (HALF) st_v4_if<kOff>(i * kThreads < n, dst, h[0], h[1], h[2], h[3]);
+                else st_v2_if<kOff>(i * kThreads < n, dst, h[0], h[1]);
+              },
+              std::make_integer_sequence<int, NV>{});
+        };
+        if (!has) store([&](float, float) { return 0ull; });
+        else if (!is_huge(ref, c))
+          store([&](float z0, float z1) { return mul2(ex2_2(fma2(pair(z0, z1), c2, minus_base)), by2); });
+        else
+          store([&](float z0, float z1) {
+            return mul2(ex2_2(pair(far_exponent(z0, ref, c), far_exponent(z1, ref, c))), by2);
+          });
+        if (ROWS && tiles > 1) {
+          if (l + 1 < tiles) issue(span_of(it, tiles + l + 1));
+          else if (it + step < items) issue(span_of(it + step, 0));
         }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-      if (lane == 0) {
-        a.lse[m] = lse;
-        a.loss[m] = part * a.temperature * a.temperature;
+    } else if (tiles > 1 && it + step < items) {
+      issue(span_of(it + step, 0));
+    }
+    __syncthreads();
+    if (ROWS && rank == 0 && threadIdx.x == 0) {
+      float sum = 0.f;
+      for (int w = 0; w < kWarps; ++w) sum += s_loss[w];   // 0 from the warps without entries
+      a.loss[m] = sum * a.temperature * a.temperature;
+    }
+    if (want_grad && has && entry_warp) {
+      for (int j = threadIdx.x; j < k; j += kThreads) {
+        const int id = ids[j];
+        if (id < slice.begin * E || id >= slice.end * E) continue;   // padding, or another CTA's token
+        int same = 0;
+        for (int i = 0; i < k4; i += 4) {
+          const int4 o = *reinterpret_cast<const int4*>(ids + i);
+          same += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
+        }
+        float t = ex2(exponent_of(ts[j], teach.m, c));
+        if (same > 1) {   // every entry of this token, in the order of the list: each of them writes the same value
+          t = 0.f;
+          for (int i = 0; i < k; ++i)
+            if (ids[i] == id) t += ex2(exponent_of(ts[i], teach.m, c));
+        }
+        const float z = j == (int)threadIdx.x ? z_own : logit_at<HALF>(row, id);
+        const float p = ex2(is_huge(ref, c) ? far_exponent(z, ref, c) : fmaf(z, c, -base)) * scale;
+        grow[id] = __float2half_rn(coef * (p - t * inv_total));
       }
     }
   }
-  if (!want_grad) return;
-
-  // ---- gradient: coef p for every token of the slice, then the teacher's tokens again
-  __half* grow = a.grad + (size_t)m * V;
-  auto store_tile = [&](int base, const uint4 (&t)[NV]) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = base + i * kThreads + threadIdx.x;
-      if (at >= v_end) continue;
-      float f[E];
-      unpack<HALF>(t[i], f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = has ? coef * (ex2((f[e] - ref) * c) * scale) : 0.f;
-      if constexpr (HALF) {
-        *reinterpret_cast<uint4*>(grow + (size_t)at * 8) =
-            make_uint4(h2_as_u32(__floats2half2_rn(f[0], f[1])), h2_as_u32(__floats2half2_rn(f[2], f[3])),
-                       h2_as_u32(__floats2half2_rn(f[4], f[5])), h2_as_u32(__floats2half2_rn(f[6], f[7])));
-      } else {
-        *reinterpret_cast<uint2*>(grow + (size_t)at * 4) =
-            make_uint2(h2_as_u32(__floats2half2_rn(f[0], f[1])), h2_as_u32(__floats2half2_rn(f[2], f[3])));
-      }
-    }
-  };
-  if (MODE != kStream) {
-    store_tile(v_begin, x);
-  } else {
-    for (int base = v_begin; base < v_end; base += kTile / E) {
-      load_tile(base, x);
-      store_tile(base, x);
-    }
-  }
-  __syncthreads();
-  if (!has) return;
-  for (int j = threadIdx.x; j < k; j += kThreads) {
-    const int id = s_idx[j];
-    if (id < v_begin * E || id >= v_end * E) continue;   // padding, or another CTA's token
-    float t = 0.f;   // every entry of this token, in the order of the list: each writes the same value
-    for (int i = 0; i < k; ++i)
-      if (s_idx[i] == id) t += ex2((s_q[i] - top) * c);
-    const float p = ex2((logit_at<HALF>(row, id) - ref) * c) * scale;
-    grow[id] = __float2half_rn(coef * (p - t * inv_total));
-  }
+  cp_async_wait<0>();   // nothing in flight when a wait ran out
 }
 
 }  // namespace distill
 
-template <int MODE, bool HALF>
-static cudaError_t distill_launch(const DistillArgs& a, int C, bool cluster, cudaStream_t stream) {
+// Launch configuration of clusters of C (ROWS) or single CTAs.
+struct DistillConfig {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.M * (unsigned)C, 1, 1);
-  cfg.blockDim = dim3(distill::kThreads, 1, 1);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, distill::q4gsw_distill_kernel<MODE, HALF>, a, C);
+  DistillConfig(unsigned grid, int C, bool rows, size_t smem, cudaStream_t stream) {
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(distill::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = rows ? 2 : 1;
+  }
+  DistillConfig(const DistillConfig&) = delete;
+};
+
+// One instance: whole rows, or tiles of the gradient; fp16 or fp32 logits.
+template <bool ROWS, bool HALF>
+struct DistillKernel {
+  static auto kernel() { return distill::q4gsw_distill_kernel<ROWS, HALF>; }
+
+  // bytes of the next tile and two sets of k teacher entries
+  static size_t smem(int k) { return (size_t)distill::kTile * (HALF ? 2 : 4) + (size_t)((k + 3) & ~3) * 16; }
+
+  static cudaError_t setup() {
+    static PerDeviceOnce attr_once;
+    return once_per_device(attr_once, current_device(), [] {
+      return cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(1024));
+    });
+  }
+
+  static cudaError_t launch(const DistillArgs& a, int C, int tiles, unsigned grid, cudaStream_t stream) {
+    const cudaError_t e = setup();
+    if (e != cudaSuccess) return e;
+    DistillConfig c(grid, C, ROWS, smem(a.k), stream);
+    return cudaLaunchKernelEx(&c.cfg, kernel(), a, C, tiles);
+  }
+
+  // Clusters of C CTAs the current device holds at once (asked once per device,
+  // for teacher lists of up to 256 entries and for longer ones).
+  static int clusters(int C, int k) {
+    static std::atomic<int> cached[kMaxDevices][2][distill::kMaxCluster + 1];
+    const int dev = current_device();
+    const int d = (dev >= 0 && dev < kMaxDevices) ? dev : 0, big = k > 256;
+    int n = cached[d][big][C].load(std::memory_order_relaxed);
+    if (n == 0) {
+      n = -1;
+      if (setup() == cudaSuccess) {
+        DistillConfig c((unsigned)C, C, true, smem(big ? 1024 : 256), nullptr);
+        if (cudaOccupancyMaxActiveClusters(&n, kernel(), &c.cfg) != cudaSuccess || n < 1) n = -1;
+      }
+      cached[d][big][C].store(n, std::memory_order_relaxed);
+    }
+    return n > 0 ? n : 1;
+  }
+};
+
+template <bool HALF>
+static cudaError_t distill_rows(const DistillArgs& a, cudaStream_t stream, char* route, int route_len) {
+  using namespace distill;
+  // CTAs per row: as many as hold it (at most a cluster of 8), and more, down to
+  // 2048 logits each, while the rows would leave SMs without work.
+  const int sms = sm_count(current_device());
+  int C = 1;
+  while (C < kMaxCluster && (long long)C * kTile < a.V) C *= 2;
+  while (C < kMaxCluster && (long long)a.M * C < sms && a.V / (2 * C) >= 2048) C *= 2;
+  const int E = HALF ? 8 : 4;
+  const int tiles = ((a.V / E + C - 1) / C * E + kTile - 1) / kTile;
+  // one wave of clusters (a cluster that had to wait for a slot would start its
+  // rows when the others end theirs)
+  const int most = DistillKernel<true, HALF>::clusters(C, a.k);
+  const unsigned n = (unsigned)(a.M < most ? a.M : most);
+  if (route)
+    snprintf(route, route_len, "distill_%s launches=1 cluster=%d clusters=%u tiles=%d", a.grad ? "step" : "fwd", C, n,
+             tiles);
+  return DistillKernel<true, HALF>::launch(a, C, tiles, n * C, stream);
 }
 
 cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
                                 int route_len) {
-  using namespace distill;
-  // CTAs per row: as many tiles as the row has (at most a cluster of 8), and
-  // more, down to a quarter of a tile each, while the launch would leave SMs
-  // without work.
-  int C = 1;
-  while (C < kMaxCluster && (long long)C * kTile < a.V) C *= 2;
-  const bool resident = (long long)C * kTile >= a.V;
-  const int sms = sm_count(current_device());
-  while (C < kMaxCluster && (long long)a.M * C < 2LL * sms && a.V / (2 * C) >= kTile / 4) C *= 2;
-  if (route)
-    snprintf(route, route_len, "distill_%s launches=1 cluster=%d %s", a.grad ? "step" : "fwd", C,
-             resident ? "resident" : "streamed");
-  if (resident)
-    return half_logits ? distill_launch<kResident, true>(a, C, true, stream)
-                       : distill_launch<kResident, false>(a, C, true, stream);
-  return half_logits ? distill_launch<kStream, true>(a, C, true, stream)
-                     : distill_launch<kStream, false>(a, C, true, stream);
+  return half_logits ? distill_rows<true>(a, stream, route, route_len)
+                     : distill_rows<false>(a, stream, route, route_len);
 }
 
 cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
                                int route_len) {
-  const int C = (a.V + distill::kTile - 1) / distill::kTile;
-  if (route) snprintf(route, route_len, "distill_bwd launches=1 tiles=%d", C);
-  return half_logits ? distill_launch<distill::kGradOnly, true>(a, C, false, stream)
-                     : distill_launch<distill::kGradOnly, false>(a, C, false, stream);
+  using namespace distill;
+  const int C = (a.V + kTile - 1) / kTile;
+  const long long items = (long long)a.M * C;
+  const int most = kPerSm * sm_count(current_device());
+  const unsigned grid = (unsigned)(items < most ? items : most);
+  if (route) snprintf(route, route_len, "distill_bwd launches=1 tiles=%d ctas=%u", C, grid);
+  return half_logits ? DistillKernel<false, true>::launch(a, C, 1, grid, stream)
+                     : DistillKernel<false, false>::launch(a, C, 1, grid, stream);
 }
 
 }  // namespace q4gsw

@@ -35,6 +35,7 @@
 #include <cstring>
 #include <cstdlib>
 #include <type_traits>
+#include <utility>
 
 #include "q4gsw_common.cuh"
 #include "q4gsw_epilogue.cuh"

@@ -161,6 +161,7 @@ struct DistillArgs {
   int M, V, k;
   int half_teacher;
   float temperature;
+  float inv_t;            // 1 / temperature
 };
 cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
                                 int route_len);

@@ -267,7 +267,7 @@ q4gsw_status q4gsw_distill_fwd(const void* logits, int half_logits, int M, int V
   return guarded([&] {
     return distill_impl(kFwd,
                         DistillArgs{logits, indices, teacher, nullptr, nullptr, loss, lse, nullptr, M, V, k,
-                                    half_teacher, temperature},
+                                    half_teacher, temperature, 1.f / temperature},
                         half_logits, stream);
   });
 }
@@ -278,7 +278,7 @@ q4gsw_status q4gsw_distill_bwd(const void* logits, int half_logits, int M, int V
   return guarded([&] {
     return distill_impl(kBwd,
                         DistillArgs{logits, indices, teacher, d_loss, lse, nullptr, nullptr, h(d_logits), M, V, k,
-                                    half_teacher, temperature},
+                                    half_teacher, temperature, 1.f / temperature},
                         half_logits, stream);
   });
 }
@@ -289,7 +289,7 @@ q4gsw_status q4gsw_distill_step(const void* logits, int half_logits, int M, int 
   return guarded([&] {
     return distill_impl(kStep,
                         DistillArgs{logits, indices, teacher, d_loss, nullptr, loss, lse, h(d_logits), M, V, k,
-                                    half_teacher, temperature},
+                                    half_teacher, temperature, 1.f / temperature},
                         half_logits, stream);
   });
 }

@@ -14,36 +14,38 @@ from .binding import _check, library
 
 ACTS = {"none": 0, "silu": 1, "gelu_tanh": 2}
 
+# the current stream's handle without building a Stream object (2 us of a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # None in a build without CUDA
+
 _f16, _f32, _i32, _u8 = torch.float16, torch.float32, torch.int32, torch.uint8
 
 
 def _need(t, name: str, dtype, shape, device):
     """Check one tensor and return its pointer."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    try:   # one test of everything: a call of a few microseconds spends as long on its arguments
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if t.device != device:
         raise ValueError(f"{name} must be on {device} (got {t.device})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _first(t, name: str, dtype, ndim: int):
     """Check the tensor that fixes the device; returns its device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims (got {t.dim()})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     return t.device
 
 
@@ -52,7 +54,7 @@ def _blob(packed, N: int, K: int, group_size: int, f32s: bool, device):
         raise TypeError("packed must be a uint8 tensor")
     if packed.device != device or not packed.is_contiguous():
         raise ValueError(f"packed must be contiguous and on {device}")
-    lib = library()
+    lib = _lib or _load()
     need = (lib.q4gsw_packed_bytes_f32s if f32s else lib.q4gsw_packed_bytes)(N, K, group_size)
     if packed.numel() < need:   # a shape that is not accepted needs 0: the call itself reports it
         raise ValueError(f"packed holds {packed.numel()} bytes, [{N}, {K}] at group size {group_size} needs {need}")
@@ -65,15 +67,26 @@ def _act(act: str, allowed=("none", "silu", "gelu_tanh")) -> int:
     return ACTS[act]
 
 
+_lib = None
+
+
+def _load():
+    global _lib
+    _lib = library()
+    return _lib
+
+
 def _call(name: str, device, *args):
     """Call the C function with the device's current stream appended."""
-    fn = getattr(library(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    fn = getattr(_lib or _load(), name)
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(name, st)
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _check(name, st)
 
 
 def q4gsw_prepack_gated(codes_gate, scales_gate, codes_up, scales_up, group_size: int, packed=None):
@@ -83,13 +96,13 @@ def q4gsw_prepack_gated(codes_gate, scales_gate, codes_up, scales_up, group_size
     F, K = codes_gate.shape
     f32s = isinstance(scales_gate, torch.Tensor) and scales_gate.dtype == _f32
     sdt = _f32 if f32s else _f16
-    lib = library()
+    lib = _lib or _load()
     nbytes = int((lib.q4gsw_packed_bytes_f32s if f32s else lib.q4gsw_packed_bytes)(2 * F, K, group_size))
     if packed is None:
         packed = torch.empty(max(nbytes, 1), dtype=_u8, device=dev)
     sshape = (K // group_size if group_size > 0 else 0, F)
-    _call("q4gsw_prepack_gated_f32s" if f32s else "q4gsw_prepack_gated", dev, codes_gate.data_ptr(),
-          _need(scales_gate, "scales_gate", sdt, sshape, dev), _need(codes_up, "codes_up", _u8, (F, K), dev),
+    _call("q4gsw_prepack_gated_f32s" if f32s else "q4gsw_prepack_gated", dev,
+          _need(codes_gate, "codes_gate", _u8, (F, K), dev), _need(scales_gate, "scales_gate", sdt, sshape, dev), _need(codes_up, "codes_up", _u8, (F, K), dev),
           _need(scales_up, "scales_up", sdt, sshape, dev), F, K, group_size,
           _need(packed, "packed", _u8, (packed.numel(),), dev), packed.numel())
     return packed
@@ -181,7 +194,7 @@ def _teacher(logits, indices, teacher):
         raise TypeError("teacher must be a float32 or float16 tensor")
     M, V = logits.shape
     k = indices.shape[1]
-    head = (logits.data_ptr(), int(logits.dtype == _f16), M, V)
+    head = (_need(logits, "logits", logits.dtype, (M, V), dev), int(logits.dtype == _f16), M, V)
     tail = (_need(indices, "indices", _i32, (M, k), dev), _need(teacher, "teacher", teacher.dtype, (M, k), dev),
             int(teacher.dtype == _f16), k)
     return dev, M, V, head, tail

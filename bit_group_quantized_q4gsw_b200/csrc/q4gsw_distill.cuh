@@ -13,7 +13,7 @@
 // is issued per logit.  Hence:
 //  - a CTA of 128 threads keeps 64 logits of its part of a row in each thread's
 //    registers from the sum to the gradient, so the logits cross the memory
-//    system once; a cluster of up to eight CTAs holds a row of 65536 tokens
+//    system once; a cluster of up to 16 CTAs holds a row of 131072 tokens
 //    (longer rows are read a second time, shortly after the first, from L2);
 //  - the launch holds as many CTAs as fit the SMs (five each) and each walks its
 //    rows.  While a row is reduced and its gradient written, the next row's
@@ -37,7 +37,7 @@
 namespace q4gsw {
 namespace distill {
 
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;             // past 8: allowed by an attribute of the kernel
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kPer = 64;                     // logits per thread and tile
 constexpr int kTile = kThreads * kPer;       // 8192 logits
@@ -577,7 +577,8 @@ struct DistillKernel {
   static cudaError_t setup() {
     static PerDeviceOnce attr_once;
     return once_per_device(attr_once, current_device(), [] {
-      return cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(1024));
+      const cudaError_t e = cudaFuncSetAttribute(kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem(1024));
+      return e != cudaSuccess ? e : cudaFuncSetAttribute(kernel(), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
   }
 
@@ -610,7 +611,7 @@ struct DistillKernel {
 template <bool HALF>
 static cudaError_t distill_rows(const DistillArgs& a, cudaStream_t stream, char* route, int route_len) {
   using namespace distill;
-  // CTAs per row: as many as hold it (at most a cluster of 8), and more, down to
+  // CTAs per row: as many as hold it (at most a cluster of 16), and more, down to
   // 2048 logits each, while the rows would leave SMs without work.
   const int sms = sm_count(current_device());
   int C = 1;

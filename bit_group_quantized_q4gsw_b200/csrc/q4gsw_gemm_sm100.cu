@@ -665,6 +665,22 @@ cudaError_t launch_gemm_bwd(const void* packed, int N, int K, int gs, bool f32s,
               : launch_gemm_ts_impl<true, false>(packed, N, K, gs, d_out, M, o, stream, route, route_len);
 }
 
+// Route of a product with an epilogue above the GEMV range.  Past 512 tokens, as
+// above.  Up to there both kernels run in whole waves, and a gated block's
+// twice as many output tiles can leave the tensor-memory kernel (128 x 256
+// tiles) a second, mostly empty wave where the shared-memory kernel (256 x 256)
+// fits one.  Time per wave, measured at 512 tokens and 512 .. 4096 input features
+// (us): 9 + 0.35 per stage, and 10 + 0.75 per stage; 512 x 16384 x 2048 takes 38.3
+// on the first and 34.4 on the second, 512 x 9472 x 2048 (148 tiles) 20.3 and 32.2.
+static bool epi_on_ss_route(int M, int rows, int contraction) {
+  if (route_pins().gemm != kGemmAuto || M > 512 || M <= 256) return use_ss_route(M);
+  const int sms = sm_count(current_device());
+  const double stages = (contraction + 63) / 64;
+  const int ts = (rows + 127) / 128 * 2, ss = (rows + 255) / 256 * 2;   // tiles: two of up to 256 tokens
+  if (ss <= sms / 2) return false;   // the contraction would be split: the tensor-memory kernel
+  return ceil((double)ss / sms) * (10 + 0.75 * stages) < ceil((double)ts / sms) * (9 + 0.35 * stages);
+}
+
 // The products with fp16 outputs through an epilogue (any M): the same routes.
 template <bool BWD, bool F32S>
 static cudaError_t product_epi(const void* packed, int N, int K, int gs, const uint16_t* act, int M, const Epi& out,
@@ -673,8 +689,9 @@ static cudaError_t product_epi(const void* packed, int N, int K, int gs, const u
     return BWD ? gemv_tma_bwd_impl(packed, N, K, gs, F32S, act, M, out, stream, route, route_len)
                : gemv_tma_fwd_impl(packed, N, K, gs, F32S, act, M, out, stream, route, route_len);
   }
-  return use_ss_route(M) ? launch_gemm_impl<BWD, F32S>(packed, N, K, gs, act, M, out, stream, route, route_len)
-                         : launch_gemm_ts_impl<BWD, F32S>(packed, N, K, gs, act, M, out, stream, route, route_len);
+  return epi_on_ss_route(M, BWD ? K : N, BWD ? N : K)
+             ? launch_gemm_impl<BWD, F32S>(packed, N, K, gs, act, M, out, stream, route, route_len)
+             : launch_gemm_ts_impl<BWD, F32S>(packed, N, K, gs, act, M, out, stream, route, route_len);
 }
 
 cudaError_t launch_product_epi(bool bwd, const void* packed, int N, int K, int gs, bool f32s, const uint16_t* act,

@@ -130,7 +130,11 @@ template <int S, typename Out>
 __device__ __forceinline__ void copy_out(const float* stage_f32, bool pushed, int slot_floats, int row_b, int row_e,
                                          int t0, int f0, const Args<Out>& args) {
   using namespace sm100;
-  constexpr int kPer = S == 1 ? 8 : (12 / S > 0 ? 12 / S : 1);   // at most 12 float4 in flight
+  // at most 12 float4 in flight (8 with an epilogue, whose operands take
+  // registers too: with 12 they spilled, and a 512-token gated forward of 16384
+  // rows took 44.3 us instead of 38.1)
+  constexpr int kMost = std::is_same_v<Out, Epi> ? 8 : 12;
+  constexpr int kPer = S == 1 ? (std::is_same_v<Out, Epi> ? 4 : 8) : (kMost / S > 0 ? kMost / S : 1);
   using Operand = decltype(epi_load4(args.out, size_t(0), 0));   // what the epilogue reads (nothing for fp32 rows)
   uint32_t src[S];   // rank qq's partial rows, in the cluster's shared window
 #pragma unroll
@@ -498,23 +502,23 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
     // One tensor store of the [bt][128] fp32 tile (rows past M and features
     // past the output clipped by the map), or the threads' copy-out.
     park();
-    bool stored = false;
+    bool by_tma = false;
     if constexpr (std::is_same_v<Out, OutSplit>) {
-      if (args.tma_out) {
-      const OutSplit& o = args.out;
-      const CUtensorMap* my = f0 < o.n1 ? &map_y0 : (f0 < o.n2 ? &map_y1 : &map_y2);
-      const int c0 = f0 < o.n1 ? f0 : (f0 < o.n2 ? f0 - o.n1 : f0 - o.n2);
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (threadIdx.x == 0 && !*abort_flag) {
-        tma_store_2d(my, stage_f32, c0, t0);
-        bulk_commit();
-        bulk_wait_read_all();
-      }
-      stored = true;
+      by_tma = args.tma_out != 0;
+      if (by_tma) {
+        const OutSplit& o = args.out;
+        const CUtensorMap* my = f0 < o.n1 ? &map_y0 : (f0 < o.n2 ? &map_y1 : &map_y2);
+        const int c0 = f0 < o.n1 ? f0 : (f0 < o.n2 ? f0 - o.n1 : f0 - o.n2);
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (threadIdx.x == 0 && !*abort_flag) {
+          tma_store_2d(my, stage_f32, c0, t0);
+          bulk_commit();
+          bulk_wait_read_all();
+        }
       }
     }
-    if (!stored) {
+    if (!by_tma) {
       __syncthreads();
       if (!*abort_flag) copy_out<1>(stage_f32, false, 0, 0, args.bt, t0, f0, args);
     }
@@ -653,25 +657,25 @@ static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs,
   CUtensorMap map_y[3];
   auto make_out_maps = [&](int bt) -> bool {
     if constexpr (!std::is_same_v<Out, OutSplit>) {
-      map_y[0] = map_y[1] = map_y[2] = map_act;   // never read: an epilogue is applied by the threads
+      map_y[0] = map_y[1] = map_y[2] = map_act;   // never read: the threads apply an epilogue
       return false;
     } else {
-    const int nb[3] = {0, out.n1, out.n2};
-    const int ne[3] = {out.n1, out.n2, out.N};
-    float* const yb[3] = {out.y0, out.y1, out.y2};
-    bool tma_out = (out.n1 % BW == 0 || out.n1 == out.N) && (out.n2 % BW == 0 || out.n2 == out.N);
-    for (int i = 0; i < 3 && tma_out; ++i) {
-      const int width = ne[i] - nb[i];
-      if (width <= 0) {
-        map_y[i] = map_y[0];
-        continue;
+      const int nb[3] = {0, out.n1, out.n2};
+      const int ne[3] = {out.n1, out.n2, out.N};
+      float* const yb[3] = {out.y0, out.y1, out.y2};
+      bool tma_out = (out.n1 % BW == 0 || out.n1 == out.N) && (out.n2 % BW == 0 || out.n2 == out.N);
+      for (int i = 0; i < 3 && tma_out; ++i) {
+        const int width = ne[i] - nb[i];
+        if (width <= 0) {
+          map_y[i] = map_y[0];
+          continue;
+        }
+        tma_out = (reinterpret_cast<uintptr_t>(yb[i]) % 16 == 0) &&
+                  make_map_2d(&map_y[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, yb[i], (uint64_t)width, M,
+                              (uint64_t)width * 4, BW, bt, CU_TENSOR_MAP_SWIZZLE_NONE);
       }
-      tma_out = (reinterpret_cast<uintptr_t>(yb[i]) % 16 == 0) &&
-                make_map_2d(&map_y[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, yb[i], (uint64_t)width, M,
-                            (uint64_t)width * 4, BW, bt, CU_TENSOR_MAP_SWIZZLE_NONE);
-    }
-    if (!tma_out) map_y[0] = map_y[1] = map_y[2] = map_act;   // never read
-    return tma_out;
+      if (!tma_out) map_y[0] = map_y[1] = map_y[2] = map_act;   // never read
+      return tma_out;
     }
   };
   a.tma_out = make_out_maps(a.bt) ? 1 : 0;

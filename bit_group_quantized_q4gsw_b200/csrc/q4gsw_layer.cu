@@ -21,6 +21,7 @@ namespace q4gsw {
 namespace layer {
 
 constexpr int kThreads = 256;
+constexpr int kRows = 4;   // rows a thread of the projection's gradient has in flight
 
 // One item = 8 gated features: 32 bytes of (g, u) pairs, 16 of d_h.  A thread
 // reads all of an item before it writes any of it, so d_gu may be gu.
@@ -69,36 +70,46 @@ __global__ void __launch_bounds__(kThreads) q4gsw_act_grad_kernel(const __half* 
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;
   if (n < N) {   // N % 8 == 0
-#pragma unroll 4
-    for (int r = (int)((long long)rank * M / C) + ty; r < r_end; r += 32) {
-      const size_t at = (size_t)r * N + n;
-      const uint4 dv = *reinterpret_cast<const uint4*>(d_y + at);
-      const uint32_t dw[4] = {dv.x, dv.y, dv.z, dv.w};
-      float d[8];
+    // rows in groups of kRows: all loads of a group are in flight together
+    for (int r0 = (int)((long long)rank * M / C) + ty; r0 < r_end; r0 += 32 * kRows) {
+      uint4 dv[kRows], zv[kRows];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(u32_as_h2(dw[j]));
-        d[2 * j] = f.x;
-        d[2 * j + 1] = f.y;
+      for (int u = 0; u < kRows; ++u) {
+        const int r = r0 + 32 * u;
+        const size_t at = (size_t)(r < r_end ? r : r0) * N + n;
+        dv[u] = *reinterpret_cast<const uint4*>(d_y + at);
+        if (z) zv[u] = *reinterpret_cast<const uint4*>(z + at);
       }
-      if (z) {
-        const uint4 zv = *reinterpret_cast<const uint4*>(z + at);
-        const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
-        uint32_t out[4];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int r = r0 + 32 * u;
+        if (r >= r_end) break;
+        const uint32_t dw[4] = {dv[u].x, dv[u].y, dv[u].z, dv[u].w};
+        float d[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 f = __half22float2(u32_as_h2(zw[j]));
-          float s0, s1;
-          act_value_slope(f.x, act, s0);
-          act_value_slope(f.y, act, s1);
-          d[2 * j] *= s0;
-          d[2 * j + 1] *= s1;
-          out[j] = h2_as_u32(__floats2half2_rn(d[2 * j], d[2 * j + 1]));
+          const float2 f = __half22float2(u32_as_h2(dw[j]));
+          d[2 * j] = f.x;
+          d[2 * j + 1] = f.y;
         }
-        *reinterpret_cast<uint4*>(d_z + at) = make_uint4(out[0], out[1], out[2], out[3]);
-      }
+        if (z) {
+          const uint32_t zw[4] = {zv[u].x, zv[u].y, zv[u].z, zv[u].w};
+          uint32_t out[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j] += d[j];
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(u32_as_h2(zw[j]));
+            float s0, s1;
+            act_value_slope(f.x, act, s0);
+            act_value_slope(f.y, act, s1);
+            d[2 * j] *= s0;
+            d[2 * j + 1] *= s1;
+            out[j] = h2_as_u32(__floats2half2_rn(d[2 * j], d[2 * j + 1]));
+          }
+          *reinterpret_cast<uint4*>(d_z + (size_t)r * N + n) = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += d[j];
+      }
     }
   }
   if (!d_bias) return;   // the same for every thread of the launch
@@ -111,13 +122,14 @@ __global__ void __launch_bounds__(kThreads) q4gsw_act_grad_kernel(const __half* 
     sums[threadIdx.x] = s;
   }
   cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
+  if (C > 1) cluster.sync();
+  else __syncthreads();
   if (rank == 0 && threadIdx.x < 64 && 64 * blockIdx.x + threadIdx.x < N) {
     float s = sums[threadIdx.x];
     for (int q = 1; q < C; ++q) s += cluster.map_shared_rank(sums, q)[threadIdx.x];
     d_bias[64 * blockIdx.x + threadIdx.x] = s;
   }
-  cluster.sync();   // no CTA leaves while rank 0 reads its sums
+  if (C > 1) cluster.sync();   // no CTA leaves while rank 0 reads its sums
 }
 
 }  // namespace layer
@@ -142,10 +154,10 @@ cudaError_t launch_gated_grad(const __half* gu, const __half* d_h, int M, int F,
 cudaError_t launch_act_grad(const __half* z, const __half* d_y, int M, int N, int act, __half* d_z, float* d_bias,
                             cudaStream_t stream) {
   const int strips = (N + 63) / 64;
-  // row ranges: enough CTAs to fill the SMs (8 resident each), at least 32 rows (one per ty) in each
+  // row ranges: about two CTAs per SM, at least one group of rows in each
   const int sms = sm_count(current_device());
   int C = 1;
-  while (C < 8 && (long long)strips * C < 4LL * sms && M / (2 * C) >= 32) C *= 2;
+  while (C < 8 && (long long)strips * C < 2LL * sms && M / (2 * C) >= 32 * layer::kRows) C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(strips, C, 1);
   cfg.blockDim = dim3(layer::kThreads, 1, 1);

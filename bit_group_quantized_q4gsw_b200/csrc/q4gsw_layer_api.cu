@@ -3,7 +3,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include <cmath>
 #include <cstdint>
 #include <cstdio>
 
@@ -161,7 +160,8 @@ q4gsw_status distill_impl(DistillCall call, DistillArgs a, int half_logits, q4gs
   if (a.M < 0 || a.V <= 0 || a.k < 1 || a.k > 1024) return Q4GSW_ERR_SHAPE;
   if (a.V % 4) return Q4GSW_ERR_SHAPE;
   if (a.V % 8) return Q4GSW_ERR_ALIGN;   // 16-byte vectors of logits and of the gradient
-  if (!(a.temperature > 0.f) || !std::isfinite(a.temperature)) return Q4GSW_ERR_SHAPE;
+  // T^2 and 1 / T are factors: both within the normal fp32 range (NaN fails, too)
+  if (!(a.temperature > 1e-18f && a.temperature < 1e18f)) return Q4GSW_ERR_SHAPE;
   // one CTA per row and tile of 8192 logits, or eight per row: a grid of at most 2^31 - 1
   const long long per_row = a.V / 8192 + 1 > 8 ? a.V / 8192 + 1 : 8;
   if (a.M > 0x7fffffffLL / per_row) return Q4GSW_ERR_SHAPE;

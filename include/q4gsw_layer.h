@@ -150,7 +150,7 @@ Q4GSW_API q4gsw_status q4gsw_linear_act_bwd_f32s(const void *packed, int N, int 
  *            appear more than once.  1 <= k <= 1024.
  *   teacher  fp32 (half_teacher 0) or fp16 (1), [M, k]; whatever stands at a
  *            padding entry is not looked at; -infinity is a weight of zero
- *   T > 0, finite
+ *   1e-18 < T < 1e18 (Q4GSW_ERR_SHAPE else)
  * A row whose entries are all padding (or all -infinity) has loss 0 and a zero
  * gradient.  A student logit of -infinity has probability 0; a row of nothing
  * but -infinity, or with a NaN, gives NaN.  An id outside [0, V) that is not

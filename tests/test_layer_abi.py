@@ -97,7 +97,7 @@ def test_distill_arguments():
 
     for kw, st in ((dict(M=-1), SHAPE), (dict(V=0), SHAPE), (dict(V=62), SHAPE), (dict(V=60), ALIGN),
                    (dict(k=0), SHAPE), (dict(k=1025), SHAPE), (dict(T=0.0), SHAPE), (dict(T=-1.0), SHAPE),
-                   (dict(T=float("inf")), SHAPE), (dict(T=float("nan")), SHAPE), (dict(hl=2), UNSUPPORTED),
+                   (dict(T=float("inf")), SHAPE), (dict(T=float("nan")), SHAPE), (dict(T=1e-39), SHAPE), (dict(T=1e19), SHAPE), (dict(hl=2), UNSUPPORTED),
                    (dict(ht=-1), UNSUPPORTED), (dict(M=0x7fffffff), SHAPE), (dict(z=None), NULL), (dict(i=None), NULL),
                    (dict(t=None), NULL), (dict(lse=None), NULL), (dict(z=P + 8), ALIGN), (dict(i=P + 2), ALIGN),
                    (dict(t=P + 2), ALIGN), (dict(t=P + 1, ht=1), ALIGN), (dict(lse=P + 2), ALIGN)):

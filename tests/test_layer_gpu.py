@@ -1,5 +1,9 @@
 """The gated feed-forward block and the projection with an epilogue against
 the fp64 oracle, within bounds counted from the kernels' roundings."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +13,8 @@ from helpers import cuda
 from oracle import q4gsw_layer as ol
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def q():
@@ -301,7 +307,7 @@ def test_python_checks_of_shapes():
     blob = m.q4gsw_prepack(cuda(codes), cuda(scales), 32)
     x = torch.zeros(4, 128, dtype=torch.float16, device="cuda")
     with pytest.raises(ValueError, match="x must have shape"):
-        m.q4gsw_gated_fwd(blob, 64, 192, 32, x) if False else m.q4gsw_linear_act_fwd(blob, 64, 64, 32, x)
+        m.q4gsw_linear_act_fwd(blob, 64, 64, 32, x)
     with pytest.raises(ValueError, match="packed holds"):
         m.q4gsw_linear_act_fwd(blob, 256, 128, 32, x)
     with pytest.raises(ValueError, match="residual"):
@@ -368,3 +374,83 @@ def test_workload_shapes_of_the_1b_layer_run_as_one_block():
     close(d_h, ol.linear_act_bwd(None, d_y, wd, "none")[0], "d_h")
     close(d_x, ol.gated_bwd(gu.cpu().numpy(), d_h.cpu().numpy(), wg, wu, "silu")[0], "d_x")
     m.q4gsw_device_error_check()
+
+
+FIRST_CALL_CAPTURED = r"""
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+import bit_group_quantized_q4gsw_b200 as q
+torch.manual_seed(0)
+F, K, gs, V, k = 264, 512, 32, 1000, 8
+def w(N):
+    return (torch.randint(0, 16, (N, K), dtype=torch.uint8, device="cuda"),
+            (torch.rand(K // gs, N, device="cuda") * 0.01).half())
+gate, up, proj = w(F), w(F), w(F)
+gated = q.q4gsw_prepack_gated(*gate, *up, gs)
+blob = q.q4gsw_prepack(*proj, gs)
+for M in (1, 12, 100, 600):
+    x, d = torch.randn(M, K, device="cuda").half(), torch.randn(M, F, device="cuda").half() * 0.01
+    z = torch.randn(M, V, device="cuda")
+    idx = torch.randint(0, V, (M, k), device="cuda").int()
+    t, dl = torch.randn(M, k, device="cuda"), torch.ones(M, device="cuda")
+    bias = torch.randn(F, device="cuda").half()
+    def step():
+        h, gu = q.q4gsw_gated_fwd(gated, F, K, gs, x, save_gu=True)
+        y, zz = q.q4gsw_linear_act_fwd(blob, F, K, gs, x, bias=bias, act="silu", residual=h, save_z=True)
+        out = q.q4gsw_gated_bwd(gated, F, K, gs, gu, d) + q.q4gsw_linear_act_bwd(blob, F, K, gs, d, z=zz, act="silu",
+                                                                               want_bias=True)
+        loss, lse, g = q.q4gsw_distill_step(z, idx, t, dl, 2.0)
+        return (h, y) + out + (loss, lse, g, q.q4gsw_distill_bwd(z, lse, idx, t, dl, 2.0)) + \
+            q.q4gsw_distill_fwd(z, idx, t, 2.0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):          # the first call of every kernel of this batch size
+        captured = step()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(captured, step())), M
+q.q4gsw_device_error_check()
+print("first calls captured ok")
+"""
+
+
+def test_first_calls_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED, ROOT], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "first calls captured ok" in r.stdout
+
+
+def test_a_kernel_before_and_after_on_the_same_stream():
+    """The calls overlap their start with the kernel before them (programmatic dependent launch): inputs written,
+    and outputs read, by neighbouring kernels of the stream are seen in order."""
+    m = q()
+    F, K, gs = 1024, 1024, 32
+    cg, sg = weight(F, K, gs, False, 21)
+    cu, su = weight(F, K, gs, False, 22)
+    cd, sd = weight(K, F, gs, False, 23)
+    gated = m.q4gsw_prepack_gated(cuda(cg), cuda(sg), cuda(cu), cuda(su), gs)
+    down = m.q4gsw_prepack(cuda(cd), cuda(sd), 32)
+    for M in (1, 16, 100, 700):
+        x0 = torch.randn(M, K, device="cuda").half()
+        want = x0.clone()
+        for _ in range(3):          # waits between the calls
+            h = m.q4gsw_gated_fwd(gated, F, K, gs, want)
+            torch.cuda.synchronize()
+            want = m.q4gsw_linear_act_fwd(down, K, F, gs, h, residual=want)
+            torch.cuda.synchronize()
+        for _ in range(5):          # none, and the residual stream updated in place
+            x = x0.clone()
+            for _ in range(3):
+                m.q4gsw_linear_act_fwd(down, K, F, gs, m.q4gsw_gated_fwd(gated, F, K, gs, x), residual=x, y=x)
+            # bit patterns: the third layer's products pass the fp16 range, and a NaN equals nothing
+            assert torch.equal(x.view(torch.int16), want.view(torch.int16))
+        # the same with one layer a call, whose values are all finite
+        one = m.q4gsw_linear_act_fwd(down, K, F, gs, m.q4gsw_gated_fwd(gated, F, K, gs, x0), residual=x0)
+        torch.cuda.synchronize()
+        assert torch.isfinite(one).all()
+        for _ in range(20):
+            x = x0.clone()
+            m.q4gsw_linear_act_fwd(down, K, F, gs, m.q4gsw_gated_fwd(gated, F, K, gs, x), residual=x, y=x)
+            assert torch.equal(x, one)

@@ -13,8 +13,8 @@
 // is issued per logit.  Hence:
 //  - a CTA of 128 threads keeps 64 logits of its part of a row in each thread's
 //    registers from the sum to the gradient, so the logits cross the memory
-//    system once; a cluster of up to 16 CTAs holds a row of 131072 tokens
-//    (longer rows are read a second time, shortly after the first, from L2);
+//    system once; a cluster of up to eight CTAs holds a row of 65536
+//    tokens (longer rows take two launches and are read by both);
 //  - the launch holds as many CTAs as fit the SMs (five each) and each walks its
 //    rows.  While a row is reduced and its gradient written, the next row's
 //    logits, teacher entries and scalars are already on their way (cp.async
@@ -38,6 +38,7 @@ namespace q4gsw {
 namespace distill {
 
 constexpr int kMaxCluster = 16;             // past 8: allowed by an attribute of the kernel
+constexpr int kHoldCluster = 8;             // CTAs that hold a row between its loss and its gradient
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kPer = 64;                     // logits per thread and tile
 constexpr int kTile = kThreads * kPer;       // 8192 logits
@@ -215,14 +216,16 @@ __device__ __forceinline__ Entry entry_of(const DistillArgs& a, const RawEntry& 
   return {e.id, a.half_teacher ? __half2float(__ushort_as_half((unsigned short)e.bits)) : __uint_as_float(e.bits)};
 }
 
-// Rows (ROWS): grid = clusters of C CTAs (a power of two); cluster q takes rows
-// q, q + clusters, ...; CTA `rank` owns the vectors [rank VV / C, (rank + 1) VV
-// / C) of each (VV = V / E), in `tiles` tiles (1: they stay in registers).
-// Gradient alone (!ROWS): no clusters; CTA b takes items b, b + grid, ... of the
-// M x C tiles.  Dynamic shared memory: the next tile and two sets of k teacher
-// entries.
-template <bool ROWS, bool HALF>
+// Rows (kLoss, kStep): grid = clusters of C CTAs (a power of two); cluster q
+// takes rows q, q + clusters, ...; CTA `rank` owns the vectors [rank VV / C, (rank
+// + 1) VV / C) of each (VV = V / E), in `tiles` tiles (kStep: one, which stays in
+// registers).  Gradient alone (kGrad): no clusters; CTA b takes items b, b + grid,
+// ... of the M x C tiles.  Dynamic shared memory: the next tile, two sets of k
+// teacher entries.
+enum Mode { kLoss, kStep, kGrad };
+template <int MODE, bool HALF>
 __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const DistillArgs a, int C, int tiles) {
+  constexpr bool ROWS = MODE != kGrad, want_grad = MODE != kLoss;
   constexpr int E = HALF ? 8 : 4;         // logits per vector
   constexpr int NV = kPer / E;            // vectors per thread and tile
   constexpr int TV = kTile / E;           // vectors per tile
@@ -242,16 +245,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inv_t = a.inv_t, c = a.inv_t * kLog2e;
   const int VV = V / E;
-  const bool want_grad = !ROWS || a.grad != nullptr;
   const int c_log = __ffs(C) - 1;
   const int rank = ROWS ? blockIdx.x & (C - 1) : 0;
   const int first = ROWS ? blockIdx.x >> c_log : blockIdx.x, step = ROWS ? gridDim.x >> c_log : gridDim.x;
   const int items = ROWS ? a.M : a.M * C;   // rows, or tiles of rows
-  // loads per item: the slice's tiles, and again for the gradient of a slice longer than one
-  const int loads = ROWS ? (tiles > 1 && want_grad ? 2 * tiles : tiles) : 1;
+  if (MODE != kLoss) tiles = 1;
   const bool entry_warp = 32 * warp < k;   // a warp whose threads have teacher entries
 
-  // Vectors [begin, end) of load `l` of item `it` (a slice's tile).
+  // Vectors [begin, end) of row m.
   struct Span {
     int m, begin, end;
   };
@@ -262,10 +263,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
     const int m = it / C, t = it - m * C;
     return {m, t * TV, min(VV, (t + 1) * TV)};
   };
+  // vectors of load `l` of an item (a tile of the slice)
   auto span_of = [&](int it, int l) -> Span {
     Span s = slice_of(it);
-    if (ROWS && tiles > 1) {
-      s.begin += (l < tiles ? l : l - tiles) * TV;
+    if (MODE == kLoss && tiles > 1) {
+      s.begin += l * TV;
       s.end = min(s.end, s.begin + TV);
     }
     return s;
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
         },
         std::make_integer_sequence<int, NV>{});
     cp_async_commit();
-    if (!ROWS || tiles > 1) {
+    if (MODE == kGrad || (MODE == kLoss && tiles > 1)) {
 #pragma unroll 1
       for (int i = NV - 1; i >= 0 && i * kThreads >= n; --i) slots[i * kThreads] = fill;
     }
@@ -384,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
         }
         // every vector is in registers (the maximum depends on it): its slots take the next load
         const float mx = fmaxf(run_m, warp_max(top_t)), base = base_of(mx, c);
-        if (l + 1 < loads) issue(span_of(it, l + 1));
-        else if (loads == 1 && it + step < items) issue(span_of(it + step, 0));
+        if (l + 1 < tiles) issue(span_of(it, l + 1));
+        else if (it + step < items) issue(span_of(it + step, 0));
         uint64_t sum[2] = {pair(rebased({run_m, run_s}, mx, c), 0.f), 0ull};
         const uint64_t c2 = pair(c, c), minus_base = pair(-base, -base);
         auto add = [&](auto weights) {
@@ -473,45 +475,39 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
     // ---- gradient: coef p for every token of the slice, then the teacher's tokens again
     __half* grow = a.grad + (size_t)m * V;
     if (want_grad) {
+      // the logits stay as they were loaded: unpacked early, those of fp16 rows took
+      // twice the registers through the barriers, and spilled
+#pragma unroll
+      for (int i = 0; i < NV; ++i) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
       const float by = coef * scale;
       const uint64_t c2 = pair(c, c), minus_base = pair(-base, -base), by2 = pair(by, by);
-      for (int l = 0; l < (ROWS ? tiles : 1); ++l) {
-        const Span s = span_of(it, l);
-        if (ROWS && tiles > 1) take(x);
-        __half* dst = grow + ((size_t)s.begin + threadIdx.x) * E;
-        const int n = s.end - s.begin - (int)threadIdx.x;
-        auto store = [&](auto values) {
-          unrolled(
-              [&](auto index) {
-                constexpr int i = decltype(index)::value;
-                float f[E];
-                unpack<HALF>(x[i], f);
-                uint32_t h[E / 2];
+      __half* dst = grow + ((size_t)slice.begin + threadIdx.x) * E;
+      const int n = slice.end - slice.begin - (int)threadIdx.x;
+      auto store = [&](auto values) {
+        unrolled(
+            [&](auto index) {
+              constexpr int i = decltype(index)::value;
+              float f[E];
+              unpack<HALF>(x[i], f);
+              uint32_t h[E / 2];
 #pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                  const float2 g = unpair(values(f[e], f[e + 1]));
-                  h[e / 2] = h2_as_u32(__floats2half2_rn(g.x, g.y));
-                }
-                constexpr int kOff = i * kThreads * E * 2;
-                if constexpr (HALF) st_v4_if<kOff>(i * kThreads < n, dst, h[0], h[1], h[2], h[3]);
-                else st_v2_if<kOff>(i * kThreads < n, dst, h[0], h[1]);
-              },
-              std::make_integer_sequence<int, NV>{});
-        };
-        if (!has) store([&](float, float) { return 0ull; });
-        else if (!is_huge(ref, c))
-          store([&](float z0, float z1) { return mul2(ex2_2(fma2(pair(z0, z1), c2, minus_base)), by2); });
-        else
-          store([&](float z0, float z1) {
-            return mul2(ex2_2(pair(far_exponent(z0, ref, c), far_exponent(z1, ref, c))), by2);
-          });
-        if (ROWS && tiles > 1) {
-          if (l + 1 < tiles) issue(span_of(it, tiles + l + 1));
-          else if (it + step < items) issue(span_of(it + step, 0));
-        }
-      }
-    } else if (tiles > 1 && it + step < items) {
-      issue(span_of(it + step, 0));
+              for (int e = 0; e < E; e += 2) {
+                const float2 g = unpair(values(f[e], f[e + 1]));
+                h[e / 2] = h2_as_u32(__floats2half2_rn(g.x, g.y));
+              }
+              constexpr int kOff = i * kThreads * E * 2;
+              if constexpr (HALF) st_v4_if<kOff>(i * kThreads < n, dst, h[0], h[1], h[2], h[3]);
+              else st_v2_if<kOff>(i * kThreads < n, dst, h[0], h[1]);
+            },
+            std::make_integer_sequence<int, NV>{});
+      };
+      if (!has) store([&](float, float) { return 0ull; });
+      else if (!is_huge(ref, c))
+        store([&](float z0, float z1) { return mul2(ex2_2(fma2(pair(z0, z1), c2, minus_base)), by2); });
+      else
+        store([&](float z0, float z1) {
+          return mul2(ex2_2(pair(far_exponent(z0, ref, c), far_exponent(z1, ref, c))), by2);
+        });
     }
     __syncthreads();
     if (ROWS && rank == 0 && threadIdx.x == 0) {
@@ -523,18 +519,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
       for (int j = threadIdx.x; j < k; j += kThreads) {
         const int id = ids[j];
         if (id < slice.begin * E || id >= slice.end * E) continue;   // padding, or another CTA's token
+        const float z = j == (int)threadIdx.x ? z_own : logit_at<HALF>(row, id);
         int same = 0;
-        for (int i = 0; i < k4; i += 4) {
-          const int4 o = *reinterpret_cast<const int4*>(ids + i);
+        for (int q = 0; q < k4; q += 4) {
+          const int4 o = *reinterpret_cast<const int4*>(ids + q);
           same += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
         }
         float t = ex2(exponent_of(ts[j], teach.m, c));
         if (same > 1) {   // every entry of this token, in the order of the list: each of them writes the same value
           t = 0.f;
-          for (int i = 0; i < k; ++i)
-            if (ids[i] == id) t += ex2(exponent_of(ts[i], teach.m, c));
+          for (int q = 0; q < k; ++q)
+            if (ids[q] == id) t += ex2(exponent_of(ts[q], teach.m, c));
         }
-        const float z = j == (int)threadIdx.x ? z_own : logit_at<HALF>(row, id);
         const float p = ex2(is_huge(ref, c) ? far_exponent(z, ref, c) : fmaf(z, c, -base)) * scale;
         grow[id] = __float2half_rn(coef * (p - t * inv_total));
       }
@@ -566,12 +562,12 @@ struct DistillConfig {
   DistillConfig(const DistillConfig&) = delete;
 };
 
-// One instance: whole rows, or tiles of the gradient; fp16 or fp32 logits.
-template <bool ROWS, bool HALF>
+// One instance: a mode, fp16 or fp32 logits.
+template <int MODE, bool HALF>
 struct DistillKernel {
-  static auto kernel() { return distill::q4gsw_distill_kernel<ROWS, HALF>; }
+  static auto kernel() { return distill::q4gsw_distill_kernel<MODE, HALF>; }
 
-  // bytes of the next tile and two sets of k teacher entries
+  // bytes of the next tile, two sets of k teacher entries
   static size_t smem(int k) { return (size_t)distill::kTile * (HALF ? 2 : 4) + (size_t)((k + 3) & ~3) * 16; }
 
   static cudaError_t setup() {
@@ -585,7 +581,7 @@ struct DistillKernel {
   static cudaError_t launch(const DistillArgs& a, int C, int tiles, unsigned grid, cudaStream_t stream) {
     const cudaError_t e = setup();
     if (e != cudaSuccess) return e;
-    DistillConfig c(grid, C, ROWS, smem(a.k), stream);
+    DistillConfig c(grid, C, MODE != distill::kGrad, smem(a.k), stream);
     return cudaLaunchKernelEx(&c.cfg, kernel(), a, C, tiles);
   }
 
@@ -608,31 +604,30 @@ struct DistillKernel {
   }
 };
 
-template <bool HALF>
+template <int MODE, bool HALF>
 static cudaError_t distill_rows(const DistillArgs& a, cudaStream_t stream, char* route, int route_len) {
   using namespace distill;
-  // CTAs per row: as many as hold it (at most a cluster of 16), and more, down to
-  // 2048 logits each, while the rows would leave SMs without work.
+  // CTAs per row.  The loss alone needs no row held: one CTA walks it, unless
+  // the rows are too few to fill the SMs (702 x 93232: one to two CTAs a row
+  // 41 us, 16 of a single tile 101 us: a row's fixed work, its reductions and the
+  // teacher's list, is then done for ever smaller slices).  With a gradient, as
+  // many as hold the row.  Both grow, down to 2048 logits a CTA, while CTAs are
+  // idle.
   const int sms = sm_count(current_device());
   int C = 1;
-  while (C < kMaxCluster && (long long)C * kTile < a.V) C *= 2;
-  while (C < kMaxCluster && (long long)a.M * C < sms && a.V / (2 * C) >= 2048) C *= 2;
+  if (MODE == kStep)
+    while (C < kHoldCluster && (long long)C * kTile < a.V) C *= 2;
+  while (C < kMaxCluster && (long long)a.M * C < (MODE == kStep ? sms : kPerSm * sms) && a.V / (2 * C) >= 2048) C *= 2;
   const int E = HALF ? 8 : 4;
   const int tiles = ((a.V / E + C - 1) / C * E + kTile - 1) / kTile;
   // one wave of clusters (a cluster that had to wait for a slot would start its
   // rows when the others end theirs)
-  const int most = DistillKernel<true, HALF>::clusters(C, a.k);
+  const int most = DistillKernel<MODE, HALF>::clusters(C, a.k);
   const unsigned n = (unsigned)(a.M < most ? a.M : most);
   if (route)
-    snprintf(route, route_len, "distill_%s launches=1 cluster=%d clusters=%u tiles=%d", a.grad ? "step" : "fwd", C, n,
+    snprintf(route, route_len, "distill_%s launches=1 cluster=%d clusters=%u tiles=%d", MODE == kStep ? "step" : "fwd", C, n,
              tiles);
-  return DistillKernel<true, HALF>::launch(a, C, tiles, n * C, stream);
-}
-
-cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
-                                int route_len) {
-  return half_logits ? distill_rows<true>(a, stream, route, route_len)
-                     : distill_rows<false>(a, stream, route, route_len);
+  return DistillKernel<MODE, HALF>::launch(a, C, tiles, n * C, stream);
 }
 
 cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
@@ -643,8 +638,32 @@ cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStrea
   const int most = kPerSm * sm_count(current_device());
   const unsigned grid = (unsigned)(items < most ? items : most);
   if (route) snprintf(route, route_len, "distill_bwd launches=1 tiles=%d ctas=%u", C, grid);
-  return half_logits ? DistillKernel<false, true>::launch(a, C, 1, grid, stream)
-                     : DistillKernel<false, false>::launch(a, C, 1, grid, stream);
+  return half_logits ? DistillKernel<kGrad, true>::launch(a, C, 1, grid, stream)
+                     : DistillKernel<kGrad, false>::launch(a, C, 1, grid, stream);
+}
+
+cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
+                                int route_len) {
+  using namespace distill;
+  // Loss and gradient in one pass for fp32 logits while a cluster of eight holds
+  // the row and the teacher's list is short.  Otherwise the loss, then the
+  // gradient from its log-sum-exp.  Measured (us, one pass and two): 512 x 32000
+  // with k = 64 27 and 36; 891 x 73496 with k = 319 317 and 142; fp16 logits, which
+  // two passes move in 6 bytes instead of 4, 2048 x 32000 84 and 75.
+  if (a.grad && (half_logits || a.V > kHoldCluster * kTile || a.k > kThreads)) {
+    DistillArgs first = a, second = a;
+    first.grad = nullptr;
+    first.d_loss = nullptr;
+    second.lse_in = a.lse;
+    const cudaError_t e = half_logits ? distill_rows<kLoss, true>(first, stream, nullptr, 0)
+                                      : distill_rows<kLoss, false>(first, stream, nullptr, 0);
+    if (e != cudaSuccess) return e;
+    if (route) snprintf(route, route_len, "distill_step launches=2 fwd + bwd");
+    return launch_distill_bwd(second, half_logits, stream, nullptr, 0);
+  }
+  if (a.grad) return distill_rows<kStep, false>(a, stream, route, route_len);
+  return half_logits ? distill_rows<kLoss, true>(a, stream, route, route_len)
+                     : distill_rows<kLoss, false>(a, stream, route, route_len);
 }
 
 }  // namespace q4gsw

@@ -170,8 +170,9 @@ Q4GSW_API q4gsw_status q4gsw_distill_bwd(const void *logits, int half_logits, in
                                float temperature, const float *d_loss, uint16_t *d_logits,
                                q4gsw_stream_t stream);
 
-/* Both at once, for a d_loss known beforehand: the logits are read from
- * memory once for the loss, lse and gradient. */
+/* Both at once, for a d_loss known beforehand: one launch that reads the
+ * logits once (fp32 logits, V <= 65536, k <= 128), else the two launches above.  (Its
+ * loss and lse are those of q4gsw_distill_fwd up to the order of the sums.) */
 Q4GSW_API q4gsw_status q4gsw_distill_step(const void *logits, int half_logits, int M, int V,
                                 const int32_t *indices, const void *teacher, int half_teacher, int k,
                                 float temperature, const float *d_loss, float *loss, float *lse,

@@ -63,7 +63,9 @@ def test_loss_and_gradient(M, V, k, T, half_logits, half_teacher):
         check(lse, want_lse, "lse")
         check(loss, want_loss, "loss")
         loss2, lse2, g = m.q4gsw_distill_step(dz, di, dt, dd, temperature=T)
-        assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+        # (another split of the row, so another order of the same sums)
+        check(lse2, want_lse, "lse of the step")
+        check(loss2, want_loss, "loss of the step")
         check(g, want_g, "d_logits of the step")
         g2 = m.q4gsw_distill_bwd(dz, lse, di, dt, dd, temperature=T)
         check(g2, ol.distill(z, idx, t, T, d, lse.cpu().numpy())[2], "d_logits of the backward")

@@ -409,10 +409,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
       if (lane == 0) s_warp[warp] = {run_m, run_s};
     } else {
       take(x);
-      if (it + step < items) issue(span_of(it + step, 0));
     }
     if (it + step < items) fetch(slice_of(it + step).m);
     const bool has = __syncthreads_or(some);
+    // No arithmetic has waited for this mode's reads of the slots yet: the barrier
+    // has, so that the copies into them come after it.
+    if (!ROWS && it + step < items) issue(span_of(it + step, 0));
 
     // ---- the row's pair: every CTA's to every CTA of the cluster
     MaxSum mine{0.f, 0.f};
@@ -435,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
     float ref, base, scale;   // p_i = 2^(z_i c - base) scale, base for ref
     if (ROWS) {
       if (C > 1) {
-        if (!sm100::mbar_wait(&s_bar[par], (turn >> 1) & 1, &s_abort, &g_device_error, 0x400u)) break;
+        // (out of time: s_abort and the device error word are set, the row's results are not valid)
+        sm100::mbar_wait(&s_bar[par], (turn >> 1) & 1, &s_abort, &g_device_error, 0x400u);
         mine = lane % kMaxCluster < C ? s_row[par][lane % kMaxCluster] : MaxSum{-INFINITY, 0.f};
         mine = lanes_total<kMaxCluster>(mine, c);
       }
@@ -535,6 +538,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
         grow[id] = __float2half_rn(coef * (p - t * inv_total));
       }
     }
+    if (ROWS && C > 1 && *static_cast<volatile int*>(&s_abort)) {
+      // A wait of this row ran out.  Every warp sees it, since a barrier stands
+      // before the next wait, so all of them leave with the same row.  A peer may
+      // still be on its way to this row and then writes its pair here: stay until
+      // every CTA of the cluster has left or stands here too (their waits are as
+      // bounded as this one was).
+      sm100::cluster_barrier();
+      break;
+    }
   }
   cp_async_wait<0>();   // nothing in flight when a wait ran out
 }
@@ -608,9 +620,9 @@ template <int MODE, bool HALF>
 static cudaError_t distill_rows(const DistillArgs& a, cudaStream_t stream, char* route, int route_len) {
   using namespace distill;
   // CTAs per row.  The loss alone needs no row held: one CTA walks it, unless
-  // the rows are too few to fill the SMs (702 x 93232: one to two CTAs a row
-  // 41 us, 16 of a single tile 101 us: a row's fixed work, its reductions and the
-  // teacher's list, is then done for ever smaller slices).  With a gradient, as
+  // the rows are too few to fill the SMs (702 x 93232 in fp16: two CTAs a row
+  // 30 us, 16 of a single tile each 101: a row's fixed work, its reductions and
+  // the teacher's list, is then done for ever smaller slices).  With a gradient, as
   // many as hold the row.  Both grow, down to 2048 logits a CTA, while CTAs are
   // idle.
   const int sms = sm_count(current_device());
@@ -648,7 +660,7 @@ cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStre
   // Loss and gradient in one pass for fp32 logits while a cluster of eight holds
   // the row and the teacher's list is short.  Otherwise the loss, then the
   // gradient from its log-sum-exp.  Measured (us, one pass and two): 512 x 32000
-  // with k = 64 27 and 36; 891 x 73496 with k = 319 317 and 142; fp16 logits, which
+  // with k = 64 27 and 36; 891 x 73496 with k = 319 317 and 168; fp16 logits, which
   // two passes move in 6 bytes instead of 4, 2048 x 32000 84 and 75.
   if (a.grad && (half_logits || a.V > kHoldCluster * kTile || a.k > kThreads)) {
     DistillArgs first = a, second = a;

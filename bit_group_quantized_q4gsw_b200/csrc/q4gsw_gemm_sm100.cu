@@ -681,7 +681,8 @@ static bool epi_on_ss_route(int M, int rows, int contraction) {
   return ceil((double)ss / sms) * (10 + 0.75 * stages) < ceil((double)ts / sms) * (9 + 0.35 * stages);
 }
 
-// The products with fp16 outputs through an epilogue (any M): the same routes.
+// The products with fp16 outputs through an epilogue (any M): the same routes,
+// but for the register-fed GEMVs, which have none (their pin is passed over).
 template <bool BWD, bool F32S>
 static cudaError_t product_epi(const void* packed, int N, int K, int gs, const uint16_t* act, int M, const Epi& out,
                                cudaStream_t stream, char* route, int route_len) {

@@ -771,8 +771,8 @@ static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs,
   cfg.gridDim = dim3(tiles_f, tiles_t, best_S);
   if (route)
     snprintf(route, route_len, "tcgen05_ts_gemm_%s launches=1 tile=%dx%dx%d stages=%d+%d grid=%dx%dx%d out=%s%s",
-             BWD ? "bwd" : "fwd", BW, a.bt, TK, ST, ST, tiles_f, tiles_t, best_S, std::is_same_v<Out, Epi> ? "epi" : a.tma_out ? "tma" : "st",
-             ad ? " adapter_stage=1" : "");
+             BWD ? "bwd" : "fwd", BW, a.bt, TK, ST, ST, tiles_f, tiles_t, best_S,
+             std::is_same_v<Out, Epi> ? "epi" : a.tma_out ? "tma" : "st", ad ? " adapter_stage=1" : "");
   return cudaLaunchKernelEx(&cfg, kern, map_act, map_pk, map_sc, map_y[0], map_y[1], map_y[2], map_ad, a);
 }
 

@@ -57,7 +57,8 @@ __global__ void q4gsw_prepack_tail_kernel(const void* __restrict__ scales, uint8
   const Layout L = layout_of(N, K, gs, sbytes);
   const size_t tid = blockIdx.x * (size_t)blockDim.x + threadIdx.x;
   const size_t stride = (size_t)gridDim.x * blockDim.x;
-  const size_t n16 = scales ? L.scales_bytes / 16 : 0;   // null: written by q4gsw_interleave_scales_kernel  // N % 8 == 0 -> a whole number of 16-byte vectors
+  // N % 8 == 0 -> a whole number of 16-byte vectors; null: q4gsw_interleave_scales_kernel writes them
+  const size_t n16 = scales ? L.scales_bytes / 16 : 0;
   const uint4* src = reinterpret_cast<const uint4*>(scales);
   uint4* dst = reinterpret_cast<uint4*>(packed + L.scales_offset);
   for (size_t i = tid; i < n16; i += stride) dst[i] = src[i];

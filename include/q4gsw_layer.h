@@ -15,6 +15,10 @@
  * where stated.  The *_f32s forms take a blob with fp32 scales (layout
  * version 2); everything else is the same.
  *
+ * q4gsw_last_route names the kernels of the last call; the route pins of
+ * q4gsw_debug_pin_routes apply, but for the register-fed GEMV, which has no
+ * epilogue (the TMA-ring GEMV runs instead).
+ *
  * fp16 values are uint16_t bit patterns.  Sums, activations and softmax
  * statistics are held in fp32; each fp16 output is rounded once, to nearest
  * even (a value beyond the fp16 range becomes infinite, as that rounding

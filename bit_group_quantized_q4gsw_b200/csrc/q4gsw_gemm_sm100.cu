@@ -96,6 +96,16 @@ struct Args {
   int sc_bytes;       // bytes of the scale box loaded per stage
 };
 
+// Tensor maps of fp16 outputs: boxes of 64 columns x 128 tokens, 128-byte
+// swizzled (y, and where they are used the saved z and the residual).
+constexpr int H_BYTES = 64 * BM * 2;   // one such box, 16 KB
+template <typename Out>
+struct OutMaps {};
+template <>
+struct alignas(64) OutMaps<Epi> {
+  CUtensorMap y, z, res;
+};
+
 constexpr int kMaxST = 5;
 struct SmemCtl {
   uint64_t full[kMaxST];       // stage s loaded (TMA transaction bytes)
@@ -103,6 +113,7 @@ struct SmemCtl {
   uint64_t wready[WST];        // dequantised tile w written (all dequantisation warps)
   uint64_t accfull;
   uint64_t drain;
+  uint64_t res[2];             // residual tile of sub-tile ms loaded (fp16 outputs)
   uint32_t tmem_base;
   int abort;
 };
@@ -125,10 +136,141 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   return v;
 }
 
+// fp16 outputs of a CTA that holds whole sums: the epilogue is applied in
+// registers, as the sums come out of tensor memory (a thread has 32 features of
+// a token), parked in fp16 and written by tensor stores, which clip to the
+// output; the residual comes in by tensor loads, to the place its sums take.
+// Against fp32 parking and a copy-out by the threads (one residual load in flight
+// each) MEASURED.
+template <int MSUB, int RING>
+__device__ __forceinline__ void epi_tiles(const Epi& o, const OutMaps<Epi>& maps, uint8_t* smem, SmemCtl* ctl,
+                                          uint32_t tmem, int warp, int lane, int m0, int n0, int M, int cols,
+                                          bool have_acc) {
+  using namespace sm100;
+  static_assert(8 * H_BYTES <= RING, "y and z of a sub-tile fit where the operand rings were");
+  volatile int* abort_flag = &ctl->abort;
+  const bool epi = warp >= 2, leader = threadIdx.x == 64;
+  const int y_bytes = (o.gated ? 2 : 4) * H_BYTES, region = y_bytes + (o.z ? 4 * H_BYTES : 0);
+  const bool apart = MSUB * region <= RING;   // else the sub-tiles take turns in one region
+  const int z_blocks = min(4, (cols - n0 + 63) / 64);
+  const int y_blocks = o.gated ? min(2, ((cols - n0) / 2 + 63) / 64) : z_blocks;
+  const int y0 = o.gated ? n0 / 2 : n0;
+  const int subs = min(MSUB, (M - m0 + BM - 1) / BM);
+  auto tile_of = [&](int ms) { return smem + (apart ? ms * region : 0); };
+  int requested = 0;   // residual tiles, by the leader
+  auto request = [&](int ms) {
+    mbar_arrive_expect_tx(&ctl->res[ms], y_blocks * H_BYTES);
+    for (int b = 0; b < y_blocks; ++b)
+      tma_load_2d(tile_of(ms) + b * H_BYTES, &maps.res, &ctl->res[ms], n0 + 64 * b, m0 + ms * BM);
+    requested = ms + 1;
+  };
+  if (leader && have_acc && o.res) {   // the rings are idle: every operand has been multiplied
+    request(0);
+    if (apart && subs == 2) request(1);
+  }
+  const int q = warp & 3, h = (warp - 2) >> 2;
+  const int row = 32 * q + lane;
+#pragma unroll 1
+  for (int ms = 0; ms < subs; ++ms) {
+    if (ms > 0 && !apart) {
+      if (leader) {
+        bulk_wait_read_all();
+        if (have_acc && o.res) request(ms);
+      }
+      __syncthreads();
+    }
+    const uint32_t y_at = smem_u32(tile_of(ms)) + row * 128, z_at = y_at + y_bytes;
+    bool ready = epi && have_acc;
+    if (ready && o.res) ready = mbar_wait(&ctl->res[ms], 0, abort_flag, &g_device_error, 16u);
+    if (__all_sync(0xffffffffu, ready)) {
+#pragma unroll 1
+      for (int c32 = 0; c32 < 2; ++c32) {
+        const int n = n0 + 64 * h + 32 * c32;
+        if (n >= cols) break;
+        uint4 bias[4];
+        if (o.bias) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)   // cols % 8 == 0
+            bias[v] = n + 8 * v < cols ? *reinterpret_cast<const uint4*>(o.bias + n + 8 * v) : make_uint4(0, 0, 0, 0);
+        }
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(ms * 256 + 64 * h + 32 * c32), r);
+        tmem_wait_ld();
+        if (o.bias) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const uint32_t b4[4] = {bias[v].x, bias[v].y, bias[v].z, bias[v].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 b = __half22float2(u32_as_h2(b4[e]));
+              r[8 * v + 2 * e] = __float_as_uint(__uint_as_float(r[8 * v + 2 * e]) + b.x);
+              r[8 * v + 2 * e + 1] = __float_as_uint(__uint_as_float(r[8 * v + 2 * e + 1]) + b.y);
+            }
+          }
+        }
+        auto value = [&](int j) { return __uint_as_float(r[j]); };
+        auto pack2 = [](float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); };
+        // 16-byte chunk `c` of this token's 128 bytes in block b
+        auto chunk = [&](uint32_t at, int b, int c) { return at + (uint32_t)(b * H_BYTES + ((c ^ (row & 7)) << 4)); };
+        if (o.z) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            sts128(chunk(z_at, h, 4 * c32 + v),
+                   make_uint4(pack2(value(8 * v), value(8 * v + 1)), pack2(value(8 * v + 2), value(8 * v + 3)),
+                              pack2(value(8 * v + 4), value(8 * v + 5)), pack2(value(8 * v + 6), value(8 * v + 7))));
+        }
+        auto finish = [&](auto kind) {
+          constexpr int act = decltype(kind)::value;
+          if (o.gated) {
+            auto out = [&](int j) { return act_value(value(2 * j), act) * value(2 * j + 1); };
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+              sts128(chunk(y_at, h >> 1, 4 * (h & 1) + 2 * c32 + v),
+                     make_uint4(pack2(out(8 * v), out(8 * v + 1)), pack2(out(8 * v + 2), out(8 * v + 3)),
+                                pack2(out(8 * v + 4), out(8 * v + 5)), pack2(out(8 * v + 6), out(8 * v + 7))));
+            return;
+          }
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const uint32_t at = chunk(y_at, h, 4 * c32 + v);
+            uint4 add = make_uint4(0, 0, 0, 0);
+            if (o.res) add = lds128_u32addr(at);
+            const uint32_t a4[4] = {add.x, add.y, add.z, add.w};
+            uint32_t y4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 a = __half22float2(u32_as_h2(a4[e]));
+              y4[e] = pack2(act_value(value(8 * v + 2 * e), act) + a.x, act_value(value(8 * v + 2 * e + 1), act) + a.y);
+            }
+            sts128(at, make_uint4(y4[0], y4[1], y4[2], y4[3]));
+          }
+        };
+        if (o.act == kActSilu) finish(std::integral_constant<int, kActSilu>{});
+        else if (o.act == kActGelu) finish(std::integral_constant<int, kActGelu>{});
+        else finish(std::integral_constant<int, kActNone>{});
+      }
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (leader && !*abort_flag) {
+      for (int b = 0; b < y_blocks; ++b) tma_store_2d(&maps.y, tile_of(ms) + b * H_BYTES, y0 + 64 * b, m0 + ms * BM);
+      if (o.z)
+        for (int b = 0; b < z_blocks; ++b)
+          tma_store_2d(&maps.z, tile_of(ms) + y_bytes + b * H_BYTES, n0 + 64 * b, m0 + ms * BM);
+      bulk_commit();
+    }
+  }
+  if (leader) {
+    for (int ms = 0; ms < requested; ++ms) mbar_wait_teardown(&ctl->res[ms], 0);   // nothing in flight after an abort
+    bulk_wait_read_all();
+  }
+}
+
 template <bool BWD, int ST, int SCB, int MSUB, bool F32S, typename Out>
 __global__ void __launch_bounds__(kThreads, 1)
 q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_constant__ CUtensorMap map_pk,
-                  const __grid_constant__ CUtensorMap map_sc, const Args<Out> args) {
+                  const __grid_constant__ CUtensorMap map_sc, const __grid_constant__ OutMaps<Out> out_maps,
+                  const Args<Out> args) {
   using namespace sm100;
   using SM = Smem<ST, SCB, MSUB>;
   constexpr int SB = F32S ? 4 : 2;   // bytes per scale
@@ -160,6 +302,8 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
     }
     mbar_init(&ctl->accfull, 1);
     mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->res[0], 1);
+    mbar_init(&ctl->res[1], 1);
     ctl->abort = 0;
     fence_mbar_init();
     prefetch_tmap(&map_act);
@@ -346,11 +490,13 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
   bool have_acc = false;
   if (epi) have_acc = mbar_wait(&ctl->accfull, 0, abort_flag, &g_device_error, 16u);
   if (epi && have_acc) tc_fence_after();
-  auto store4 = [&](int m, int n, float4 val) {
-    epi_store4(args.out, (size_t)m, n, val, epi_load4(args.out, (size_t)m, n));
-  };
+  const bool by_tensor = std::is_same_v<Out, Epi> && S == 1;
+  if constexpr (std::is_same_v<Out, Epi>) {
+    if (by_tensor) epi_tiles<MSUB, OFF_SC>(args.out, out_maps, smem, ctl, tmem, warp, lane, m0, n0, args.M,
+                                           args.out_cols, have_acc);
+  }
 #pragma unroll 1
-  for (int ms = 0; ms < MSUB; ++ms) {
+  for (int ms = 0; ms < (by_tensor ? 0 : MSUB); ++ms) {
     const int mb = m0 + ms * BM;
     if (epi && have_acc) {
       const int q = warp & 3, h = (warp - 2) >> 2;
@@ -370,15 +516,18 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
         }
       }
     }
-    if (S == 1) {
+    if (S == 1) {   // fp32 rows (fp16 ones went by tensor)
       __syncthreads();
       const int rows = args.M - mb < BM ? args.M - mb : BM;
-      if (!*abort_flag) {
-        for (int idx = threadIdx.x; idx < rows * 64; idx += kThreads) {
-          const int row = idx >> 6, chunk = idx & 63;
-          const int n = n0 + 4 * chunk;
-          if (n >= args.out_cols) continue;
-          store4(mb + row, n, *reinterpret_cast<const float4*>(stage_f32 + row * 256 + 4 * (chunk ^ (row & 7))));
+      if constexpr (std::is_same_v<Out, OutSplit>) {
+        if (!*abort_flag) {
+          for (int idx = threadIdx.x; idx < rows * 64; idx += kThreads) {
+            const int row = idx >> 6, chunk = idx & 63;
+            const int n = n0 + 4 * chunk;
+            if (n >= args.out_cols) continue;
+            epi_store4(args.out, (size_t)(mb + row), n,
+                       *reinterpret_cast<const float4*>(stage_f32 + row * 256 + 4 * (chunk ^ (row & 7))), NoOperand{});
+          }
         }
       }
       __syncthreads();
@@ -394,7 +543,8 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
           const int m = mb + row, n = n0 + 4 * chunk;
           if (m >= args.M || n >= args.out_cols) continue;
           const int off = row * 256 + 4 * (chunk ^ (row & 7));
-          // all S loads in flight at once, then the sum in rank order
+          // the epilogue's operands and all S loads in flight at once, then the sum in rank order
+          const auto operands = epi_load4(args.out, (size_t)m, n);
           float4 part[8];
 #pragma unroll
           for (int qq = 0; qq < 8; ++qq)
@@ -408,7 +558,7 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
               acc.z += part[qq].z;
               acc.w += part[qq].w;
             }
-          store4(m, n, acc);
+          epi_store4(args.out, (size_t)m, n, acc, operands);
         }
       }
       cluster.sync();
@@ -469,7 +619,7 @@ static double stage_time(int msub) { return msub == 2 ? 1.6 : 1.0; }
 // the device can hold at once (a GPC must host a whole cluster).
 template <bool BWD, int ST, int SCB, int MSUB, bool F32S, typename Out>
 static cudaError_t gemm_variant(const CUtensorMap& map_act, const CUtensorMap& map_pk, const CUtensorMap& map_sc,
-                                const gemm::Args<Out>& a, int tiles_n, cudaStream_t stream, bool launch, int* S_out,
+                                const gemm::OutMaps<Out>& out_maps, const gemm::Args<Out>& a, int tiles_n, cudaStream_t stream, bool launch, int* S_out,
                                 double* cost_out) {
   using namespace gemm;
   auto kern = q4gsw_gemm_kernel<BWD, ST, SCB, MSUB, F32S, Out>;
@@ -524,7 +674,7 @@ static cudaError_t gemm_variant(const CUtensorMap& map_act, const CUtensorMap& m
   if (!launch) return cudaSuccess;
   attr[0].val.clusterDim.z = best_S;
   cfg.gridDim = dim3(tiles_n, tiles_m, best_S);
-  return cudaLaunchKernelEx(&cfg, kern, map_act, map_pk, map_sc, a);
+  return cudaLaunchKernelEx(&cfg, kern, map_act, map_pk, map_sc, out_maps, a);
 }
 
 // Number of 128-token accumulators per CTA pinned by q4gsw_debug_pin_routes
@@ -572,6 +722,17 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
   const int contraction = BWD ? N : K;
   a.stages_total = (contraction + TK - 1) / TK;
   const int tiles_n = (a.out_cols + BN - 1) / BN;
+  OutMaps<Out> om;
+  if constexpr (std::is_same_v<Out, Epi>) {
+    auto half_map = [&](CUtensorMap* map, const __half* base, int cols) {
+      return make_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols, M, (uint64_t)cols * 2, 64, BM,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (!half_map(&om.y, out.y, out.gated ? out.N / 2 : out.N)) return cudaErrorInvalidValue;
+    om.z = om.res = om.y;   // not read where there is no such tensor
+    if ((out.z && !half_map(&om.z, out.z, out.N)) || (out.res && !half_map(&om.res, out.res, out.N)))
+      return cudaErrorInvalidValue;
+  }
   // Scale slots of 4 KB (fp32 scales with 16-column groups) leave room for one
   // 128-token accumulator per CTA only.
   const bool one_acc_only = sc_bytes > 2048;
@@ -583,12 +744,12 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
                      CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
     if (sc_bytes <= 1024)
-      return msub == 2 ? gemm_variant<BWD, 3, 1024, 2, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost)
-                       : gemm_variant<BWD, 5, 1024, 1, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost);
+      return msub == 2 ? gemm_variant<BWD, 3, 1024, 2, F32S, Out>(map_a, map_pk, map_sc, om, a, tiles_n, stream, launch, S, cost)
+                       : gemm_variant<BWD, 5, 1024, 1, F32S, Out>(map_a, map_pk, map_sc, om, a, tiles_n, stream, launch, S, cost);
     if (sc_bytes <= 2048)
-      return msub == 2 ? gemm_variant<BWD, 3, 2048, 2, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost)
-                       : gemm_variant<BWD, 4, 2048, 1, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost);
-    return gemm_variant<BWD, 4, 4096, 1, F32S, Out>(map_a, map_pk, map_sc, a, tiles_n, stream, launch, S, cost);
+      return msub == 2 ? gemm_variant<BWD, 3, 2048, 2, F32S, Out>(map_a, map_pk, map_sc, om, a, tiles_n, stream, launch, S, cost)
+                       : gemm_variant<BWD, 4, 2048, 1, F32S, Out>(map_a, map_pk, map_sc, om, a, tiles_n, stream, launch, S, cost);
+    return gemm_variant<BWD, 4, 4096, 1, F32S, Out>(map_a, map_pk, map_sc, om, a, tiles_n, stream, launch, S, cost);
   };
   int msub = one_acc_only ? 1 : forced_msub();
   int S = 1;

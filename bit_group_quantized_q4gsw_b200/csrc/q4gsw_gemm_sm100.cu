@@ -94,6 +94,7 @@ struct Args {
   int out_cols;       // forward: N, backward: K
   int stages_total;   // contraction / TK
   int sc_bytes;       // bytes of the scale box loaded per stage
+  int tile0, tiles_n; // fp16 outputs: the launch's first output tile, tiles per row of tiles
 };
 
 // Tensor maps of fp16 outputs: boxes of 64 columns x 128 tokens, 128-byte
@@ -140,8 +141,11 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 // registers, as the sums come out of tensor memory (a thread has 32 features of
 // a token), parked in fp16 and written by tensor stores, which clip to the
 // output; the residual comes in by tensor loads, to the place its sums take.
-// Against fp32 parking and a copy-out by the threads (one residual load in flight
-// each) MEASURED.
+// Against fp32 parking and a copy-out by the threads (us): 512 tokens on
+// [16384, 2048] gated 35.0 -> 31.2, with bias and residual 48.2 -> 35.0 (each
+// thread had one residual load in flight); 4096 tokens on a gated 4096 x 14336
+// block 791 -> 753, of which 725 remain without this function (its exponentials
+// and quotients are 16 of the 28).
 template <int MSUB, int RING>
 __device__ __forceinline__ void epi_tiles(const Epi& o, const OutMaps<Epi>& maps, uint8_t* smem, SmemCtl* ctl,
                                           uint32_t tmem, int warp, int lane, int m0, int n0, int M, int cols,
@@ -284,8 +288,13 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
   const uint32_t sbase = smem_u32(smem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * BN;    // first output feature of the tile
-  const int m0 = blockIdx.y * BM * MSUB;    // first token of the tile
+  int tile_n = blockIdx.x, tile_m = blockIdx.y;
+  if constexpr (std::is_same_v<Out, Epi>) {   // a range of the tiles (gemm_variant)
+    tile_m = (args.tile0 + blockIdx.x) / args.tiles_n;
+    tile_n = args.tile0 + blockIdx.x - tile_m * args.tiles_n;
+  }
+  const int n0 = tile_n * BN;           // first output feature of the tile
+  const int m0 = tile_m * BM * MSUB;    // first token of the tile
   const int S = gridDim.z, split = blockIdx.z;
   const int st_begin = (int)((long long)split * args.stages_total / S);
   const int st_end = (int)((long long)(split + 1) * args.stages_total / S);
@@ -611,6 +620,9 @@ static bool make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base
 // tile's dequantisation, its shared-memory stores and the packed-code copy are
 // paid once).
 static double stage_time(int msub) { return msub == 2 ? 1.6 : 1.0; }
+// From the last wave of one launch to the first stage of the next, in the same
+// unit (from the case above that two launches make slower).
+constexpr double kLaunchGap = 14.0;
 
 // Chooses the split-K factor S of one kernel variant (and its cost), and
 // launches it when `launch` is set.  Each candidate S costs waves(S) *
@@ -669,12 +681,51 @@ static cudaError_t gemm_variant(const CUtensorMap& map_act, const CUtensorMap& m
       best_S = S;
     }
   }
-  *S_out = best_S;
-  *cost_out = best_cost;
-  if (!launch) return cudaSuccess;
-  attr[0].val.clusterDim.z = best_S;
-  cfg.gridDim = dim3(tiles_n, tiles_m, best_S);
-  return cudaLaunchKernelEx(&cfg, kern, map_act, map_pk, map_sc, out_maps, a);
+  if constexpr (std::is_same_v<Out, Epi>) {
+    // Whole waves of unsplit tiles, and what is left over in a second launch
+    // that splits the contraction so that it fills the SMs, too: a launch's gap
+    // and a shorter wave instead of a whole one.  (The fp32 products keep one
+    // launch and their order of sums.)  One launch and two (us), gated: 600 tokens
+    // on 2048 x 8192 62.7 and 56.7; on 4096 x 14336 1024 tokens 219 and 200, 4096
+    // tokens 748 and 737.  Not worth it where the rest splits in two at 32 stages:
+    // 2048 tokens on 2048 x 8192 120.9 and 124.9.
+    const int n1 = max_clusters[d][1].load(std::memory_order_relaxed);
+    int rest = n1 > 0 ? tiles % n1 : 0, rest_S = 1;
+    double rest_cost = 1e30;
+    for (int S = 2; rest > 0 && S <= 8 && a.stages_total / S >= 4; ++S) {
+      const int n = max_clusters[d][S].load(std::memory_order_relaxed);
+      if (n < rest) continue;
+      const double cost = (double)a.stages_total / S * t + 8.0 * MSUB;
+      if (cost < rest_cost - 1e-9) {
+        rest_cost = cost;
+        rest_S = S;
+      }
+    }
+    const double both = (double)(tiles / (n1 > 0 ? n1 : 1)) * (a.stages_total * t + 2.0 * MSUB) + rest_cost + kLaunchGap;
+    const bool two = rest_S > 1 && tiles > rest && both < best_cost - 1e-9;
+    *S_out = two ? -rest_S : best_S;
+    *cost_out = two ? both : best_cost;
+    if (!launch) return cudaSuccess;
+    if (!two) rest = 0, rest_S = best_S;
+    Args<Out> part = a;
+    part.tiles_n = tiles_n;
+    part.tile0 = 0;
+    attr[0].val.clusterDim.z = two ? 1 : best_S;
+    cfg.gridDim = dim3(tiles - rest, 1, two ? 1 : best_S);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_act, map_pk, map_sc, out_maps, part);
+    if (e != cudaSuccess || !two) return e;
+    part.tile0 = tiles - rest;
+    attr[0].val.clusterDim.z = rest_S;
+    cfg.gridDim = dim3(rest, 1, rest_S);
+    return cudaLaunchKernelEx(&cfg, kern, map_act, map_pk, map_sc, out_maps, part);
+  } else {
+    *S_out = best_S;
+    *cost_out = best_cost;
+    if (!launch) return cudaSuccess;
+    attr[0].val.clusterDim.z = best_S;
+    cfg.gridDim = dim3(tiles_n, tiles_m, best_S);
+    return cudaLaunchKernelEx(&cfg, kern, map_act, map_pk, map_sc, out_maps, a);
+  }
 }
 
 // Number of 128-token accumulators per CTA pinned by q4gsw_debug_pin_routes
@@ -713,6 +764,7 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
 
   Args<Out> a;
   a.sc_bytes = sc_bytes;
+  a.tile0 = a.tiles_n = 0;
   a.out = out;
   a.M = M;
   a.N = N;
@@ -765,11 +817,16 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
   }
   e = run(msub, true, &S, &cost);
   const int st = msub == 2 ? 3 : (sc_bytes <= 1024 ? 5 : 4);
+  const int tiles_m = (M + BM * msub - 1) / (BM * msub);
   if (route)
-    snprintf(route, route_len, "tcgen05_gemm_%s launches=1 tile=%dx%dx%d stages=%d+%d grid=%dx%dx%d",
-             BWD ? "bwd" : "fwd", BM * msub, BN, TK, st, WST, tiles_n, (M + BM * msub - 1) / (BM * msub), S);
+    snprintf(route, route_len, "tcgen05_gemm_%s launches=%d tile=%dx%dx%d stages=%d+%d grid=%dx%dx%d",
+             BWD ? "bwd" : "fwd", S < 0 ? 2 : 1, BM * msub, BN, TK, st, WST, tiles_n, tiles_m, S < 0 ? 1 : S);
   if (route && std::is_same_v<Out, Epi>) {
-    const size_t len = strlen(route);
+    size_t len = strlen(route);
+    if (S < 0) {
+      snprintf(route + len, route_len - len, " rest_splits=%d", -S);
+      len = strlen(route);
+    }
     snprintf(route + len, route_len - len, " out=epi");
   }
   return e;
@@ -831,15 +888,16 @@ cudaError_t launch_gemm_bwd(const void* packed, int N, int K, int gs, bool f32s,
 // twice as many output tiles can leave the tensor-memory kernel (128 x 256
 // tiles) a second, mostly empty wave where the shared-memory kernel (256 x 256)
 // fits one.  Time per wave, measured at 512 tokens and 512 .. 4096 input features
-// (us): 9 + 0.35 per stage, and 10 + 0.75 per stage; 512 x 16384 x 2048 takes 38.3
-// on the first and 34.4 on the second, 512 x 9472 x 2048 (148 tiles) 20.3 and 32.2.
+// (us): 10 + 0.32 per stage of 64, and 7 + 0.75; 512 x 16384 takes 25.7 on the
+// first and 14.4 on the second with 512 input features, 37.7 and 31.2 with 2048,
+// 60.7 and 61.2 with 4096; 512 x 9472 (148 tiles) with 2048 19.3 and 22.0.
 static bool epi_on_ss_route(int M, int rows, int contraction) {
   if (route_pins().gemm != kGemmAuto || M > 512 || M <= 256) return use_ss_route(M);
   const int sms = sm_count(current_device());
   const double stages = (contraction + 63) / 64;
   const int ts = (rows + 127) / 128 * 2, ss = (rows + 255) / 256 * 2;   // tiles: two of up to 256 tokens
   if (ss <= sms / 2) return false;   // the contraction would be split: the tensor-memory kernel
-  return ceil((double)ss / sms) * (10 + 0.75 * stages) < ceil((double)ts / sms) * (9 + 0.35 * stages);
+  return ceil((double)ss / sms) * (7 + 0.75 * stages) < ceil((double)ts / sms) * (10 + 0.32 * stages);
 }
 
 // The products with fp16 outputs through an epilogue (any M): the same routes,

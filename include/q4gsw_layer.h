@@ -66,7 +66,8 @@ Q4GSW_API q4gsw_status q4gsw_prepack_gated_f32s(const uint8_t *codes_gate, const
                                       void *packed, size_t packed_bytes, q4gsw_stream_t stream);
 
 /*
- * Forward, one launch: x fp16 [M, K] -> h fp16 [M, F].
+ * Forward, one launch (two where whole waves of output tiles leave a few over,
+ * which then split the contraction): x fp16 [M, K] -> h fp16 [M, F].
  *   gu  fp16 [M, 2 F] or NULL: the pairs (g_j, u_j) at columns 2 j, 2 j + 1,
  *       what the backward pass reads.
  * Error of h: that of g and u as in q4gsw_linear_fwd, carried through
@@ -80,7 +81,8 @@ Q4GSW_API q4gsw_status q4gsw_gated_fwd_f32s(const void *packed, int F, int K, in
                                   q4gsw_stream_t stream);
 
 /*
- * Backward, two launches: gu as saved by the forward, d_h fp16 [M, F] ->
+ * Backward, a launch for the activation's gradient and a product as above: gu as
+ * saved by the forward, d_h fp16 [M, F] ->
  *   d_gu  fp16 [M, 2 F], the pairs (d_g, d_u) in the columns of gu (rounded
  *         once; what an adapter on the gate or up projection trains from);
  *         d_gu may be gu itself;
@@ -103,7 +105,7 @@ Q4GSW_API q4gsw_status q4gsw_gated_bwd_f32s(const void *packed, int F, int K, in
  * ---------------------------------------------------------------------- */
 
 /*
- * Forward, one launch: x fp16 [M, K] -> y fp16 [M, N].
+ * Forward, one launch (or two, as above): x fp16 [M, K] -> y fp16 [M, N].
  *   bias      fp16 [N] or NULL
  *   residual  fp16 [M, N] or NULL; y may be the residual's buffer (the stream
  *             is then updated in place)
@@ -120,7 +122,8 @@ Q4GSW_API q4gsw_status q4gsw_linear_act_fwd_f32s(const void *packed, int N, int 
                                        q4gsw_stream_t stream);
 
 /*
- * Backward, one or two launches: d_y fp16 [M, N] ->
+ * Backward, a launch for d_z and d_bias where there are any and a product as
+ * above: d_y fp16 [M, N] ->
  *   d_x     fp16 [M, K]
  *   d_z     fp16 [M, N], required with an activation (with act NONE d_z is
  *           d_y: pass NULL); d_z may be z or d_y itself

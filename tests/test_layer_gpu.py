@@ -351,6 +351,90 @@ def test_both_gemm_routes_agree_with_the_oracle(gemm, M):
     close(d_gu, want_dgu, "d_gu")
 
 
+# few input features: no split, so that every output goes out by tensor stores; tiles of 256 columns and 128 or
+# 256 tokens that end inside the output, one sub-tile and two, with and without room for both at once
+@pytest.mark.parametrize("gemm", ["ss1", "ss2"])
+@pytest.mark.parametrize("M,N,K", [(17, 8, 64), (128, 72, 192), (129, 264, 448), (257, 520, 128), (640, 1048, 192)])
+def test_whole_sums_of_the_shared_memory_gemm(gemm, M, N, K):
+    m = q()
+    gs = 32
+    codes, scales = weight(N, K, gs, False, 31)
+    w = ol.dequant(codes, scales, gs)
+    blob = m.q4gsw_prepack(cuda(codes), cuda(scales), gs)
+    rng = np.random.default_rng(M + N)
+    x = rng.standard_normal((M, K)).astype(np.float16)
+    bias = rng.standard_normal(N).astype(np.float16)
+    res = rng.standard_normal((M, N)).astype(np.float16)
+    d_y = (rng.standard_normal((M, N)) * 0.05).astype(np.float16)
+    m.q4gsw_debug_pin_routes(gemm=gemm)
+    try:
+        for kind, b, r, save in (("gelu_tanh", bias, res, True), ("silu", None, res, False), ("none", bias, None, False),
+                                 ("silu", bias, None, True)):
+            y, z = (torch.full((M + 2, N), 7.0, dtype=torch.float16, device="cuda") for _ in range(2))
+            if r is not None:
+                y[:M] = cuda(r)                       # the residual stream updated in place
+            m.q4gsw_linear_act_fwd(blob, N, K, gs, cuda(x), bias=None if b is None else cuda(b), act=kind,
+                                   residual=None if r is None else y[:M], y=y[:M], z=z[:M] if save else None)
+            assert "out=epi" in m.q4gsw_last_route() and m.q4gsw_last_route().split("grid=")[1].split()[0].endswith("x1")
+            want_y, want_z = ol.linear_act_fwd(x, w, kind, b, r)
+            close(y[:M], want_y, f"y {kind}")
+            if save:
+                close(z[:M], want_z, f"z {kind}")
+            assert (y[M:] == 7.0).all() and (z[M if save else 0:] == 7.0).all()
+        F = N // 16 * 8
+        cg, sg = weight(F, K, gs, False, 32)
+        cu, su = weight(F, K, gs, False, 33)
+        gated = m.q4gsw_prepack_gated(cuda(cg), cuda(sg), cuda(cu), cuda(su), gs) if F else None
+        if F:
+            wg, wu = ol.dequant(cg, sg, gs), ol.dequant(cu, su, gs)
+            h, gu = m.q4gsw_gated_fwd(gated, F, K, gs, cuda(x), act="gelu_tanh", save_gu=True)
+            want_h, want_gu = ol.gated_fwd(x, wg, wu, "gelu_tanh")
+            close(h, want_h, "h")
+            close(gu, want_gu, "gu")
+            assert torch.equal(h, m.q4gsw_gated_fwd(gated, F, K, gs, cuda(x), act="gelu_tanh"))
+        d_x, _, _ = m.q4gsw_linear_act_bwd(blob, N, K, gs, cuda(d_y))
+        close(d_x, ol.linear_act_bwd(None, d_y, w, "none")[0], "d_x")
+    finally:
+        m.q4gsw_debug_pin_routes()
+    m.q4gsw_device_error_check()
+
+
+@pytest.mark.parametrize("gemm,M", [("ss1", 520), ("ss2", 1040)])
+def test_tiles_left_over_by_whole_waves(gemm, M):
+    """30 x 5 output tiles on 148 SMs: two of them in a second launch that splits the contraction."""
+    m = q()
+    N, K, gs = 7680, 2048, 128
+    codes, scales = weight(N, K, gs, False, 34)
+    w = ol.dequant(codes, scales, gs)
+    blob = m.q4gsw_prepack(cuda(codes), cuda(scales), gs)
+    rng = np.random.default_rng(M)
+    x = rng.standard_normal((M, K)).astype(np.float16)
+    res = rng.standard_normal((M, N)).astype(np.float16)
+    want_y, want_z = ol.linear_act_fwd(x, w, "silu", None, res)
+    m.q4gsw_debug_pin_routes(gemm=gemm)
+    try:
+        y = cuda(res)
+        _, z = m.q4gsw_linear_act_fwd(blob, N, K, gs, cuda(x), act="silu", residual=y, y=y, save_z=True)
+        if torch.cuda.get_device_properties(0).multi_processor_count == 148:
+            assert "launches=2" in m.q4gsw_last_route() and "rest_splits=" in m.q4gsw_last_route()
+        close(y, want_y, "y")
+        close(z, want_z, "z")
+        g = torch.cuda.CUDAGraph()
+        y2 = torch.empty_like(y)
+        xs, rs = cuda(x), cuda(res)
+        side = torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=side):
+            m.q4gsw_linear_act_fwd(blob, N, K, gs, xs, act="silu", residual=rs, y=y2)
+        for _ in range(3):
+            y2.fill_(7.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y2, y)
+    finally:
+        m.q4gsw_debug_pin_routes()
+    m.q4gsw_device_error_check()
+
+
 def test_workload_shapes_of_the_1b_layer_run_as_one_block():
     """norm-free feed-forward half of a layer: gated block, down projection onto the residual, and back."""
     m = q()

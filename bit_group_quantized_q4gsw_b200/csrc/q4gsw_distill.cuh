@@ -396,7 +396,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
             float f[E];
             unpack<HALF>(x[i], f);
 #pragma unroll
-            for (int e = 0; e < E; e += 2) sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], weights(f[e], f[e + 1]));
+            for (int e = 0; e < E; e += 2) {
+              const uint64_t w = weights(f[e], f[e + 1]);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], w);
+              const float2 kept = unpair(w);
+              f[e] = kept.x;
+              f[e + 1] = kept.y;
+            }
+            // the weights take the logits' registers: the gradient is a factor away from them
+            if constexpr (MODE == kStep)
+              x[i] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                __float_as_uint(f[3]));
           }
         };
         if (!is_huge(mx, c)) add([&](float z0, float z1) { return ex2_2(fma2(pair(z0, z1), c2, minus_base)); });
@@ -482,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
       // twice the registers through the barriers, and spilled
 #pragma unroll
       for (int i = 0; i < NV; ++i) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
-      const float by = coef * scale;
+      // (kStep) the weights are against the warp's maximum
+      const float by = coef * scale * (MODE == kStep ? rebased({run_m, 1.f}, ref, c) : 1.f);
       const uint64_t c2 = pair(c, c), minus_base = pair(-base, -base), by2 = pair(by, by);
       __half* dst = grow + ((size_t)slice.begin + threadIdx.x) * E;
       const int n = slice.end - slice.begin - (int)threadIdx.x;
@@ -505,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
             std::make_integer_sequence<int, NV>{});
       };
       if (!has) store([&](float, float) { return 0ull; });
+      else if (MODE == kStep) store([&](float w0, float w1) { return mul2(pair(w0, w1), by2); });
       else if (!is_huge(ref, c))
         store([&](float z0, float z1) { return mul2(ex2_2(fma2(pair(z0, z1), c2, minus_base)), by2); });
       else

@@ -25,31 +25,32 @@ namespace layer {
 constexpr int kThreads = 256;
 constexpr int kRows = 4;   // rows a thread of the projection's gradient has in flight
 
-// One item = 8 gated features: 32 bytes of (g, u) pairs, 16 of d_h.  A thread
-// reads all of an item before it writes any of it, so d_gu may be gu.
+// One item a thread = 8 gated features: 32 bytes of (g, u) pairs, 16 of d_h, all
+// read before any is written, so d_gu may be gu.  (As many CTAs as are resident,
+// walking the items, took 0.7 us longer at 512 x 8192: the second item's loads
+// waited for the first's results.)
 __global__ void __launch_bounds__(kThreads) q4gsw_gated_grad_kernel(const __half* gu, const __half* d_h, __half* d_gu,
                                                                     size_t items, int act) {
   griddep_launch_dependents();
   griddep_wait();
-  const size_t stride = (size_t)gridDim.x * kThreads;
-  for (size_t i = blockIdx.x * (size_t)kThreads + threadIdx.x; i < items; i += stride) {
-    const uint4 p0 = reinterpret_cast<const uint4*>(gu)[2 * i], p1 = reinterpret_cast<const uint4*>(gu)[2 * i + 1];
-    const uint4 dh = reinterpret_cast<const uint4*>(d_h)[i];
-    const uint32_t pw[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
-    const uint32_t hw[4] = {dh.x, dh.y, dh.z, dh.w};
-    uint32_t out[8];
+  const size_t i = blockIdx.x * (size_t)kThreads + threadIdx.x;
+  if (i >= items) return;
+  const uint4 p0 = reinterpret_cast<const uint4*>(gu)[2 * i], p1 = reinterpret_cast<const uint4*>(gu)[2 * i + 1];
+  const uint4 dh = reinterpret_cast<const uint4*>(d_h)[i];
+  const uint32_t pw[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+  const uint32_t hw[4] = {dh.x, dh.y, dh.z, dh.w};
+  uint32_t out[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 p = __half22float2(u32_as_h2(pw[j]));   // (g, u)
-      const float2 d2 = __half22float2(u32_as_h2(hw[j >> 1]));
-      const float d = (j & 1) ? d2.y : d2.x;
-      float slope;
-      const float a = act_value_slope(p.x, act, slope);
-      out[j] = h2_as_u32(__floats2half2_rn(d * p.y * slope, d * a));
-    }
-    reinterpret_cast<uint4*>(d_gu)[2 * i] = make_uint4(out[0], out[1], out[2], out[3]);
-    reinterpret_cast<uint4*>(d_gu)[2 * i + 1] = make_uint4(out[4], out[5], out[6], out[7]);
+  for (int j = 0; j < 8; ++j) {
+    const float2 p = __half22float2(u32_as_h2(pw[j]));   // (g, u)
+    const float2 d2 = __half22float2(u32_as_h2(hw[j >> 1]));
+    const float d = (j & 1) ? d2.y : d2.x;
+    float slope;
+    const float a = act_value_slope(p.x, act, slope);
+    out[j] = h2_as_u32(__floats2half2_rn(d * p.y * slope, d * a));
   }
+  reinterpret_cast<uint4*>(d_gu)[2 * i] = make_uint4(out[0], out[1], out[2], out[3]);
+  reinterpret_cast<uint4*>(d_gu)[2 * i + 1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
 // grid = (strips of 64 features, C row ranges), cluster = (1, C, 1).  Thread
@@ -142,10 +143,10 @@ __global__ void __launch_bounds__(kThreads) q4gsw_act_grad_kernel(const __half* 
 cudaError_t launch_gated_grad(const __half* gu, const __half* d_h, int M, int F, int act, __half* d_gu,
                               cudaStream_t stream) {
   const size_t items = (size_t)M * (size_t)F / 8;
-  const size_t most = (size_t)8 * sm_count(current_device());   // resident CTAs
-  const size_t want = (items + layer::kThreads - 1) / layer::kThreads;
+  const size_t grid = (items + layer::kThreads - 1) / layer::kThreads;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(want < most ? want : most), 1, 1);
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
   cfg.blockDim = dim3(layer::kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

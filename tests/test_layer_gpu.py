@@ -101,7 +101,7 @@ LINEAR = [
     (17, 8, 64, 16, False, "gelu_tanh", True, True), (77, 264, 448, 16, False, "none", False, False),
     (130, 1048, 1024, 32, True, "gelu_tanh", True, False), (508, 2048, 1024, 32, False, "none", True, True),
     (512, 136, 4096, 256, False, "silu", True, True), (600, 200, 192, 64, False, "gelu_tanh", True, True),
-    (1030, 392, 1024, 128, True, "none", True, True),
+    (1030, 392, 1024, 128, True, "none", True, True), (2600, 4104, 64, 64, False, "gelu_tanh", True, False),
 ]
 
 

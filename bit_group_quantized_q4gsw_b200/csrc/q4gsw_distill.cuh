@@ -7,13 +7,15 @@
 //   loss = T^2 sum_j q_j (log q_j - z[i_j] / T + lse)
 //   d_z[i] = d_loss T (exp(z_i / T - lse) - sum of q_j with i_j = i)
 //
-// The rows are long (V tokens) and each logit is used for one exponential or
-// two, so the kernels are streams: what they cost is the bytes of the logits
-// and of the gradient, provided enough of them are always in flight and little
-// is issued per logit.  Hence:
+// The rows are long (V tokens) and each logit is used for one exponential, so
+// the kernels are streams: what they cost is the bytes of the logits and of the
+// gradient, provided enough of them are always in flight and little is issued
+// per logit.  Hence:
 //  - a CTA of 128 threads keeps 64 logits of its part of a row in each thread's
-//    registers from the sum to the gradient, so the logits cross the memory
-//    system once; a cluster of up to eight CTAs holds a row of 65536
+//    registers, and from the sum on their weights in their place, from which the
+//    gradient is a factor away: the logits cross the memory system once and each
+//    costs one exponential (with a second one for the gradient 27.3 us instead
+//    of 25.2 for the step of 512 x 32000); a cluster of up to eight CTAs holds a row of 65536
 //    tokens (longer rows take two launches and are read by both);
 //  - the launch holds as many CTAs as fit the SMs (five each) and each walks its
 //    rows.  While a row is reduced and its gradient written, the next row's
@@ -488,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
     // ---- gradient: coef p for every token of the slice, then the teacher's tokens again
     __half* grow = a.grad + (size_t)m * V;
     if (want_grad) {
-      // the logits stay as they were loaded: unpacked early, those of fp16 rows took
-      // twice the registers through the barriers, and spilled
+      // the logits (kStep: their weights) stay as they are: unpacked early, those of
+      // fp16 rows took twice the registers through the barriers, and spilled
 #pragma unroll
       for (int i = 0; i < NV; ++i) asm volatile("" : "+r"(x[i].x), "+r"(x[i].y), "+r"(x[i].z), "+r"(x[i].w));
       // (kStep) the weights are against the warp's maximum
@@ -672,7 +674,7 @@ cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStre
   // Loss and gradient in one pass for fp32 logits while a cluster of eight holds
   // the row and the teacher's list is short.  Otherwise the loss, then the
   // gradient from its log-sum-exp.  Measured (us, one pass and two): 512 x 32000
-  // with k = 64 27 and 36; 891 x 73496 with k = 319 317 and 168; fp16 logits, which
+  // with k = 64 25 and 36; 891 x 73496 with k = 319 317 and 168; fp16 logits, which
   // two passes move in 6 bytes instead of 4, 2048 x 32000 84 and 75.
   if (a.grad && (half_logits || a.V > kHoldCluster * kTile || a.k > kThreads)) {
     DistillArgs first = a, second = a;

@@ -9,6 +9,10 @@
 // The epilogue adds no pass over memory: a projection followed by separate
 // bias, activation and residual passes writes and re-reads its fp32 result
 // (8 bytes an element) per pass; here each element is written once, in 2 bytes.
+// What it costs beside the plain fp32 product (us): a token of 2048 x 8192 6.9 and
+// 6.7, 16 tokens of 14336 x 4096 15.0 and 14.2 (bias and residual), 508 tokens of
+// 2048 x 8192 20.7 and 19.8, 512 tokens of 16384 x 2048 35.0 and 35.0, gated
+// there 31.2.
 //
 // The gated block's weight interleaves its two matrices row by row (feature
 // 2 j = gate row j, 2 j + 1 = up row j; the packed layout already stores such

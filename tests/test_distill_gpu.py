@@ -119,6 +119,36 @@ def test_a_teacher_weight_on_a_masked_token_gives_an_infinite_loss_and_a_finite_
     assert abs(g[0, 5].item() + 0.5) < 1e-3 and abs(g[0, 6].item() - (1 / 63 - 0.5)) < 1e-3
 
 
+@pytest.mark.parametrize("T", [0.5, 2.0])
+@pytest.mark.parametrize("offset", [0.0, -2e4, 2e4])
+def test_parts_of_a_row_masked_whole(T, offset):
+    """The gradient of one pass is a factor away from weights against a part's own maximum: parts that are masked
+    whole, with -infinity or with the type's lowest value, beside parts far from zero."""
+    m = q()
+    V, k = 32000, 16
+    rng = np.random.default_rng(int(abs(offset)) + int(4 * T))
+    base = (rng.standard_normal((4, V)) * 3 + offset).astype(np.float32)
+    masks = [(0, 0), (0, 8000), (0, 24000), (8000, 16000)]
+    idx = (24000 + np.stack([rng.permutation(8000)[:k] for _ in masks])).astype(np.int32)
+    t = (rng.standard_normal((4, k)) * 2).astype(np.float32)
+    d = rng.uniform(0.5, 1.5, 4).astype(np.float32)
+    out = []
+    for fill in (-np.inf, np.finfo(np.float32).min):
+        z = base.copy()
+        for r, (lo, hi) in enumerate(masks):
+            z[r, lo:hi] = fill
+        out.append(m.q4gsw_distill_step(cuda(z), cuda(idx), cuda(t), cuda(d), temperature=T))
+        assert "launches=1" in m.q4gsw_last_route()
+        if fill == -np.inf:
+            for got, want, what in zip(out[0], ol.distill(z, idx, t, T, d), ("loss", "lse", "d_logits")):
+                check(got, want, what)
+    for a, b in zip(*out):      # a masked token weighs nothing either way
+        assert torch.equal(a, b)
+    for r, (lo, hi) in enumerate(masks):
+        assert (out[0][2][r, lo:hi] == 0).all()
+    m.q4gsw_device_error_check()
+
+
 def test_ids_out_of_range_count_as_padding_and_are_reported():
     m = q()
     M, V, k = 4, 256, 6

@@ -170,3 +170,63 @@ def distill(logits, indices, teacher, temperature, d_loss=None, lse_in=None):
         b = _rounded(d, np.abs(coef) * (p + qs) * 2.0 ** -19 * size[:, None])
         grad = (d, b)
     return (loss, b_loss), (lse, b_lse), grad
+
+
+def distill_spread(logits, indices, teacher, temperature, d_loss=None, lse_in=None):
+    """As ``distill``, with bounds that go by how far the logits of a row are from each other, not from zero: what a
+    row has in common cancels in p and in the loss, and every value that an output is made of is held against the
+    row's own maximum.  (The gradient from a saved ``lse_in`` is that of ``lse_in`` as it was saved.)
+
+    In units of 2^-24, with s = |z - max| / T (s_t for the teacher) and S = sum p s:
+      an exponent (z - max) c: 3 s for c = fp32(fp32(1/T) fp32(log2 e)), s for its own rounding, s for each of at
+      most three changes of maximum (tile, warp, CTA): 8 s of a weight with some to spare, 8 S of their sum;
+      a weight's exponential 4, each change of maximum 4 + 1; a sum over V: V / 256 additions in a row in one thread
+      and 5 for a change of maximum per tile of 8192, then 16 over lanes, warps and CTAs: V / 200 + 128 with some to
+      spare;
+      the teacher's weights: the same over at most 8 additions in a thread, 128;
+      1 / sum, the products with coef and the difference p - q: 8, within the 128.
+    A logarithm adds 2 of itself, a quotient by T and a sum 2 of theirs each.  From a saved lse the exponent is
+    z / T - lse: 8 of its size, and while |lse| < 180 another 8 of |z| / T + |lse|.
+    """
+    (loss, _), (lse, _), grad = distill(logits, indices, teacher, temperature, d_loss, lse_in)
+    unit = 2.0 ** -24
+    z = np.asarray(logits, np.float64) / temperature
+    idx = np.asarray(indices)
+    V = z.shape[1]
+    valid = (idx >= 0) & (idx < V)
+    t = np.where(valid, np.asarray(teacher, np.float64), -np.inf) / temperature
+    far = lambda a: np.where(np.isfinite(a), np.abs(a), 0.0)   # noqa: E731  (a weight of zero: no matter how far)
+    m = z.max(1, keepdims=True)
+    s = far(z - m)
+    p = np.exp(z - m)
+    p /= p.sum(1, keepdims=True)
+    top = t.max(1, keepdims=True)
+    top = np.where(np.isfinite(top), top, 0.0)
+    s_t = far(t - top)
+    q = np.exp(t - top)
+    total = q.sum(1, keepdims=True)
+    q = q / np.where(total > 0, total, 1.0)
+    S, S_t = (p * s).sum(1, keepdims=True), (q * s_t).sum(1, keepdims=True)
+    of_sum = (V / 200 + 128 + 8 * S) * unit
+    of_q = (128 + 8 * (s_t + S_t)) * unit
+    log_s = lse[:, None] - m
+    at = far(np.take_along_axis(z, np.where(valid, idx, 0), 1) - m)
+    log_total = np.log(np.where(total > 0, total, 1.0))
+    parts = s_t + np.abs(log_total) + at + np.abs(log_s)        # what a term of the loss is added from
+    b_loss = temperature ** 2 * ((q * (of_q * parts + 8 * unit * parts)).sum(1) + of_sum[:, 0] + 128 * unit)
+    b_lse = of_sum[:, 0] + unit * (2 * np.abs(log_s[:, 0]) + 2 * np.abs(m[:, 0]) + np.abs(lse))
+    if grad is None:
+        return (loss, b_loss), (lse, b_lse), None
+    d = grad[0]
+    if lse_in is None:
+        of_p = of_sum + 8 * s * unit
+    else:
+        ref = np.asarray(lse_in, np.float64)[:, None]
+        p = np.exp(z - ref)
+        near = np.where(np.abs(ref) < 180, far(z) + np.abs(ref), 0.0)
+        of_p = (16 + 8 * far(z - ref) + 8 * near) * unit
+    coef = np.abs(np.asarray(d_loss, np.float64)[:, None] * temperature)
+    err = p * of_p
+    for row in range(z.shape[0]):
+        np.add.at(err[row], idx[row][valid[row]], (q * of_q)[row][valid[row]])
+    return (loss, b_loss), (lse, b_lse), (d, _rounded(d, coef * err))

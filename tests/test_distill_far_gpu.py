@@ -1,0 +1,51 @@
+"""The distillation operators where a row lies far from zero, against bounds that go by the spread of the row."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import cuda
+from oracle import q4gsw_layer as ol
+from test_distill_gpu import check, inputs, q
+
+pytestmark = pytest.mark.gpu
+
+OFFSETS = [0.0, 1e3, -2e4, 2e4]
+
+
+def shifted(M, V, k, offset, seed, **kw):
+    """Rows around `offset`, the teacher's too; parts of a row around other values, so that the warps' and the
+    CTAs' maxima differ."""
+    z, idx, t, d = inputs(M, V, k, seed, half_teacher=False, **kw)
+    rng = np.random.default_rng(seed + 1)
+    z = z.astype(np.float32) + rng.uniform(-4, 4, (M, V // 8)).astype(np.float32).repeat(8, 1) + np.float32(offset)
+    return z, idx, t + np.float32(offset), d
+
+
+@pytest.mark.parametrize("T", [0.5, 1.0, 1.7])
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("M,V,k", [(3, 1024, 8), (5, 32000, 64), (2, 65536, 128), (200, 8192, 16)])
+def test_what_a_row_has_in_common_cancels_in_the_one_pass_step(M, V, k, offset, T):
+    m = q()
+    T = float(np.float32(T))
+    z, idx, t, d = shifted(M, V, k, offset, 21, dup=True)
+    loss, lse, g = m.q4gsw_distill_step(cuda(z), cuda(idx), cuda(t), cuda(d), temperature=T)
+    assert "launches=1" in m.q4gsw_last_route()
+    _, want_lse, want_g = ol.distill_spread(z, idx, t, T, d)
+    check(lse, want_lse, "lse")
+    check(g, want_g, "d_logits")
+    m.q4gsw_device_error_check()
+
+
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("M,V", [(1, 262144), (800, 49152)])
+def test_many_tiles_a_row_far_from_zero(M, V, offset):
+    """A CTA of the loss walks several tiles, in which its running maximum grows."""
+    m = q()
+    T, k = 0.5, 20
+    z, idx, t, d = shifted(M, V, k, offset, 22)
+    z = np.sort(z.reshape(M, -1, 4096), axis=1).reshape(M, V)      # from tile to tile
+    _, lse = m.q4gsw_distill_fwd(cuda(z), cuda(idx), cuda(t), temperature=T)
+    assert "tiles=1" not in m.q4gsw_last_route().split()
+    rows = slice(0, 4)
+    check(lse[rows], ol.distill_spread(z[rows], idx[rows], t[rows], T)[1], "lse")
+    m.q4gsw_device_error_check()

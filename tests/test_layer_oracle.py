@@ -89,3 +89,16 @@ def test_distillation_loss_is_zero_for_a_student_that_agrees():
     (loss, _), (lse, _), (g, _) = ol.distill(z, np.array([[3, 9, 12]]), t, 2.0, np.ones(1))
     assert abs(loss[0]) < 1e-12 and np.abs(g).max() < 1e-12
     assert abs(lse[0] - np.log(np.exp((t[0] + 5.0) / 2).sum())) < 1e-12
+
+
+def test_spread_bounds_do_not_grow_with_what_a_row_has_in_common():
+    rng = np.random.default_rng(7)
+    z, t = rng.integers(-9, 10, (4, 256)) / 4, rng.integers(-9, 10, (4, 12)) / 4      # exact after a shift, too
+    idx = np.stack([rng.permutation(256)[:12] for _ in range(4)]).astype(np.int32)
+    idx[1, 5:], idx[2, :] = -1, -1
+    c = rng.uniform(0.5, 2, 4)
+    near, far = (ol.distill_spread(z + s, idx, t + s, 0.5, c) for s in (0.0, 2.0 ** 14))
+    for a, b, what in zip(near, far, ("loss", "lse", "d_logits")):
+        if what != "lse":
+            assert np.abs(a[0] - b[0]).max() < 1e-9
+            assert np.abs(a[1] / b[1] - 1).max() < 1e-6, what

@@ -463,12 +463,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
       base = base_of(ref, c);
       scale = 1.f / mine.s;
       if (rank == 0 && entry_warp) {
-        // log of the sum against the maximum itself (its base was rounded); (ref -
-        // ref) is 0, or NaN where the row's maximum is not finite
+        // log of the sum against the maximum itself (its base was rounded)
         auto log_of = [&](const MaxSum& v) {
           return logf(v.s) - (is_huge(v.m, c) ? 0.f : fmaf(v.m, c, -base_of(v.m, c)) * kLn2);
         };
-        const float lse = fmaf(ref, inv_t, log_of(mine)) + (ref - ref);
+        // (ref - ref) is 0, or NaN where the row's maximum is not finite
+        const float log_sum = log_of(mine) + (ref - ref);
         float part = 0.f;
         if (has) {
           const float log_total = log_of(teach);
@@ -478,13 +478,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
             // a weight of zero adds nothing, whatever its token's logit (a NaN weight is added)
             if (e.id >= 0 && !(q == 0.f)) {
               const float z = j == (int)threadIdx.x ? z_own : logit_at<HALF>(row, e.id);
-              part += q * ((e.t - teach.m) * inv_t - log_total - z * inv_t + lse);
+              // both sides against their maxima: in lse itself a row far from zero has lost the
+              // fraction of its logarithm (1e-3 of the loss at logits around 2e4)
+              part += q * ((e.t - teach.m) * inv_t - log_total - (z - ref) * inv_t + log_sum);
             }
           }
         }
         part = lanes_sum<32>(part);
         if (lane == 0) s_loss[warp] = part;
-        if (threadIdx.x == 0) a.lse[m] = lse;
+        if (threadIdx.x == 0) a.lse[m] = fmaf(ref, inv_t, log_sum);
       }
     } else {
       ref = lse_saved * a.temperature;   // z / T - lse = (z - lse T) / T

@@ -49,3 +49,36 @@ def test_many_tiles_a_row_far_from_zero(M, V, offset):
     rows = slice(0, 4)
     check(lse[rows], ol.distill_spread(z[rows], idx[rows], t[rows], T)[1], "lse")
     m.q4gsw_device_error_check()
+
+
+@pytest.mark.parametrize("T", [0.5, 1.0, 1.7])
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("M,V,k", [(3, 1024, 8), (5, 32000, 64), (1, 262144, 200), (2, 32000, 1024)])
+def test_what_a_row_has_in_common_cancels_in_the_loss(M, V, k, offset, T):
+    """The loss is a difference of the two distributions; neither side's distance from zero is in it."""
+    m = q()
+    T = float(np.float32(T))
+    z, idx, t, d = shifted(M, V, k, offset, 23)
+    z[0] = np.float32(offset) - np.float32(30)
+    z[0, idx[0]] = t[0]                        # a student that agrees: a loss near zero
+    loss, lse = m.q4gsw_distill_fwd(cuda(z), cuda(idx), cuda(t), temperature=T)
+    want_loss, want_lse, _ = ol.distill_spread(z, idx, t, T)
+    check(lse, want_lse, "lse")
+    check(loss, want_loss, "loss")
+    loss, _, _ = m.q4gsw_distill_step(cuda(z), cuda(idx), cuda(t), cuda(d), temperature=T)
+    check(loss, want_loss, "loss of the step")
+
+
+def test_the_loss_of_a_row_masked_whole_by_the_lowest_value():
+    """Uniform over the vocabulary, although the row's log-sum-exp over T may pass the fp32 range."""
+    m = q()
+    V, k = 1024, 8
+    z = np.full((2, V), np.finfo(np.float32).min, np.float32)
+    idx = np.arange(2 * k, dtype=np.int32).reshape(2, k)
+    t = np.random.default_rng(24).standard_normal((2, k)).astype(np.float32)
+    for T in (0.5, 1.0, 2.0):
+        e = np.exp(t.astype(np.float64) / T)
+        p = e / e.sum(1, keepdims=True)
+        want = T * T * (p * (np.log(p) + np.log(V))).sum(1)
+        loss, _ = m.q4gsw_distill_fwd(cuda(z), cuda(idx), cuda(t), temperature=T)
+        assert np.abs(loss.cpu().numpy() - want).max() <= 2.0 ** -18 * T * T * np.log(V), T

@@ -223,6 +223,22 @@ __device__ __forceinline__ Entry entry_of(const DistillArgs& a, const RawEntry& 
   return {e.id, a.half_teacher ? __half2float(__ushort_as_half((unsigned short)e.bits)) : __uint_as_float(e.bits)};
 }
 
+// A step of two launches hands the log-sum-exp from the first to the second.  In
+// fp32 that is good for p while the row is near zero (about 4 |lse| 2^-24 of p, at
+// the limit 1.5e-5, a thirtieth of the fp16 rounding); of a row far from it the
+// fraction is lost, and one that is masked whole by the lowest value would have p =
+// 1 instead of 1 / V.  For such a row the first launch also leaves the pair itself,
+// where the gradient of each tile will stand: only that tile's CTA reads it there,
+// before it writes.  (A pair for every row: 2048 x 32000 in fp16 83.9 us instead of
+// 81.6, 891 x 73496 264 instead of 261; none at all 81.4 and 256.)
+constexpr float kNear = 64.f;
+__device__ __forceinline__ bool is_near(float lse) { return fabsf(lse) < kNear; }
+// The place for the tile that begins at vector `begin` (of E logits): 16-byte
+// aligned, 8 logits at least.
+__device__ __forceinline__ MaxSum* pair_of_tile(const DistillArgs& a, int m, int begin, int E) {
+  return reinterpret_cast<MaxSum*>(a.grad + (size_t)m * a.V + (size_t)begin * E);
+}
+
 // Rows (kLoss, kStep): grid = clusters of C CTAs (a power of two); cluster q
 // takes rows q, q + clusters, ...; CTA `rank` owns the vectors [rank VV / C, (rank
 // + 1) VV / C) of each (VV = V / E), in `tiles` tiles (kStep: one, which stays in
@@ -230,7 +246,9 @@ __device__ __forceinline__ Entry entry_of(const DistillArgs& a, const RawEntry& 
 // ... of the M x C tiles.  Dynamic shared memory: the next tile, two sets of k
 // teacher entries.
 enum Mode { kLoss, kStep, kGrad };
-template <int MODE, bool HALF>
+// PAIR: the two launches of a step (a run-time branch cost the loss and the
+// gradient alone 4 %).
+template <int MODE, bool HALF, bool PAIR>
 __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const DistillArgs a, int C, int tiles) {
   constexpr bool ROWS = MODE != kGrad, want_grad = MODE != kLoss;
   constexpr int E = HALF ? 8 : 4;         // logits per vector
@@ -348,6 +366,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
     const int m = slice.m;
     const char* row = row_of(m);
     const float coef = d_loss_ahead * a.temperature, lse_saved = lse_ahead;
+    MaxSum mine{0.f, 1.f};    // the row's pair (kGrad: of a row far from zero)
+    if (!ROWS && PAIR && !is_near(lse_saved)) mine = *pair_of_tile(a, m, slice.begin, E);
     int* ids = s_id + par * k4;
     float* ts = s_t + par * k4;
 
@@ -434,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
     if (!ROWS && it + step < items) issue(span_of(it + step, 0));
 
     // ---- the row's pair: every CTA's to every CTA of the cluster
-    MaxSum mine{0.f, 0.f};
     if (ROWS) {
       mine = lanes_total<kWarps>(s_warp[lane % kWarps], c);
       if (C > 1 && warp == kWarps - 1) {
@@ -486,8 +505,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
         }
         part = lanes_sum<32>(part);
         if (lane == 0) s_loss[warp] = part;
-        if (threadIdx.x == 0) a.lse[m] = fmaf(ref, inv_t, log_sum);
+        const float lse = fmaf(ref, inv_t, log_sum);
+        if (threadIdx.x == 0) a.lse[m] = lse;
+        if (MODE == kLoss && PAIR && warp == 0 && !is_near(lse))
+          for (int v = lane * TV; v < VV; v += 32 * TV) *pair_of_tile(a, m, v, E) = mine;
       }
+    } else if (PAIR && !is_near(lse_saved)) {
+      ref = mine.m;
+      base = base_of(ref, c);
+      scale = 1.f / mine.s;
     } else {
       ref = lse_saved * a.temperature;   // z / T - lse = (z - lse T) / T
       base = lse_saved * kLog2e;
@@ -595,10 +621,10 @@ struct DistillConfig {
   DistillConfig(const DistillConfig&) = delete;
 };
 
-// One instance: a mode, fp16 or fp32 logits.
-template <int MODE, bool HALF>
+// One instance: a mode, fp16 or fp32 logits, whether a pair per row goes from launch to launch.
+template <int MODE, bool HALF, bool PAIR>
 struct DistillKernel {
-  static auto kernel() { return distill::q4gsw_distill_kernel<MODE, HALF>; }
+  static auto kernel() { return distill::q4gsw_distill_kernel<MODE, HALF, PAIR>; }
 
   // bytes of the next tile, two sets of k teacher entries
   static size_t smem(int k) { return (size_t)distill::kTile * (HALF ? 2 : 4) + (size_t)((k + 3) & ~3) * 16; }
@@ -637,7 +663,7 @@ struct DistillKernel {
   }
 };
 
-template <int MODE, bool HALF>
+template <int MODE, bool HALF, bool PAIR>
 static cudaError_t distill_rows(const DistillArgs& a, cudaStream_t stream, char* route, int route_len) {
   using namespace distill;
   // CTAs per row.  The loss alone needs no row held: one CTA walks it, unless
@@ -655,24 +681,39 @@ static cudaError_t distill_rows(const DistillArgs& a, cudaStream_t stream, char*
   const int tiles = ((a.V / E + C - 1) / C * E + kTile - 1) / kTile;
   // one wave of clusters (a cluster that had to wait for a slot would start its
   // rows when the others end theirs)
-  const int most = DistillKernel<MODE, HALF>::clusters(C, a.k);
+  const int most = DistillKernel<MODE, HALF, PAIR>::clusters(C, a.k);
   const unsigned n = (unsigned)(a.M < most ? a.M : most);
   if (route)
     snprintf(route, route_len, "distill_%s launches=1 cluster=%d clusters=%u tiles=%d", MODE == kStep ? "step" : "fwd", C, n,
              tiles);
-  return DistillKernel<MODE, HALF>::launch(a, C, tiles, n * C, stream);
+  return DistillKernel<MODE, HALF, PAIR>::launch(a, C, tiles, n * C, stream);
 }
 
-cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
-                               int route_len) {
+template <bool HALF, bool PAIR>
+static cudaError_t distill_grad(const DistillArgs& a, cudaStream_t stream, char* route, int route_len) {
   using namespace distill;
   const int C = (a.V + kTile - 1) / kTile;
   const long long items = (long long)a.M * C;
   const int most = kPerSm * sm_count(current_device());
   const unsigned grid = (unsigned)(items < most ? items : most);
   if (route) snprintf(route, route_len, "distill_bwd launches=1 tiles=%d ctas=%u", C, grid);
-  return half_logits ? DistillKernel<kGrad, true>::launch(a, C, 1, grid, stream)
-                     : DistillKernel<kGrad, false>::launch(a, C, 1, grid, stream);
+  return DistillKernel<kGrad, HALF, PAIR>::launch(a, C, 1, grid, stream);
+}
+
+cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
+                               int route_len) {
+  return half_logits ? distill_grad<true, false>(a, stream, route, route_len)
+                     : distill_grad<false, false>(a, stream, route, route_len);
+}
+
+// The loss, then the gradient.
+template <bool HALF>
+static cudaError_t distill_step_in_two(DistillArgs a, cudaStream_t stream, char* route, int route_len) {
+  const cudaError_t e = distill_rows<distill::kLoss, HALF, true>(a, stream, nullptr, 0);
+  if (e != cudaSuccess) return e;
+  if (route) snprintf(route, route_len, "distill_step launches=2 fwd + bwd");
+  a.lse_in = a.lse;
+  return distill_grad<HALF, true>(a, stream, nullptr, 0);
 }
 
 cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
@@ -680,23 +721,15 @@ cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStre
   using namespace distill;
   // Loss and gradient in one pass for fp32 logits while a cluster of eight holds
   // the row and the teacher's list is short.  Otherwise the loss, then the
-  // gradient from its log-sum-exp.  Measured (us, one pass and two): 512 x 32000
+  // gradient.  Measured (us, one pass and two): 512 x 32000
   // with k = 64 25 and 36; 891 x 73496 with k = 319 317 and 168; fp16 logits, which
   // two passes move in 6 bytes instead of 4, 2048 x 32000 84 and 75.
-  if (a.grad && (half_logits || a.V > kHoldCluster * kTile || a.k > kThreads)) {
-    DistillArgs first = a, second = a;
-    first.grad = nullptr;
-    first.d_loss = nullptr;
-    second.lse_in = a.lse;
-    const cudaError_t e = half_logits ? distill_rows<kLoss, true>(first, stream, nullptr, 0)
-                                      : distill_rows<kLoss, false>(first, stream, nullptr, 0);
-    if (e != cudaSuccess) return e;
-    if (route) snprintf(route, route_len, "distill_step launches=2 fwd + bwd");
-    return launch_distill_bwd(second, half_logits, stream, nullptr, 0);
-  }
-  if (a.grad) return distill_rows<kStep, false>(a, stream, route, route_len);
-  return half_logits ? distill_rows<kLoss, true>(a, stream, route, route_len)
-                     : distill_rows<kLoss, false>(a, stream, route, route_len);
+  if (a.grad && (half_logits || a.V > kHoldCluster * kTile || a.k > kThreads))
+    return half_logits ? distill_step_in_two<true>(a, stream, route, route_len)
+                       : distill_step_in_two<false>(a, stream, route, route_len);
+  if (a.grad) return distill_rows<kStep, false, false>(a, stream, route, route_len);
+  return half_logits ? distill_rows<kLoss, true, false>(a, stream, route, route_len)
+                     : distill_rows<kLoss, false, false>(a, stream, route, route_len);
 }
 
 }  // namespace q4gsw

@@ -178,8 +178,12 @@ Q4GSW_API q4gsw_status q4gsw_distill_bwd(const void *logits, int half_logits, in
                                q4gsw_stream_t stream);
 
 /* Both at once, for a d_loss known beforehand: one launch that reads the
- * logits once (fp32 logits, V <= 65536, k <= 128), else the two launches above.  (Its
- * loss and lse are those of q4gsw_distill_fwd up to the order of the sums.) */
+ * logits once (fp32 logits, V <= 65536, k <= 128), else two that each read them.  (Its
+ * loss and lse are those of q4gsw_distill_fwd up to the order of the sums.)  The
+ * gradient does not depend on how far from zero a row is; that of
+ * q4gsw_distill_bwd carries the rounding of the saved lse, |lse| 2^-24 of p, and
+ * sees a row that is masked whole by the type's lowest value as lse rounds it
+ * (p = 1 for fp32, where this call gives 1 / V). */
 Q4GSW_API q4gsw_status q4gsw_distill_step(const void *logits, int half_logits, int M, int V,
                                 const int32_t *indices, const void *teacher, int half_teacher, int k,
                                 float temperature, const float *d_loss, float *loss, float *lse,

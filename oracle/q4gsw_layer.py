@@ -172,7 +172,7 @@ def distill(logits, indices, teacher, temperature, d_loss=None, lse_in=None):
     return (loss, b_loss), (lse, b_lse), grad
 
 
-def distill_spread(logits, indices, teacher, temperature, d_loss=None, lse_in=None):
+def distill_spread(logits, indices, teacher, temperature, d_loss=None, lse_in=None, two=False):
     """As ``distill``, with bounds that go by how far the logits of a row are from each other, not from zero: what a
     row has in common cancels in p and in the loss, and every value that an output is made of is held against the
     row's own maximum.  (The gradient from a saved ``lse_in`` is that of ``lse_in`` as it was saved.)
@@ -186,7 +186,9 @@ def distill_spread(logits, indices, teacher, temperature, d_loss=None, lse_in=No
       the teacher's weights: the same over at most 8 additions in a thread, 128;
       1 / sum, the products with coef and the difference p - q: 8, within the 128.
     A logarithm adds 2 of itself, a quotient by T and a sum 2 of theirs each.  From a saved lse the exponent is
-    z / T - lse: 8 of its size, and while |lse| < 180 another 8 of |z| / T + |lse|.
+    z / T - lse: 8 of its size, and while |lse| < 64 another 8 of |z| / T + |lse|.  ``two``: a step of two launches,
+    whose second takes a row with |lse| < 64 from the lse of the first: 2 of |z| / T, 3 of |lse| with its own
+    rounding and one of log V <= 15, altogether within 4 (|z| / T + |lse| + 4).
     """
     (loss, _), (lse, _), grad = distill(logits, indices, teacher, temperature, d_loss, lse_in)
     unit = 2.0 ** -24
@@ -220,10 +222,12 @@ def distill_spread(logits, indices, teacher, temperature, d_loss=None, lse_in=No
     d = grad[0]
     if lse_in is None:
         of_p = of_sum + 8 * s * unit
+        if two:
+            of_p = of_p + np.where(np.abs(lse[:, None]) < 64, 4 * (far(z) + np.abs(lse[:, None]) + 4), 0.0) * unit
     else:
         ref = np.asarray(lse_in, np.float64)[:, None]
         p = np.exp(z - ref)
-        near = np.where(np.abs(ref) < 180, far(z) + np.abs(ref), 0.0)
+        near = np.where(np.abs(ref) < 64, far(z) + np.abs(ref), 0.0)
         of_p = (16 + 8 * far(z - ref) + 8 * near) * unit
     coef = np.abs(np.asarray(d_loss, np.float64)[:, None] * temperature)
     err = p * of_p

@@ -82,3 +82,40 @@ def test_the_loss_of_a_row_masked_whole_by_the_lowest_value():
         want = T * T * (p * (np.log(p) + np.log(V))).sum(1)
         loss, _ = m.q4gsw_distill_fwd(cuda(z), cuda(idx), cuda(t), temperature=T)
         assert np.abs(loss.cpu().numpy() - want).max() <= 2.0 ** -18 * T * T * np.log(V), T
+
+
+TWO_LAUNCHES = [(3, 1024, 200, True), (5, 32000, 64, True), (2, 65544, 17, False), (3, 8200, 512, False),
+                (1, 262144, 20, True), (300, 16392, 8, True)]
+
+
+@pytest.mark.parametrize("T", [0.5, 1.7])
+@pytest.mark.parametrize("offset", [0.0, -2e4, 2e4])
+@pytest.mark.parametrize("M,V,k,half", TWO_LAUNCHES)
+def test_what_a_row_has_in_common_cancels_in_the_step_of_two_launches(M, V, k, half, offset, T):
+    m = q()
+    T = float(np.float32(T))
+    z, idx, t, d = shifted(M, V, k, offset, 25, dup=True)
+    z = z.astype(np.float16 if half else np.float32)
+    out = m.q4gsw_distill_step(cuda(z), cuda(idx), cuda(t), cuda(d), temperature=T)
+    assert "launches=2" in m.q4gsw_last_route()
+    rows = slice(0, 8)
+    want = ol.distill_spread(z[rows], idx[rows], t[rows], T, d[rows], two=True)
+    for got, ref, what in zip(out, want, ("loss", "lse", "d_logits")):
+        check(got[rows], ref, what)
+    m.q4gsw_device_error_check()
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("k", [8, 200])
+def test_the_step_on_a_row_masked_whole(half, k):
+    """All logits at the type's lowest value: uniform probabilities from one launch and from two."""
+    m = q()
+    V = 1024
+    z = np.full((2, V), np.finfo(np.float16 if half else np.float32).min, np.float16 if half else np.float32)
+    _, idx, t, _ = inputs(2, V, k, 26)
+    d = np.array([1.0, 512.0], np.float32)
+    for T in (0.5, 1.0, 2.0):
+        loss, _, g = m.q4gsw_distill_step(cuda(z), cuda(idx), cuda(t), cuda(d), temperature=T)
+        _, _, want = ol.distill_spread(np.zeros_like(z), idx, t, T, d)     # (the same probabilities)
+        check(g, want, "d_logits")
+        assert torch.isfinite(loss).all()

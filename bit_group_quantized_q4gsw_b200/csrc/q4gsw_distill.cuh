@@ -72,8 +72,8 @@ struct alignas(8) MaxSum {
 // maximum (2.9e-3 of p at logits around 2e4, T = 0.5).
 __device__ __forceinline__ bool is_huge(float m, float c) { return !(fabsf(m) * c < kHuge); }
 __device__ __forceinline__ float base_of(float m, float c) { return m == -INFINITY ? 0.f : __fmul_rn(m, c); }
-__device__ __forceinline__ float far_exponent(float x, float m, float c) {
-  return (x - (m == -INFINITY ? 0.f : m)) * c;
+__device__ __forceinline__ float far_exponent(float x, float m, float c, float m_low = 0.f) {
+  return ((x - (m == -INFINITY ? 0.f : m)) - m_low) * c;
 }
 __device__ __forceinline__ float exponent_of(float x, float m, float c) {
   return is_huge(m, c) ? far_exponent(x, m, c) : fmaf(x, c, -base_of(m, c));
@@ -470,7 +470,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
       teach = lanes_total<kWarps>(s_teach[par][lane % kWarps], c);
       inv_total = 1.f / teach.s;
     }
-    float ref, base, scale;   // p_i = 2^(z_i c - base) scale, base for ref
+    // p_i = 2^(z_i c - base) scale, base for ref; far from zero 2^((z_i - ref - ref_low) c) scale
+    float ref, base, scale, ref_low = 0.f;
+    bool far_lse = false;
+    auto far = [&] { return ROWS ? is_huge(ref, c) : far_lse; };
     if (ROWS) {
       if (C > 1) {
         // (out of time: s_abort and the device error word are set, the row's results are not valid)
@@ -514,10 +517,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
       ref = mine.m;
       base = base_of(ref, c);
       scale = 1.f / mine.s;
+      far_lse = is_huge(ref, c);
     } else {
-      ref = lse_saved * a.temperature;   // z / T - lse = (z - lse T) / T
+      // z / T - lse = (z - lse T) / T.  Here nothing cancels what rounding z c and the
+      // base changed (4 |lse| 2^-24 of p): far from zero the difference comes first,
+      // against lse T in two parts, and its rounding is one of the difference.
+      ref = __fmul_rn(lse_saved, a.temperature);
       base = lse_saved * kLog2e;
       scale = 1.f;
+      far_lse = !is_near(lse_saved);
+      if (far_lse && fabsf(ref) < INFINITY) ref_low = fmaf(lse_saved, a.temperature, -ref);
     }
 
     // ---- gradient: coef p for every token of the slice, then the teacher's tokens again
@@ -552,11 +561,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
       };
       if (!has) store([&](float, float) { return 0ull; });
       else if (MODE == kStep) store([&](float w0, float w1) { return mul2(pair(w0, w1), by2); });
-      else if (!is_huge(ref, c))
+      else if (!far())
         store([&](float z0, float z1) { return mul2(ex2_2(fma2(pair(z0, z1), c2, minus_base)), by2); });
       else
         store([&](float z0, float z1) {
-          return mul2(ex2_2(pair(far_exponent(z0, ref, c), far_exponent(z1, ref, c))), by2);
+          return mul2(ex2_2(pair(far_exponent(z0, ref, c, ref_low), far_exponent(z1, ref, c, ref_low))), by2);
         });
     }
     __syncthreads();
@@ -581,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
           for (int q = 0; q < k; ++q)
             if (ids[q] == id) t += ex2(exponent_of(ts[q], teach.m, c));
         }
-        const float p = ex2(is_huge(ref, c) ? far_exponent(z, ref, c) : fmaf(z, c, -base)) * scale;
+        const float p = ex2(far() ? far_exponent(z, ref, c, ref_low) : fmaf(z, c, -base)) * scale;
         grow[id] = __float2half_rn(coef * (p - t * inv_total));
       }
     }

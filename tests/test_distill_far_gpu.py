@@ -119,3 +119,17 @@ def test_the_step_on_a_row_masked_whole(half, k):
         _, _, want = ol.distill_spread(np.zeros_like(z), idx, t, T, d)     # (the same probabilities)
         check(g, want, "d_logits")
         assert torch.isfinite(loss).all()
+
+
+@pytest.mark.parametrize("T", [0.5, 1.0, 1.7])
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("M,V,k,half", [(3, 1024, 8, False), (5, 32000, 64, True), (2, 70000, 200, False)])
+def test_the_gradient_from_a_saved_log_sum_exp(M, V, k, half, offset, T):
+    """Of the log-sum-exp as it was saved, however far from zero it is."""
+    m = q()
+    T = float(np.float32(T))
+    z, idx, t, d = shifted(M, V, k, offset, 27, dup=True)
+    z = z.astype(np.float16 if half else np.float32)
+    _, lse = m.q4gsw_distill_fwd(cuda(z), cuda(idx), cuda(t), temperature=T)
+    g = m.q4gsw_distill_bwd(cuda(z), lse, cuda(idx), cuda(t), cuda(d), temperature=T)
+    check(g, ol.distill_spread(z, idx, t, T, d, lse.cpu().numpy())[2], "d_logits")

@@ -687,7 +687,7 @@ static cudaError_t distill_rows(const DistillArgs& a, cudaStream_t stream, char*
     while (C < kHoldCluster && (long long)C * kTile < a.V) C *= 2;
   while (C < kMaxCluster && (long long)a.M * C < (MODE == kStep ? sms : kPerSm * sms) && a.V / (2 * C) >= 2048) C *= 2;
   const int E = HALF ? 8 : 4;
-  const int tiles = ((a.V / E + C - 1) / C * E + kTile - 1) / kTile;
+  const int tiles = (int)(((a.V / E + C - 1LL) / C * E + kTile - 1) / kTile);   // (V may end at 2^31 - 8)
   // one wave of clusters (a cluster that had to wait for a slot would start its
   // rows when the others end theirs)
   const int most = DistillKernel<MODE, HALF, PAIR>::clusters(C, a.k);
@@ -701,7 +701,7 @@ static cudaError_t distill_rows(const DistillArgs& a, cudaStream_t stream, char*
 template <bool HALF, bool PAIR>
 static cudaError_t distill_grad(const DistillArgs& a, cudaStream_t stream, char* route, int route_len) {
   using namespace distill;
-  const int C = (a.V + kTile - 1) / kTile;
+  const int C = (a.V - 1) / kTile + 1;   // (V may end at 2^31 - 8)
   const long long items = (long long)a.M * C;
   const int most = kPerSm * sm_count(current_device());
   const unsigned grid = (unsigned)(items < most ? items : most);

@@ -133,3 +133,32 @@ def test_the_gradient_from_a_saved_log_sum_exp(M, V, k, half, offset, T):
     _, lse = m.q4gsw_distill_fwd(cuda(z), cuda(idx), cuda(t), temperature=T)
     g = m.q4gsw_distill_bwd(cuda(z), lse, cuda(idx), cuda(t), cuda(d), temperature=T)
     check(g, ol.distill_spread(z, idx, t, T, d, lse.cpu().numpy())[2], "d_logits")
+
+
+def test_the_longest_vocabulary():
+    """V = 2^31 - 8: the number of a row's tiles and every index within the row stay in 32 bits."""
+    m = q()
+    V = 2 ** 31 - 8
+    free, _ = torch.cuda.mem_get_info()
+    if free < 16 * 2 ** 30:
+        pytest.skip("needs 16 GB")
+    z = torch.zeros((1, V), dtype=torch.float16, device="cuda")
+    z[0, V - 2] = z[0, 5] = 8.0
+    idx = torch.tensor([[0, V - 1]], dtype=torch.int32, device="cuda")
+    t = torch.zeros((1, 2), device="cuda")
+    total = V - 2 + 2 * np.exp(8.0)
+    lse = torch.tensor([np.log(total)], dtype=torch.float32, device="cuda")
+    # d_loss 2^14: a token's gradient is a whole number of fp16 steps but for 3e-6 of it
+    d = torch.tensor([2.0 ** 14], device="cuda")
+    loss, lse2 = m.q4gsw_distill_fwd(z, idx, t)
+    assert abs(lse2.item() - np.log(total)) <= 2.0 ** -18 * np.log(total)
+    assert abs(loss.item() - (np.log(0.5) + np.log(total))) <= 2.0 ** -18 * np.log(total)
+    for g in (m.q4gsw_distill_bwd(z, lse, idx, t, d), m.q4gsw_distill_step(z, idx, t, d)[2]):
+        want = np.float16(2.0 ** 14 / total)
+        assert abs(2.0 ** 14 / total / float(want) - 1) < 1e-3
+        same = (g[0] == float(want)).sum().item()
+        assert same == V - 4
+        for i, p in ((0, 1 / total - 0.5), (V - 1, 1 / total - 0.5), (5, np.exp(8) / total), (V - 2, np.exp(8) / total)):
+            assert abs(g[0, i].item() - 2.0 ** 14 * p) <= 2.0 ** -10 * 2.0 ** 14 * abs(p), i
+        del g
+    m.q4gsw_device_error_check()

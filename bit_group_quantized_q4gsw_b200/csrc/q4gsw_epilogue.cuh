@@ -32,6 +32,17 @@ namespace q4gsw {
 // the value, far below the fp16 rounding of every result that uses it.
 __device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
+// A saved value that passed the fp16 range is an infinity; products of it with
+// the zeros that the activations reach there would be NaN.  2^42 stands for it:
+// act and act' have reached their limits, z^3 is in the fp32 range, and what is
+// multiplied by it rounds to an fp16 infinity from the least fp16 step on.  A NaN
+// stays, and finite fp16 values are not touched.
+__device__ __forceinline__ float within(float z) {
+  float v;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(v) : "f"(z), "f"(4398046511104.f));   // min of |z|, z's sign
+  return v;
+}
+
 // act(z) and, in `slope`, act'(z).
 //   silu       z s,  s = 1 / (1 + e^-z);           s (1 + z (1 - s))
 //   gelu_tanh  z s,  s = 1 / (1 + e^-2v) = (1 + tanh v) / 2,
@@ -42,6 +53,7 @@ __device__ __forceinline__ float act_value(float z, int act) {
   const float v = 0.7978845608028654f * fmaf(0.044715f * z * z, z, z);
   return z * sigmoid_f32(2.f * v);
 }
+// (of a finite z: `within` for saved values)
 __device__ __forceinline__ float act_value_slope(float z, int act, float& slope) {
   if (act == kActNone) {
     slope = 1.f;

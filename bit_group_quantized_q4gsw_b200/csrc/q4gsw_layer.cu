@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(kThreads) q4gsw_gated_grad_kernel(const __half
     for (int j = 0; j < 4; ++j) {
       const float2 v = __half22float2(u32_as_h2(pw[j]));   // (g, u)
       float slope;
-      const float a = act_value_slope(v.x, act, slope);
-      out[j] = h2_as_u32(__floats2half2_rn(d[j] * v.y * slope, d[j] * a));
+      const float a = act_value_slope(within(v.x), act, slope);
+      out[j] = h2_as_u32(__floats2half2_rn(d[j] * within(v.y) * slope, d[j] * a));
     }
     reinterpret_cast<uint4*>(d_gu)[i] = make_uint4(out[0], out[1], out[2], out[3]);
   }
@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(kThreads) q4gsw_act_grad_kernel(const __half* 
           for (int j = 0; j < 4; ++j) {
             const float2 f = __half22float2(u32_as_h2(zw[j]));
             float s0, s1;
-            act_value_slope(f.x, act, s0);
-            act_value_slope(f.y, act, s1);
+            act_value_slope(within(f.x), act, s0);
+            act_value_slope(within(f.y), act, s1);
             d[2 * j] *= s0;
             d[2 * j + 1] *= s1;
             out[j] = h2_as_u32(__floats2half2_rn(d[2 * j], d[2 * j + 1]));

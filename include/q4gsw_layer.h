@@ -87,6 +87,8 @@ Q4GSW_API q4gsw_status q4gsw_gated_fwd_f32s(const void *packed, int F, int K, in
  *         once; what an adapter on the gate or up projection trains from);
  *         d_gu may be gu itself;
  *   d_x   fp16 [M, K] = d_gu W.
+ * A g or u that was saved as an infinity (beyond the fp16 range) gives the limits:
+ * act and act' of it, and zero where d_h, act or act' is zero.
  */
 Q4GSW_API q4gsw_status q4gsw_gated_bwd(const void *packed, int F, int K, int group_size,
                              const uint16_t *gu, const uint16_t *d_h, int M, int act,
@@ -129,7 +131,8 @@ Q4GSW_API q4gsw_status q4gsw_linear_act_fwd_f32s(const void *packed, int N, int 
  *           d_y: pass NULL); d_z may be z or d_y itself
  *   d_bias  fp32 [N] or NULL (summed in fp32 before d_z is rounded); written
  *           as zeros when M == 0
- *   z       as saved by the forward; required with an activation, else NULL
+ *   z       as saved by the forward; required with an activation, else NULL (an
+ *           infinity gives the limit of act')
  */
 Q4GSW_API q4gsw_status q4gsw_linear_act_bwd(const void *packed, int N, int K, int group_size,
                                   const uint16_t *z, const uint16_t *d_y, int M, int act,

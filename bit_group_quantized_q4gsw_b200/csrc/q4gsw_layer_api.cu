@@ -95,7 +95,7 @@ q4gsw_status gated_bwd_impl(const void* packed, int F, int K, int gs, bool f32s,
   const Epi out{h(d_x), nullptr, nullptr, nullptr, K, kActNone, 0};
   char inner[128] = "", route[160];
   e = launch_product_epi(true, packed, 2 * F, K, gs, f32s, d_gu, M, out, stream, inner, sizeof(inner));
-  snprintf(route, sizeof(route), "gated launches=2 grad + %s", inner);
+  snprintf(route, sizeof(route), "gated grad launches=1 + %s", inner);   // every part counts its own
   set_route(route);
   return from_cuda(e);
 }
@@ -149,7 +149,7 @@ q4gsw_status act_bwd_impl(const void* packed, int N, int K, int gs, bool f32s, c
   char inner[128] = "", route[160];
   const cudaError_t e = launch_product_epi(true, packed, N, K, gs, f32s, has_act ? d_z : d_y, M, out, stream, inner,
                                            sizeof(inner));
-  snprintf(route, sizeof(route), "linear_act %s%s", grad ? "launches=2 grad + " : "", inner);
+  snprintf(route, sizeof(route), "linear_act %s%s", grad ? "grad launches=1 + " : "", inner);
   set_route(route);
   return from_cuda(e);
 }

@@ -39,3 +39,22 @@ def test_saved_values_beyond_the_fp16_range_give_the_limits_of_the_gradient():
             assert np.isfinite(d_u[0, 4])
             assert (d_g[1, :6] == 0).all() and (d_u[1, :6] == 0).all()
             assert np.isnan(d_g[0, 6:8]).all() and np.isnan(d_u[0, 6])
+
+
+def launches(route):
+    """The kernels of a call: every part of a route counts its own."""
+    return sum(int(w.split("=")[1]) for w in route.split() if w.startswith("launches="))
+
+
+def test_routes_count_every_launch():
+    m = q()
+    N, K, gs = 72, 128, 32
+    blob = m.q4gsw_prepack(*(cuda(a) for a in weight(N, K, gs, False, 41)), gs)
+    for M in (3, 40):
+        d = torch.randn(M, N, device="cuda").half()
+        z = torch.randn(M, N, device="cuda").half()
+        for want, f in ((1, lambda: m.q4gsw_linear_act_bwd(blob, N, K, gs, d)),
+                        (2, lambda: m.q4gsw_linear_act_bwd(blob, N, K, gs, d, want_bias=True)),
+                        (2, lambda: m.q4gsw_linear_act_bwd(blob, N, K, gs, d, z=z, act="silu"))):
+            f()
+            assert launches(m.q4gsw_last_route()) == want, m.q4gsw_last_route()

@@ -129,6 +129,8 @@ def q4gsw_prepack_gated(codes_gate, scales_gate, codes_up, scales_up, group_size
     nbytes = int((lib.q4gsw_packed_bytes_f32s if f32s else lib.q4gsw_packed_bytes)(2 * F, K, group_size))
     if packed is None:
         packed = _empty(max(nbytes, 1), dtype=_u8, device=index)
+    elif not isinstance(packed, torch.Tensor):
+        raise TypeError("packed must be a torch.Tensor")
     _call("q4gsw_prepack_gated_f32s" if f32s else "q4gsw_prepack_gated", index, cg, sg, cu, su, F, K, group_size,
           _need(packed, "packed", _u8, (packed.numel(),), index), packed.numel())
     return packed
@@ -184,7 +186,8 @@ def q4gsw_linear_act_fwd(packed, N: int, K: int, group_size: int, x, bias=None, 
 def q4gsw_linear_act_bwd(packed, N: int, K: int, group_size: int, d_y, z=None, act: str = "none", d_z=None, d_x=None,
                          d_bias=None, want_bias: bool = False, f32s: bool = False):
     """(d_x fp16 [M, K], d_z fp16 [M, N], d_bias fp32 [N]) from d_y fp16 [M, N] and, with an activation, z as
-    saved by the forward.  d_z is None without an activation (it is d_y then), d_bias unless asked for."""
+    saved by the forward.  d_z is None without an activation (it is d_y then), d_bias unless asked for (a buffer
+    for it is 16-byte aligned, like every other)."""
     code = _act(act)
     pd, M, index = _rows(d_y, "d_y", _f16, N)
     pw = _blob(packed, N, K, group_size, f32s, index)

@@ -181,3 +181,13 @@ def test_random_shapes(seed):
     finally:
         m.q4gsw_debug_pin_routes()
     m.q4gsw_device_error_check()
+
+
+def test_prepack_gated_refuses_what_is_no_tensor():
+    m = q()
+    c, s = (cuda(a) for a in weight(64, 128, 32, False, 49))
+    with pytest.raises(TypeError, match="packed"):
+        m.q4gsw_prepack_gated(c, s, c, s, 32, packed=bytearray(1 << 16))
+    with pytest.raises(m.Q4gswError) as e:
+        m.q4gsw_prepack_gated(c, s, c, s, 32, packed=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status_name == "Q4GSW_ERR_SIZE"

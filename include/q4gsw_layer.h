@@ -5,8 +5,8 @@
  *
  * Notation, statuses, alignment, streams and the packed weight are those of
  * q4gsw.h: M tokens, K input features, w[n,k] = (code[n,k] - 8) scale[k/gs, n],
- * device pointers on the current device, 16-byte aligned (arrays of 4-byte
- * words: 4-byte aligned), contiguous row-major, calls enqueue on `stream` and
+ * device pointers on the current device, 16-byte aligned (where less is enough
+ * it is said below), contiguous row-major, calls enqueue on `stream` and
  * return without waiting, arguments are checked on the host before anything
  * is enqueued, M == 0 enqueues nothing, repeated calls return the same bits.
  * No call allocates device memory or keeps anything between calls, so calls
@@ -71,7 +71,10 @@ Q4GSW_API q4gsw_status q4gsw_prepack_gated_f32s(const uint8_t *codes_gate, const
  *   gu  fp16 [M, 2 F] or NULL: the pairs (g_j, u_j) at columns 2 j, 2 j + 1,
  *       what the backward pass reads.
  * Error of h: that of g and u as in q4gsw_linear_fwd, carried through
- * act(g) u, plus one fp16 rounding.
+ * act(g) u, plus one fp16 rounding.  (As there, up to 16 tokens the codes are
+ * multiplied exactly; above, and in every input gradient below, the weight is
+ * the fp16 rounding of (code - 8) scale: 3.3e-4 of h in the 2-norm instead of
+ * 2.1e-4.)
  */
 Q4GSW_API q4gsw_status q4gsw_gated_fwd(const void *packed, int F, int K, int group_size,
                              const uint16_t *x, int M, int act, uint16_t *h, uint16_t *gu,
@@ -86,7 +89,7 @@ Q4GSW_API q4gsw_status q4gsw_gated_fwd_f32s(const void *packed, int F, int K, in
  *   d_gu  fp16 [M, 2 F], the pairs (d_g, d_u) in the columns of gu (rounded
  *         once; what an adapter on the gate or up projection trains from);
  *         d_gu may be gu itself;
- *   d_x   fp16 [M, K] = d_gu W.
+ *   d_x   fp16 [M, K] = d_gu W, of d_gu as rounded.
  * A g or u that was saved as an infinity (beyond the fp16 range) gives the limits:
  * act and act' of it, and zero where d_h, act or act' is zero.
  */
@@ -129,8 +132,8 @@ Q4GSW_API q4gsw_status q4gsw_linear_act_fwd_f32s(const void *packed, int N, int 
  *   d_x     fp16 [M, K]
  *   d_z     fp16 [M, N], required with an activation (with act NONE d_z is
  *           d_y: pass NULL); d_z may be z or d_y itself
- *   d_bias  fp32 [N] or NULL (summed in fp32 before d_z is rounded); written
- *           as zeros when M == 0
+ *   d_bias  fp32 [N] or NULL, 16-byte aligned like the others (summed in fp32
+ *           before d_z is rounded); written as zeros when M == 0
  *   z       as saved by the forward; required with an activation, else NULL (an
  *           infinity gives the limit of act')
  */
@@ -163,7 +166,7 @@ Q4GSW_API q4gsw_status q4gsw_linear_act_bwd_f32s(const void *packed, int N, int 
  *   1e-18 < T < 1e18 (Q4GSW_ERR_SHAPE else)
  * A row whose entries are all padding (or all -infinity) has loss 0 and a zero
  * gradient.  A student logit of -infinity has probability 0; a row of nothing
- * but -infinity, or with a NaN, gives NaN.  An id outside [0, V) that is not
+ * but -infinity, or with a NaN or +infinity, gives NaN.  An id outside [0, V) that is not
  * -1 cannot be seen on the host: the entry counts as padding and
  * q4gsw_device_error_check then returns Q4GSW_ERR_INDEX.
  * indices, teacher, loss, lse and d_loss need 4-byte alignment (an fp16 teacher 2).

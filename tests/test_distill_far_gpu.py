@@ -162,3 +162,16 @@ def test_the_longest_vocabulary():
             assert abs(g[0, i].item() - 2.0 ** 14 * p) <= 2.0 ** -10 * 2.0 ** 14 * abs(p), i
         del g
     m.q4gsw_device_error_check()
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_a_row_with_an_infinite_logit_is_nan_and_stays_alone(half):
+    m = q()
+    z, idx, t, d = inputs(3, 9000, 8, 28, half_logits=half)
+    clean = m.q4gsw_distill_step(cuda(z), cuda(idx), cuda(t), cuda(d))
+    z[1, 4000] = np.inf
+    out = m.q4gsw_distill_step(cuda(z), cuda(idx), cuda(t), cuda(d))
+    for a, b in zip(out, clean):
+        assert torch.isnan(a[1]).all() and torch.equal(a[[0, 2]], b[[0, 2]])
+    g = m.q4gsw_distill_bwd(cuda(z), out[1], cuda(idx), cuda(t), cuda(d))
+    assert torch.isnan(g[1]).all() and torch.isfinite(g[[0, 2]]).all()

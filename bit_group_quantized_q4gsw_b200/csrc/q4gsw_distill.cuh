@@ -7,16 +7,20 @@
 //   loss = T^2 sum_j q_j (log q_j - z[i_j] / T + lse)
 //   d_z[i] = d_loss T (exp(z_i / T - lse) - sum of q_j with i_j = i)
 //
-// The rows are long (V tokens) and each logit is used for one exponential, so
-// the kernels are streams: what they cost is the bytes of the logits and of the
-// gradient, provided enough of them are always in flight and little is issued
-// per logit.  Hence:
+// The rows are long (V tokens) and each logit is used for one exponential: streams,
+// whose floor is the bytes of the logits and of the gradient.  The gradient alone is
+// near it (45.6 us, floor 40.2, for 2048 x 32000 in fp16); the step is bound by each
+// row's chain of maximum, sum, exchange and gradient and by what it issues per logit
+// (23.5 us, floor 15.0, for 512 x 32000), the loss of a few long rows by launch and
+// latency (10.5 us, floor 5.9, for 37 x 262144).  So as many bytes as possible are
+// kept in flight and as little as possible is issued per logit:
 //  - a CTA of 128 threads keeps 64 logits of its part of a row in each thread's
 //    registers, and from the sum on their weights in their place, from which the
 //    gradient is a factor away: the logits cross the memory system once and each
 //    costs one exponential (with a second one for the gradient 27.3 us instead
-//    of 25.2 for the step of 512 x 32000); a cluster of up to eight CTAs holds a row of 65536
-//    tokens (longer rows take two launches and are read by both);
+//    of 25.2 for the step of 512 x 32000); a cluster of up to eight CTAs holds a row
+//    of 65536 tokens (longer rows take two launches and are read by both).  At 96
+//    registers, five CTAs an SM, the step spills 48 bytes a thread, the fp32 loss 12;
 //  - the launch holds as many CTAs as fit the SMs (five each) and each walks its
 //    rows.  While a row is reduced and its gradient written, the next row's
 //    logits, teacher entries and scalars are already on their way (cp.async
@@ -145,8 +149,7 @@ __device__ __forceinline__ void st_async_pair(uint32_t dst, MaxSum v, uint32_t b
                : "memory");
 }
 
-// Two fp32 operations in one instruction: the kernels are bound by what they
-// issue per logit.
+// Two fp32 operations in one instruction: what is issued per logit counts.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t v;
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
@@ -563,10 +566,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) q4gsw_distill_kernel(const D
       else if (MODE == kStep) store([&](float w0, float w1) { return mul2(pair(w0, w1), by2); });
       else if (!far())
         store([&](float z0, float z1) { return mul2(ex2_2(fma2(pair(z0, z1), c2, minus_base)), by2); });
-      else
+      else if (PAIR)   // rare: near the end of the fp32 range
         store([&](float z0, float z1) {
           return mul2(ex2_2(pair(far_exponent(z0, ref, c, ref_low), far_exponent(z1, ref, c, ref_low))), by2);
         });
+      else {   // the same, two at a time (2048 x 32000 around 200: 57.7 us instead of 60.1; PAIR would spill)
+        const float minus = ref == -INFINITY ? 0.f : -ref;
+        const uint64_t minus_ref = pair(minus, minus), minus_low = pair(-ref_low, -ref_low);
+        store([&](float z0, float z1) {
+          return mul2(ex2_2(mul2(add2(add2(pair(z0, z1), minus_ref), minus_low), c2)), by2);
+        });
+      }
     }
     __syncthreads();
     if (ROWS && rank == 0 && threadIdx.x == 0) {
@@ -730,9 +740,9 @@ cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStre
   using namespace distill;
   // Loss and gradient in one pass for fp32 logits while a cluster of eight holds
   // the row and the teacher's list is short.  Otherwise the loss, then the
-  // gradient.  Measured (us, one pass and two): 512 x 32000
-  // with k = 64 25 and 36; 891 x 73496 with k = 319 317 and 168; fp16 logits, which
-  // two passes move in 6 bytes instead of 4, 2048 x 32000 84 and 75.
+  // gradient.  Measured (us, one pass and two): 512 x 32000 with k = 64 25 and 36;
+  // 891 x 73496 with k = 319 317 and 169; fp16 logits, which two passes move in 6
+  // bytes instead of 4, 2048 x 32000 84 and 78.
   if (a.grad && (half_logits || a.V > kHoldCluster * kTile || a.k > kThreads))
     return half_logits ? distill_step_in_two<true>(a, stream, route, route_len)
                        : distill_step_in_two<false>(a, stream, route, route_len);

@@ -9,10 +9,11 @@
 // The epilogue adds no pass over memory: a projection followed by separate
 // bias, activation and residual passes writes and re-reads its fp32 result
 // (8 bytes an element) per pass; here each element is written once, in 2 bytes.
-// What it costs beside the plain fp32 product (us): a token of 2048 x 8192 6.9 and
-// 6.7, 16 tokens of 14336 x 4096 15.0 and 14.2 (bias and residual), 508 tokens of
-// 2048 x 8192 20.7 and 19.8, 512 tokens of 16384 x 2048 35.0 and 35.0, gated
-// there 31.2.
+// With it and the plain fp32 product (us, replayed back to back on the same buffers
+// at 1965 MHz): a token of 2048 x 8192 with residual 6.7 and 6.6; with bias and
+// residual 16 tokens of 14336 x 4096 13.8 and 13.7, 508 tokens of 2048 x 8192 19.8
+// and 19.5, 512 tokens of 16384 x 2048 30.0 and 33.6 (28.6 without either); gated
+// there 30.4.
 //
 // The gated block's weight interleaves its two matrices row by row (feature
 // 2 j = gate row j, 2 j + 1 = up row j; the packed layout already stores such
@@ -27,9 +28,10 @@
 
 namespace q4gsw {
 
-// 1 / (1 + e^-z).  e^-z overflows to infinity for z < -88 and the quotient is
-// then 0, its limit; the fast exponential and quotient are within 2^-21 of
-// the value, far below the fp16 rounding of every result that uses it.
+// 1 / (1 + e^-z).  The fast exponential is within (2 + 1.2 |z|) 2^-24 of its value
+// and the quotient within 2^-22: 2^-20 at |z| = 10, 2^-17 at the far end of the
+// negative side, still far below the fp16 rounding of every result that uses it.
+// Past a denominator of 2^126 (z < -87) the quotient is 0, its limit.
 __device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 // A saved value that passed the fp16 range is an infinity; products of it with

@@ -145,7 +145,8 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 // [16384, 2048] gated 35.0 -> 31.2, with bias and residual 48.2 -> 35.0 (each
 // thread had one residual load in flight); 4096 tokens on a gated 4096 x 14336
 // block 791 -> 753, of which 725 remain without this function (its exponentials
-// and quotients are 16 of the 28).
+// and quotients are 16 of the 28).  With two accumulators a CTA the kernel spills 16
+// bytes a thread here, once per output tile.
 template <int MSUB, int RING>
 __device__ __forceinline__ void epi_tiles(const Epi& o, const OutMaps<Epi>& maps, uint8_t* smem, SmemCtl* ctl,
                                           uint32_t tmem, int warp, int lane, int m0, int n0, int M, int cols,
@@ -621,7 +622,7 @@ static bool make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base
 // paid once).
 static double stage_time(int msub) { return msub == 2 ? 1.6 : 1.0; }
 // From the last wave of one launch to the first stage of the next, in the same
-// unit (from the case above that two launches make slower).
+// unit (from the case that two launches make slower, in gemm_variant).
 constexpr double kLaunchGap = 14.0;
 
 // Chooses the split-K factor S of one kernel variant (and its cost), and

@@ -7,10 +7,11 @@
 //
 // Both are streams of fp16: 10 bytes per gated feature (g, u, d_h in, two
 // gradients out), 6 per projected feature.  What they write the product that
-// follows reads back, and at training sizes it is still in L2 then.  They are
-// bound by DRAM, the small ones by filling its pipe: from cold caches 512 x 8192
-// gated features (42 MB) take 9.7 us, 1021 x 14336 (146 MB) 20.5 us, 256 x 14336
-// projected features (22 MB) 10.7 us.
+// follows reads back, and at training sizes it is still in L2 then.  From cold
+// caches 1021 x 14336 gated features (146 MB) take 19.8 us, bound by DRAM (66 % of
+// its rate, writes in L2 apart); 512 x 8192 (42 MB) 9.3 us and 256 x 14336 projected
+// features (22 MB) 10.6 us at 33 and 17 %, bound by the latency of one or two
+// dependent rounds of loads.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

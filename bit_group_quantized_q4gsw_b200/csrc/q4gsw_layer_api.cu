@@ -162,7 +162,8 @@ q4gsw_status distill_impl(DistillCall call, DistillArgs a, int half_logits, q4gs
   if (a.V % 8) return Q4GSW_ERR_ALIGN;   // 16-byte vectors of logits and of the gradient
   // T^2 and 1 / T are factors: both within the normal fp32 range (NaN fails, too)
   if (!(a.temperature > 1e-18f && a.temperature < 1e18f)) return Q4GSW_ERR_SHAPE;
-  // one CTA per row and tile of 8192 logits, or eight per row: a grid of at most 2^31 - 1
+  // one item per row and tile of 8192 logits must count in 32 bits (the grids are no
+  // larger than what is resident, up to 16 CTAs a row)
   const long long per_row = a.V / 8192 + 1 > 8 ? a.V / 8192 + 1 : 8;
   if (a.M > 0x7fffffffLL / per_row) return Q4GSW_ERR_SHAPE;
   if ((half_logits != 0 && half_logits != 1) || (a.half_teacher != 0 && a.half_teacher != 1))

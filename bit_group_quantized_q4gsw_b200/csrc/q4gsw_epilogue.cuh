@@ -28,9 +28,10 @@
 
 namespace q4gsw {
 
-// 1 / (1 + e^-z).  The fast exponential is within (2 + 1.2 |z|) 2^-24 of its value
-// and the quotient within 2^-22: 2^-20 at |z| = 10, 2^-17 at the far end of the
-// negative side, still far below the fp16 rounding of every result that uses it.
+// 1 / (1 + e^-z).  The fast exponential is within 2 + 1.2 |z| units in the last
+// place (at most 2^-23 of its value each) and the quotient within 2: 2^-19 at |z| =
+// 10, 2^-16 at the far end of the negative side, still far below the fp16 rounding of
+// every result that uses it.
 // Past a denominator of 2^126 (z < -87) the quotient is 0, its limit.
 __device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 

@@ -12,3 +12,7 @@ from .layer import (  # noqa: F401
     q4gsw_distill_bwd, q4gsw_distill_fwd, q4gsw_distill_step, q4gsw_gated_bwd, q4gsw_gated_fwd, q4gsw_linear_act_bwd,
     q4gsw_linear_act_fwd, q4gsw_prepack_gated,
 )
+from .adapters import (  # noqa: F401
+    GradSet, NormsGrad, q4gsw_adapters_bwd, q4gsw_adapters_fwd, q4gsw_adapters_plan, q4gsw_grad_clip, q4gsw_grad_norm,
+    q4gsw_grad_set, q4gsw_norms_bwd, q4gsw_norms_fwd,
+)

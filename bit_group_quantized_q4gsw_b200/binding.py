@@ -77,6 +77,27 @@ LAYER_SIGNATURES = [
     ("q4gsw_distill_step", _I, [_VP, _I, _I, _I, _VP, _VP, _I, _I, _F, _VP, _VP, _VP, _VP, _VP]),
 ]
 
+# the same for include/q4gsw_adapters.h (called from adapters.py)
+_AD_FWD = [_VP, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _VP, _I, _VP, _VP, _VP, _VP, _VP]
+_AD_BWD = [_VP, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _I, _VP, _VP, _VP, _I, _I, _VP, _VP, _VP, _VP, _VP]
+ADAPTER_SIGNATURES = [
+    ("q4gsw_adapters_plan_bytes", _SZ, [_I, _I]),
+    ("q4gsw_adapters_plan", _I, [_VP, _I, _I, _VP, _SZ, _VP]),
+    ("q4gsw_adapters_fwd", _I, _AD_FWD),
+    ("q4gsw_adapters_fwd_f32s", _I, _AD_FWD),
+    ("q4gsw_adapters_bwd", _I, _AD_BWD),
+    ("q4gsw_adapters_bwd_f32s", _I, _AD_BWD),
+    ("q4gsw_norms_fwd", _I, [_VP, _VP, _VP, _VP, _I, _F, _VP, _F, _F, _I, _I, _VP, _VP, _VP]),
+    ("q4gsw_norms_workspace_bytes", _SZ, [_I, _I]),
+    ("q4gsw_norms_bwd", _I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _F, _VP, _F, _F, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP,
+                             _VP, _SZ, _VP]),
+    ("q4gsw_grad_table_bytes", _SZ, [_I, _VP]),
+    ("q4gsw_grad_table", _I, [_I, _VP, _VP, _VP, _VP, _VP, _VP, _SZ]),
+    ("q4gsw_grad_workspace_bytes", _SZ, []),
+    ("q4gsw_grad_norm", _I, [_VP, _SZ, _I, _F, _VP, _VP, _SZ, _VP]),
+    ("q4gsw_grad_clip", _I, [_VP, _SZ, _I, _F, _F, _VP, _VP, _SZ, _VP]),
+]
+
 _lib = None
 
 
@@ -103,7 +124,7 @@ def library(path: str | None = None) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"q4gsw CUDA library not found at {path}; run `python -m bit_group_quantized_q4gsw_b200.build`")
     lib = ctypes.CDLL(path)
-    for name, res, args in SIGNATURES + LAYER_SIGNATURES:
+    for name, res, args in SIGNATURES + LAYER_SIGNATURES + ADAPTER_SIGNATURES:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

@@ -1,0 +1,57 @@
+// q4gsw_adapters.cuh - the plan of a batch over many adapters: its map in
+// device memory, shared by the kernel that writes it and those that read it.
+//
+// int32 words:
+//   head   [4]          tiles in use, 0, 0, 0
+//   first  [L + 2]      the sorted order's start of adapter a; of the tokens without
+//                       one (L); M (L + 1)
+//   order  [M]          the tokens, sorted by adapter, those without one last
+//   tile   [slots]      the adapter of each tile, kNoAdapter, or kNoTile past the last
+//   rows   [slots][16]  the tokens of each tile, -1 where it has fewer
+// (each part padded to 16 bytes).  The number of slots follows from M and L alone,
+// so that grids are known on the host: a group of c tokens has ceil(c / 16) tiles,
+// together at most (M + 15 g) / 16 for g = min(L + 1, M) groups.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+namespace q4gsw {
+namespace ma {
+
+constexpr int kTileRows = 16;
+constexpr int kMaxAdapters = 1024;
+constexpr int kMaxPlanTokens = 1 << 27;
+constexpr int kNoAdapter = -1;
+constexpr int kNoTile = -2;
+
+struct PlanView {
+  int32_t* head;
+  int32_t* first;
+  int32_t* order;
+  int32_t* tile;
+  int32_t* rows;
+};
+
+__host__ __device__ inline int plan_slots(int M, int L) {
+  const int g = L + 1 < M ? L + 1 : M;
+  return (int)(((long long)M + 15LL * g) / kTileRows);
+}
+__host__ __device__ inline size_t plan_pad(size_t words) { return (words + 3) / 4 * 4; }
+
+__host__ __device__ inline PlanView plan_view(int32_t* p, int M, int L) {
+  PlanView v;
+  v.head = p;
+  v.first = v.head + 4;
+  v.order = v.first + plan_pad((size_t)L + 2);
+  v.tile = v.order + plan_pad((size_t)M);
+  v.rows = v.tile + plan_pad((size_t)plan_slots(M, L));
+  return v;
+}
+__host__ __device__ inline size_t plan_words(int M, int L) {
+  const size_t s = (size_t)plan_slots(M, L);
+  return 4 + plan_pad((size_t)L + 2) + plan_pad((size_t)M) + plan_pad(s) + s * kTileRows;
+}
+
+}  // namespace ma
+}  // namespace q4gsw

@@ -840,6 +840,7 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
 #include "q4gsw_gemv_tma.cuh"
 #include "q4gsw_dq8ca_tma.cuh"
 #include "q4gsw_distill.cuh"
+#include "q4gsw_adapters_plan.cuh"
 
 namespace q4gsw {
 

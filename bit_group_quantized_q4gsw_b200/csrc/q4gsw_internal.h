@@ -168,6 +168,61 @@ cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStre
 cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
                                int route_len);
 
+// Adapters of many requests (q4gsw_adapters.cu; the plan: q4gsw_adapters.cuh).
+// down: out fp32 [M][r] = (scale) act P;  up: out fp16 [M][C] = res + scale inter P;
+// grad: out fp32 = (scale) sums over each adapter's tokens of act and q.  by_rows: the
+// adapters' matrices have the other operand's features as their rows' elements
+// (down: A [r, C]) or as their rows (up, grad: B [C, r]).
+struct AdaptersRef {
+  const int32_t* plan;
+  int L, r;
+};
+constexpr int kMaxAdapterFeatures = 64 * 65535;
+cudaError_t launch_adapters_plan(const int32_t* ids, int M, int L, void* plan, cudaStream_t stream);
+cudaError_t launch_adapters_down(const AdaptersRef& ad, const uint16_t* act, bool by_rows, const uint16_t* proj,
+                                 const float* scale, int M, int C, float* out, cudaStream_t stream);
+cudaError_t launch_adapters_up(const AdaptersRef& ad, const float* inter, bool by_rows, const uint16_t* proj,
+                               const float* scale, int M, int C, const uint16_t* res, uint16_t* out,
+                               cudaStream_t stream);
+cudaError_t launch_adapters_grad(const AdaptersRef& ad, const uint16_t* act, const float* q, bool by_rows,
+                                 const float* scale, int M, int C, bool accumulate, float* out, cudaStream_t stream);
+
+// The norms around a block (q4gsw_norms.cu).  Pointers as in q4gsw_norms_fwd / _bwd.
+struct NormsArgs {
+  const __half* h;        // forward: the stream; backward: the stream after the block
+  const __half* block;
+  const __half* w_post;
+  const __half* gate;
+  const __half* w_pre;
+  const __half* d_x;
+  const __half* d_h;
+  __half* h_out;          // forward; backward: d_residual
+  __half* x;              // forward; backward: d_block
+  __half* d_gate_rows;
+  float* d_w_pre;
+  float* d_w_post;
+  float* d_gate;
+  float* part;            // backward with sums over the rows: the workspace
+  float residual_scale, weight_offset, eps;
+  int gate_rows, M, D;
+};
+constexpr int kMaxNormFeatures = 32768;
+size_t norms_workspace_bytes(int M, int D);
+cudaError_t launch_norms_fwd(const NormsArgs& a, cudaStream_t stream, char* route, int route_len);
+cudaError_t launch_norms_bwd(const NormsArgs& a, cudaStream_t stream, char* route, int route_len);
+
+// Gradient lists (q4gsw_grads.cu): the table's bytes (0: too many pieces), its host
+// contents, and the two calls.
+size_t grad_table_bytes(int count, const int64_t* sizes);
+size_t grad_table_least(int count);   // of a list of empty tensors
+void grad_table_fill(int count, const void* const* grads, const int* half_grads, void* const* outs,
+                     const int* half_outs, const int64_t* sizes, void* table);
+size_t grad_workspace_bytes();
+cudaError_t launch_grad_norm(const void* table, size_t table_bytes, int count, float inv_scale, float* norm,
+                             void* workspace, cudaStream_t stream);
+cudaError_t launch_grad_clip(const void* table, size_t table_bytes, int count, float max_norm, float inv_scale,
+                             float* norm, void* workspace, cudaStream_t stream);
+
 // Embedding rows out[t] = dequant(W)[indices[t]] (fp32); an index outside
 // [0, N) gives a zero row and sets kIndexErrorBit in the device error word.
 cudaError_t launch_embedding(const void* packed, int N, int K, int gs, bool f32s, const int32_t* indices, int T, float* out,

@@ -113,7 +113,7 @@ q4gsw_status adapters_bwd_impl(const void* packed, int N, int K, int gs, bool f3
 }
 
 q4gsw_status check_norms(int M, int D, float residual_scale, float weight_offset, float eps) {
-  if (M < 0 || D <= 0 || D % 4 || D > kMaxNormFeatures) return Q4GSW_ERR_SHAPE;
+  if (M < 0 || M > kMaxNormRows || D <= 0 || D % 4 || D > kMaxNormFeatures) return Q4GSW_ERR_SHAPE;
   if (D % 8) return Q4GSW_ERR_ALIGN;   // 16-byte vectors
   if (!std::isfinite(residual_scale) || !std::isfinite(weight_offset) || !std::isfinite(eps) || eps < 0.f)
     return Q4GSW_ERR_SHAPE;

@@ -206,7 +206,7 @@ struct NormsArgs {
   float residual_scale, weight_offset, eps;
   int gate_rows, M, D;
 };
-constexpr int kMaxNormFeatures = 32768;
+constexpr int kMaxNormFeatures = 32768, kMaxNormRows = 1 << 30;
 size_t norms_workspace_bytes(int M, int D);
 cudaError_t launch_norms_fwd(const NormsArgs& a, cudaStream_t stream, char* route, int route_len);
 cudaError_t launch_norms_bwd(const NormsArgs& a, cudaStream_t stream, char* route, int route_len);

@@ -106,7 +106,7 @@ Q4GSW_API q4gsw_status q4gsw_adapters_bwd_f32s(const void *packed, int N, int K,
  *   x  = h' * rsqrt(mean(h'^2) + eps) * (weight_offset + w_pre)
  * gate is fp16 [D] (gate_rows 0, the same for every row) or [M, D] (1).
  * D > 0, D % 8 == 0 (Q4GSW_ERR_SHAPE below a multiple of 4, Q4GSW_ERR_ALIGN
- * else), D <= 32768; eps >= 0 and finite, as residual_scale and weight_offset
+ * else), D <= 32768, M <= 2^30; eps >= 0 and finite, as residual_scale and weight_offset
  * must be (Q4GSW_ERR_SHAPE).
  * ---------------------------------------------------------------------- */
 

@@ -83,7 +83,7 @@ def test_norms_arguments():
                                    n, None)
 
     inf, nan = float("inf"), float("nan")
-    for kw, st in ((dict(M=-1), SHAPE), (dict(D=0), SHAPE), (dict(D=62), SHAPE), (dict(D=60), ALIGN), (dict(D=32776), SHAPE),
+    for kw, st in ((dict(M=-1), SHAPE), (dict(M=(1 << 30) + 1), SHAPE), (dict(D=0), SHAPE), (dict(D=62), SHAPE), (dict(D=60), ALIGN), (dict(D=32776), SHAPE),
                    (dict(f=inf), SHAPE), (dict(o=nan), SHAPE), (dict(eps=-1.0), SHAPE), (dict(eps=nan), SHAPE),
                    (dict(rows=2), UNSUPPORTED), (dict(h=None), NULL), (dict(block=None), NULL), (dict(pre=None), NULL),
                    (dict(h=P + 8), ALIGN), (dict(block=P + 8), ALIGN), (dict(post=P + 2), ALIGN), (dict(gate=P + 2), ALIGN),

@@ -164,7 +164,7 @@ Q4GSW_API q4gsw_status q4gsw_norms_bwd(const uint16_t *h_out, const uint16_t *d_
  * grads[i] itself where the types agree, and outs may be NULL for the norm alone.  The table is plain
  * data: the caller copies it to the device (16-byte aligned) and keeps it as
  * long as the buffers stay where they are.  No two outs may overlap.
- * Q4GSW_ERR_SIZE for a table of more than 2^31 - 1 pieces of 8192 elements. */
+ * Q4GSW_ERR_SIZE for a table of more than 2^31 - 1 pieces of 1024 elements. */
 Q4GSW_API size_t q4gsw_grad_table_bytes(int count, const int64_t *sizes);
 Q4GSW_API q4gsw_status q4gsw_grad_table(int count, const void *const *grads, const int *half_grads, void *const *outs,
                               const int *half_outs, const int64_t *sizes, void *table, size_t table_bytes);

@@ -12,7 +12,24 @@ from typing import NamedTuple
 import torch
 
 from .binding import _check, library
-from .layer import _blob, _call, _empty, _f16, _f32, _i32, _need, _out, _rows, _u8
+from .layer import _blob, _call, _empty, _f16, _f32, _i32, _need, _rows, _u8
+
+_like = {}   # an empty tensor of each type and device: new tensors of its kind cost less than torch.empty
+
+
+def _new(shape, dtype, index: int):
+    t = _like.get((dtype, index))
+    if t is None:
+        t = _like[dtype, index] = _empty(0, dtype=dtype, device=index)
+    return t.new_empty(shape)
+
+
+def _out(t, name: str, dtype, shape, index: int):
+    """(tensor, pointer) of an output: the caller's buffer, or a new one."""
+    if t is None:
+        t = _new(shape, dtype, index)
+        return t, t.data_ptr()
+    return t, _need(t, name, dtype, shape, index)
 
 
 _plan_bytes = {}   # bytes of a plan by (M, L): a pure function of these
@@ -38,7 +55,7 @@ def q4gsw_adapters_plan(ids, L: int, plan=None):
     pi = _need(ids, "ids", _i32, (M,), index)
     nbytes = _plan_size(M, L)
     if plan is None:
-        plan = _empty(max(nbytes // 4, 4), dtype=_i32, device=index)
+        plan = _new(max(nbytes // 4, 4), _i32, index)
     _call("q4gsw_adapters_plan", index, pi, M, L, _need(plan, "plan", _i32, (plan.numel(),), index), 4 * plan.numel())
     return plan
 
@@ -105,6 +122,14 @@ def q4gsw_adapters_bwd(packed, N: int, K: int, group_size: int, plan, a, b, x, u
     return d_x, d_a, d_b
 
 
+def _out_like(t, name: str, like, index: int):
+    """The same for a tensor of another's type and shape (known to be contiguous)."""
+    if t is None:
+        t = torch.empty_like(like)
+        return t, t.data_ptr()
+    return t, _need(t, name, like.dtype, like.shape, index)
+
+
 def _norm_operands(M: int, D: int, index: int, block, w_post, gate, w_pre):
     if block is None and (w_post is not None or gate is not None):
         raise ValueError("without a block there is no w_post and no gate")
@@ -135,9 +160,9 @@ def q4gsw_norms_fwd(h, block=None, w_post=None, gate=None, residual_scale: float
             raise ValueError("without a block and w_pre there is nothing to compute")
         h_out = h
     else:
-        h_out, po = _out(h_out, "h_out", _f16, (M, D), index)
+        h_out, po = _out_like(h_out, "h_out", h, index)
     if w_pre is not None:
-        x, px = _out(x, "x", _f16, (M, D), index)
+        x, px = _out_like(x, "x", h, index)
     elif x is not None:
         raise ValueError("x needs w_pre")
     _call("q4gsw_norms_fwd", index, ph, pblock, ppost, pgate, rows, residual_scale, ppre, weight_offset, eps, M, D, po, px)
@@ -178,19 +203,27 @@ def q4gsw_norms_bwd(h_out, d_x=None, d_h=None, block=None, w_post=None, gate=Non
                                 ("d_w_pre", d_w_pre, w_pre)):
         if buffer is not None and there is None:
             raise ValueError(f"{name} has nothing that it would be the gradient of")
-    d_residual, pr = _out(d_residual, "d_residual", _f16, (M, D), index)
+    d_residual, pr = _out_like(d_residual, "d_residual", d, index)
     pdb = pgr = pg = pwo = pwe = pws = None
     nbytes = 0
     if block is not None:
-        d_block, pdb = _out(d_block, "d_block", _f16, (M, D), index)
+        d_block, pdb = _out_like(d_block, "d_block", d, index)
+    if want_weights:    # one allocation for the sums that have no buffer
+        want = [d_gate is None and gate is not None and not rows, d_w_post is None and w_post is not None,
+                d_w_pre is None and w_pre is not None]
+        if any(want):
+            new = iter(_new((sum(want), D), _f32, index).unbind())
+            d_gate = next(new) if want[0] else d_gate
+            d_w_post = next(new) if want[1] else d_w_post
+            d_w_pre = next(new) if want[2] else d_w_pre
     if rows:
-        d_gate, pgr = _out(d_gate, "d_gate", _f16, (M, D), index)
-    elif gate is not None and (want_weights or d_gate is not None):
-        d_gate, pg = _out(d_gate, "d_gate", _f32, (D,), index)
-    if w_post is not None and (want_weights or d_w_post is not None):
-        d_w_post, pwo = _out(d_w_post, "d_w_post", _f32, (D,), index)
-    if w_pre is not None and (want_weights or d_w_pre is not None):
-        d_w_pre, pwe = _out(d_w_pre, "d_w_pre", _f32, (D,), index)
+        d_gate, pgr = _out_like(d_gate, "d_gate", d, index)
+    elif d_gate is not None:
+        pg = _need(d_gate, "d_gate", _f32, (D,), index)
+    if d_w_post is not None:
+        pwo = _need(d_w_post, "d_w_post", _f32, (D,), index)
+    if d_w_pre is not None:
+        pwe = _need(d_w_pre, "d_w_pre", _f32, (D,), index)
     if pg or pwo or pwe:
         need = _norms_bytes.get((M, D))
         if need is None:
@@ -198,7 +231,7 @@ def q4gsw_norms_bwd(h_out, d_x=None, d_h=None, block=None, w_post=None, gate=Non
             if len(_norms_bytes) < 4096:
                 _norms_bytes[M, D] = need
         if workspace is None:
-            workspace = _empty(max(need, 16), dtype=_u8, device=index)
+            workspace = _new(max(need, 16), _u8, index)
         nbytes = workspace.numel()
         pws = _need(workspace, "workspace", _u8, (nbytes,), index)
     _call("q4gsw_norms_bwd", index, ph, pdx, pdh, pblock, ppost, pgate, rows, residual_scale, ppre, weight_offset, eps, M,
@@ -283,7 +316,7 @@ def _grad_call(name: str, grads: GradSet, head, norm, workspace):
         _grad_bytes = int(library().q4gsw_grad_workspace_bytes())
     norm, pn = _out(norm, "norm", _f32, (1,), grads.index)
     if workspace is None:
-        workspace = _empty(_grad_bytes, dtype=_u8, device=grads.index)
+        workspace = _new(_grad_bytes, _u8, grads.index)
     pw = _need(workspace, "workspace", _u8, (workspace.numel(),), grads.index)
     _call(name, grads.index, grads.table_ptr, grads.table_bytes, grads.count, *head, pn, pw, workspace.numel())
     return norm

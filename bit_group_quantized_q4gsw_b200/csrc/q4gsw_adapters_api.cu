@@ -59,14 +59,20 @@ q4gsw_status adapters_fwd_impl(const void* packed, int N, int K, int gs, bool f3
       !aligned16(residual) || !aligned16(y) || !aligned16(u) || !word(scale))
     return Q4GSW_ERR_ALIGN;
   const AdaptersRef ad{static_cast<const int32_t*>(plan), L, r};
-  cudaError_t e = launch_adapters_down(ad, x, true, a, nullptr, M, K, u, stream);
-  if (e == cudaSuccess) e = launch_adapters_up(ad, u, true, b, scale, M, N, residual, y, stream);
+  const bool low = adapters_low_fits(ad, M);
+  cudaError_t e;
+  if (low) {
+    e = launch_adapters_low(ad, true, x, a, b, scale, M, K, N, u, residual, y, stream);
+  } else {
+    e = launch_adapters_down(ad, x, true, a, nullptr, M, K, u, stream);
+    if (e == cudaSuccess) e = launch_adapters_up(ad, u, true, b, scale, M, N, residual, y, stream);
+  }
   char inner[128] = "", route[160];
   if (e == cudaSuccess) {
-    const Epi out{h(y), nullptr, h(bias), h(y), N, kActNone, 0};
+    const Epi out{h(y), nullptr, h(bias), h(y), N, kActNone, 0, 1};
     e = launch_product_epi(false, packed, N, K, gs, f32s, x, M, out, stream, inner, sizeof(inner));
   }
-  snprintf(route, sizeof(route), "adapters down launches=1 + up launches=1 + %s", inner);
+  snprintf(route, sizeof(route), "adapters %s + %s", low ? "low launches=1" : "down launches=1 + up launches=1", inner);
   set_route(route);
   return from_cuda(e);
 }
@@ -94,20 +100,22 @@ q4gsw_status adapters_bwd_impl(const void* packed, int N, int K, int gs, bool f3
     return Q4GSW_ERR_ALIGN;
   const AdaptersRef ad{static_cast<const int32_t*>(plan), L, r};
   char inner[128] = "", route[160];
-  cudaError_t e = launch_adapters_down(ad, d_y, false, b, scale, M, N, v, stream);
-  if (e == cudaSuccess && grads) {
-    e = launch_adapters_grad(ad, x, v, false, nullptr, M, K, accumulate != 0, d_a, stream);
-    if (e == cudaSuccess) e = launch_adapters_grad(ad, d_y, u, true, scale, M, N, accumulate != 0, d_b, stream);
+  const bool low = d_x && adapters_low_fits(ad, M);
+  cudaError_t e;
+  if (low) {
+    e = launch_adapters_low(ad, false, d_y, a, b, scale, M, K, N, v, nullptr, d_x, stream);
+  } else {
+    e = launch_adapters_down(ad, d_y, false, b, scale, M, N, v, stream);
+    if (e == cudaSuccess && d_x) e = launch_adapters_up(ad, v, false, a, nullptr, M, K, nullptr, d_x, stream);
   }
+  if (e == cudaSuccess && grads)
+    e = launch_adapters_grad(ad, x, v, d_a, K, d_y, u, scale, d_b, N, M, accumulate != 0, stream);
   if (e == cudaSuccess && d_x) {
-    e = launch_adapters_up(ad, v, false, a, nullptr, M, K, nullptr, d_x, stream);
-    if (e == cudaSuccess) {
-      const Epi out{h(d_x), nullptr, nullptr, h(d_x), K, kActNone, 0};
-      e = launch_product_epi(true, packed, N, K, gs, f32s, d_y, M, out, stream, inner, sizeof(inner));
-    }
+    const Epi out{h(d_x), nullptr, nullptr, h(d_x), K, kActNone, 0, 1};
+    e = launch_product_epi(true, packed, N, K, gs, f32s, d_y, M, out, stream, inner, sizeof(inner));
   }
-  snprintf(route, sizeof(route), "adapters down launches=1%s%s%s", grads ? " + grad launches=2" : "",
-           d_x ? " + up launches=1 + " : "", inner);
+  snprintf(route, sizeof(route), "adapters %s%s%s%s", low ? "low launches=1" : d_x ? "down launches=1 + up launches=1" : "down launches=1",
+           grads ? " + grad launches=1" : "", d_x ? " + " : "", inner);
   set_route(route);
   return from_cuda(e);
 }

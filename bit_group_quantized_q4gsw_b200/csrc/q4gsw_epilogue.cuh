@@ -73,6 +73,11 @@ __device__ __forceinline__ float act_value_slope(float z, int act, float& slope)
   return z * s;
 }
 
+// Whether a product reads its activations before it waits for the kernel in front.
+__device__ __forceinline__ bool reads_early(const OutSplit&) { return false; }
+__device__ __forceinline__ bool reads_early(const float*) { return false; }
+__device__ __forceinline__ bool reads_early(const Epi& o) { return o.early; }
+
 // ---------------------------------------------------------------- OutSplit
 // What an epilogue reads before it stores: nothing here.
 struct NoOperand {};

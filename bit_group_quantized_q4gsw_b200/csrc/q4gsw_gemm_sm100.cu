@@ -358,7 +358,7 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
         mbar_arrive_expect_tx(&ctl->full[it], A_STAGE + P_BYTES + args.sc_bytes);
         load_weights(it);
       }
-      griddep_wait();
+      if (!reads_early(args.out)) griddep_wait();
       for (int it = 0; it < pre; ++it) load_act(it);
       int issued = pre;
       for (int it = pre; it < nit; ++it) {

@@ -264,7 +264,7 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
         mbar_arrive_expect_tx(&ctl->full[it], it < nit ? tx : tx_ad);
         if (it < nit) load_weights(it);
       }
-      griddep_wait();
+      if (!reads_early(args.out)) griddep_wait();
       for (int it = 0; it < pre; ++it) load_act(it);
       int issued = pre;
       for (int it = pre; it < nitx; ++it) {

@@ -182,7 +182,7 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
         load_weights(it);
       }
       if (XS) {
-        griddep_wait();
+        if (!reads_early(out)) griddep_wait();
         for (int it = 0; it < pre; ++it) load_x(it);
       }
       int issued = pre;
@@ -199,7 +199,7 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
     }
   } else {
     // ------------------------------------------------------------ consumers
-    griddep_wait();   // outputs of this kernel may still be read by the previous one
+    if (!reads_early(out)) griddep_wait();   // outputs of this kernel may still be read by the previous one
     const int w = warp & 3;             // 64-column block of every stage
     const int rt0 = (warp >> 2) * RTW;  // first row tile of this warp
     // per-thread shared-memory offsets inside a stage: 16-byte code chunk t of
@@ -401,6 +401,7 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
         else out.y2[m * (out.N - out.n2) + (n - out.n2)] = v;
       }
     } else {
+      if (reads_early(out)) griddep_wait();   // the residual
       // pairs of features (N % 8 == 0: a pair is wholly inside or outside)
       for (int e = threadIdx.x; e < (te - tb) * 32; e += C::THREADS) {
         const int tok = tb + (e >> 5), nl = 2 * (e & 31);
@@ -523,7 +524,7 @@ q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
         mbar_arrive_expect_tx(&ctl->full[it], tx);
         load_weights(it);
       }
-      griddep_wait();   // d_out may come from the previous kernel of the stream
+      if (!reads_early(dx)) griddep_wait();   // d_out may come from the previous kernel of the stream
       for (int it = 0; it < pre; ++it) load_d(it);
       int issued = pre;
       for (int it = pre; it < nit; ++it) {
@@ -539,7 +540,7 @@ q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
     }
   } else {
     // ------------------------------------------------------------ consumers
-    griddep_wait();   // outputs may still be read by the previous kernel
+    if (!reads_early(dx)) griddep_wait();   // outputs may still be read by the previous kernel
     const int c = warp - 1;
     const int rowA = 8 * c + t, rowB = rowA + 4;   // pair rows of the stage
     const int J = g >> 2;                          // 64-column block of this lane
@@ -659,6 +660,7 @@ q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
         dx[(size_t)(tok0 + tok) * K + kbase + kl] = v;
       }
     } else {
+      if (reads_early(dx)) griddep_wait();   // the residual
       for (int e = tb * 128 + 2 * threadIdx.x; e < te * 128; e += 2 * kBwdThreads) {
         const int tok = e >> 7, kl = e & 127;
         if (kl >= kw) continue;   // kw is a multiple of 64

@@ -70,7 +70,10 @@ __host__ __device__ inline OutSplit single_output(float* y, int N) { return OutS
 //   gated   v = (g, u) pairs (weight rows interleaved): y[m, j] = act(g_j) u_j,
 //           z[m, 2 j] = g_j, z[m, 2 j + 1] = u_j
 //   else    z[m, n] = v + bias[n],  y[m, n] = act(z) + res[m, n]
-// bias, res and z may be null; y may be res.
+// bias, res and z may be null; y may be res.  early: the product's activations were
+// complete before the kernel in front of it could start (the first kernel behind them
+// lets its successors start only behind its own wait), so they are read at once and only
+// the epilogue waits for that kernel, which may still be writing the residual.
 enum ActKind { kActNone = 0, kActSilu = 1, kActGelu = 2 };
 struct Epi {
   __half* y;
@@ -80,6 +83,7 @@ struct Epi {
   int N;
   int act;
   int gated;
+  int early = 0;
 };
 
 // The compute launchers take f32s = the packed blob has fp32 scales (layout
@@ -170,9 +174,8 @@ cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStrea
 
 // Adapters of many requests (q4gsw_adapters.cu; the plan: q4gsw_adapters.cuh).
 // down: out fp32 [M][r] = (scale) act P;  up: out fp16 [M][C] = res + scale inter P;
-// grad: out fp32 = (scale) sums over each adapter's tokens of act and q.  by_rows: the
-// adapters' matrices have the other operand's features as their rows' elements
-// (down: A [r, C]) or as their rows (up, grad: B [C, r]).
+// grad: d_a = sums over each adapter's tokens of v^T x, d_b of scale d_y^T u, fp32.
+// by_rows: the adapters' matrices are [r, C] for down (A) and [C, r] for up (B).
 struct AdaptersRef {
   const int32_t* plan;
   int L, r;
@@ -184,8 +187,14 @@ cudaError_t launch_adapters_down(const AdaptersRef& ad, const uint16_t* act, boo
 cudaError_t launch_adapters_up(const AdaptersRef& ad, const float* inter, bool by_rows, const uint16_t* proj,
                                const float* scale, int M, int C, const uint16_t* res, uint16_t* out,
                                cudaStream_t stream);
-cudaError_t launch_adapters_grad(const AdaptersRef& ad, const uint16_t* act, const float* q, bool by_rows,
-                                 const float* scale, int M, int C, bool accumulate, float* out, cudaStream_t stream);
+// down and up in one launch, for few tiles (adapters_low_fits)
+bool adapters_low_fits(const AdaptersRef& ad, int M);
+cudaError_t launch_adapters_low(const AdaptersRef& ad, bool fwd, const uint16_t* act, const uint16_t* a,
+                                const uint16_t* b, const float* scale, int M, int K, int N, float* inter,
+                                const uint16_t* res, uint16_t* out, cudaStream_t stream);
+cudaError_t launch_adapters_grad(const AdaptersRef& ad, const uint16_t* x, const float* v, float* d_a, int K,
+                                 const uint16_t* d_y, const float* u, const float* scale, float* d_b, int N, int M,
+                                 bool accumulate, cudaStream_t stream);
 
 // The norms around a block (q4gsw_norms.cu).  Pointers as in q4gsw_norms_fwd / _bwd.
 struct NormsArgs {

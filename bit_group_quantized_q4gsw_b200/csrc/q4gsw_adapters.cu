@@ -93,9 +93,31 @@ __device__ __forceinline__ void load_bytes(uint32_t (&w)[(BYTES + 3) / 4], const
   }
 }
 
+// 16 bytes to shared memory, zeros where !in (nothing is read then).
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t shared_address(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Four 8 x 8 matrices of fp16: lanes 8 i .. 8 i + 7 give the rows of matrix i.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+
 // halves i of two registers: (lo.half[i], hi.half[i])
 __device__ __forceinline__ uint32_t pair_halves(uint32_t lo, uint32_t hi, int i) {
   return prmt(lo, hi, i ? 0x7632u : 0x5410u);
+}
+
+// The exponent k of a float's pattern (2^k <= |v| < 2^(k + 1)), held where 2^k and 2^-k
+// are both normal numbers.
+__device__ __forceinline__ int exponent_of(uint32_t bits) {
+  const int k = (int)(bits >> 23 & 255u) - 127;
+  return max(-126, min(k, 126));
 }
 
 // ---------------------------------------------------------------- down
@@ -180,21 +202,55 @@ __device__ __forceinline__ void down_park(const float (&acc)[RJ][4], float (*red
 }
 
 // out[m][j] = f sum_c act[m][c] P(c, j) for the tokens m of a tile, P and f (where scale
-// is given) of the tile's adapter.
+// is given) of the tile's adapter, for many tiles (few: q4gsw_adapters_low_kernel).
 //
-// A CTA has WT consecutive tiles, eight warps 8 / WT to a tile; the warps of a tile and
-// the KS CTAs of the cluster (grid = (slots / WT, KS)) split the contraction.  The
-// warps' sums are added in shared memory and the CTAs' through distributed shared
-// memory, both in a fixed order.  mma.sync m16n8k16: the work is bound by bytes (the
-// activations once, the adapter's matrix once a CTA, from L1 by the warps of its other
-// tiles) and by the latency of the loads.
-template <bool BY_ROWS, int RJ, int WT>
-__global__ void __launch_bounds__(kThreads)
+// A CTA has WT = 2 consecutive tiles (with four: 40 us in place of 29 at 4096 x 4096, rank
+// 64), eight warps 8 / WT to a tile.  Stages of 128 columns
+// of the tiles' tokens and of the matrix of one adapter go through a ring in shared
+// memory (cp.async), from which the warps take their fragments by ldmatrix: the matrix
+// is read once a CTA.  Tiles of several adapters take turns, one pass over the stages
+// each.  The warps of a tile and the KS CTAs of the cluster (grid = (slots / WT, KS))
+// split the contraction; sums go to fp32 registers stage by stage (the tensor cores
+// truncate theirs), and the warps' and the CTAs' are added in a fixed order.
+// tile[w] by a run-time w, without an array in local memory
+template <int WT>
+__device__ __forceinline__ int tile_of(const int (&tile)[WT], int w) {
+  int v = tile[0];
+#pragma unroll
+  for (int i = 1; i < WT; ++i) v = w == i ? tile[i] : v;
+  return v;
+}
+
+constexpr int kDownTiles = 2;
+template <bool BY_ROWS, int RJ>
+struct DownRing {
+  static constexpr int R = 8 * RJ, WT = kDownTiles, WK = kWarps / WT;
+  static constexpr int COLS = 128;                                   // columns of a stage
+  static constexpr int STAGES = 3;
+  // rows of 16-byte chunks, an odd number of them: ldmatrix meets no bank twice
+  static constexpr int X_PITCH = 2 * COLS + 16;
+  static constexpr int P_ROWS = BY_ROWS ? R : COLS;
+  static constexpr int P_CHUNKS = BY_ROWS ? COLS / 8 : RJ;           // of a row
+  static constexpr int P_PITCH = BY_ROWS ? X_PITCH : 16 * (RJ | 1);
+  static constexpr int X_BYTES = WT * kTileRows * X_PITCH, P_BYTES = P_ROWS * P_PITCH;
+  static constexpr int STAGE = X_BYTES + P_BYTES;
+  static constexpr int RED = kWarps * kTileRows * R * 4;             // reuses the ring
+  static constexpr int RECV = WT * kTileRows * R * 4;
+  static constexpr int RING = STAGES * STAGE > RED ? STAGES * STAGE : RED;
+  static constexpr int BYTES = RING + RECV;
+};
+
+template <bool BY_ROWS, int RJ>
+__global__ void __launch_bounds__(kThreads, 2)
 q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* scale, const int32_t* plan, float* out,
                            int M, int L, int C) {
-  constexpr int R = 8 * RJ, WK = kWarps / WT;
-  __shared__ float red[kWarps][kTileRows][R];
-  __shared__ float recv[WT][kTileRows][R];     // [sender][owned row] of each tile
+  using D = DownRing<BY_ROWS, RJ>;
+  constexpr int R = D::R, WT = D::WT, WK = D::WK;
+  extern __shared__ __align__(16) unsigned char down_smem[];
+  __shared__ int s_row[WT * kTileRows];
+  auto red = reinterpret_cast<float (*)[kTileRows][R]>(down_smem);             // [kWarps]
+  auto recv = reinterpret_cast<float (*)[kTileRows][R]>(down_smem + D::RING);   // [WT], [sender][owned row] of each
+  const uint32_t ring = shared_address(down_smem);
   griddep_wait();
   griddep_launch_dependents();     // behind the wait: what ran before has been written when the next kernel starts
   const PlanView P = plan_view(const_cast<int32_t*>(plan), M, L);
@@ -202,35 +258,108 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int slots = plan_slots(M, L), slot0 = blockIdx.x * WT;
-  const int slot = slot0 + warp / WK;
-  const int adapter = slot < slots ? ld_int(P.tile + slot) : kNoTile;
-  const int32_t* rows = P.rows + (size_t)slot * kTileRows;
+  int tile[WT];
+#pragma unroll
+  for (int w = 0; w < WT; ++w) tile[w] = slot0 + w < slots ? ld_int(P.tile + slot0 + w) : kNoTile;
   // tiles in use come first: where the first is unused, so is the whole cluster
-  if (WT == 1 ? adapter == kNoTile : ld_int(P.tile + slot0) == kNoTile) return;
+  if (tile[0] == kNoTile) return;
   if (KS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  float acc[RJ][4];
+  if (threadIdx.x < WT * kTileRows)
+    s_row[threadIdx.x] = slot0 + (int)threadIdx.x / kTileRows < slots
+                             ? ld_int(P.rows + (size_t)slot0 * kTileRows + threadIdx.x) : -1;
+  __syncthreads();
+  const int stages = (C + D::COLS - 1) / D::COLS;
+  const int it_begin = (int)((long long)ks * stages / KS), it_end = (int)((long long)(ks + 1) * stages / KS);
+  const int my_tile = warp / WK, my_part = warp % WK;
+  float total[RJ][4];
 #pragma unroll
   for (int j = 0; j < RJ; ++j)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
-  if (adapter >= 0) {
+    for (int e = 0; e < 4; ++e) total[j][e] = 0.f;
+  for (int run = 0; run < WT;) {
+    const int adapter = tile_of(tile, run);
+    int run_end = run + 1;
+    while (run_end < WT && tile_of(tile, run_end) == adapter) ++run_end;
+    if (adapter < 0) {
+      run = run_end;
+      continue;
+    }
     const __half* mat = proj + (size_t)adapter * R * C;
-    // rows that the tile lacks read its first (never stored)
-    const int ra = ld_int(rows + g), rb = ld_int(rows + g + 8), r0 = ld_int(rows);
-    const __half* a0 = act + (size_t)(ra < 0 ? r0 : ra) * C;
-    const __half* a1 = act + (size_t)(rb < 0 ? r0 : rb) * C;
-    const int chunks = (C + 63) / 64;   // C % 8 == 0: a group of 8 columns is wholly in or out
-    const int parts = KS * WK, part = ks * WK + warp % WK;
-    const int s_begin = (int)((long long)part * chunks / parts), s_end = (int)((long long)(part + 1) * chunks / parts);
-    down_chunks<BY_ROWS, RJ, (RJ <= 2 ? 2 : 1)>(mat, a0, a1, C, s_begin, s_end, g, t, acc);
+    auto issue = [&](int it) {
+      if (it < it_end) {
+        const uint32_t st = ring + (uint32_t)(it % D::STAGES) * D::STAGE;
+        const int c0 = it * D::COLS;
+        const int q = threadIdx.x % 16, c = c0 + 8 * q;         // C % 8 == 0: a chunk is wholly in or out
+#pragma unroll
+        for (int i = 0; i < WT; ++i) {
+          const int row = 16 * i + threadIdx.x / 16, m = s_row[row];
+          const bool in = i >= run && i < run_end && m >= 0 && c < C;
+          copy_16(st + row * D::X_PITCH + 16 * q, act + (in ? (size_t)m * C + c : 0), in);
+        }
+        const uint32_t sp = st + D::X_BYTES;
+        if constexpr (BY_ROWS) {
+          for (int row = threadIdx.x / 16; row < R; row += kThreads / 16)
+            copy_16(sp + row * D::P_PITCH + 16 * q, mat + (c < C ? (size_t)row * C + c : 0), c < C);
+        } else {
+          for (int e = threadIdx.x; e < D::P_ROWS * RJ; e += kThreads) {
+            const int row = e / RJ, k = e % RJ;
+            const bool in = c0 + row < C;
+            copy_16(sp + row * D::P_PITCH + 16 * k, mat + (in ? (size_t)(c0 + row) * R + 8 * k : 0), in);
+          }
+        }
+      }
+      cp_async_commit();
+    };
+    for (int i = 0; i < D::STAGES - 1; ++i) issue(it_begin + i);
+    for (int it = it_begin; it < it_end; ++it) {
+      cp_async_wait<D::STAGES - 2>();
+      __syncthreads();                     // the stage has landed, and the one refilled below has been used by all
+      issue(it + D::STAGES - 1);
+      if (my_tile < run || my_tile >= run_end) continue;
+      const uint32_t st = ring + (uint32_t)(it % D::STAGES) * D::STAGE;
+      // rows 0-7, 8-15 at columns 0-7, then both at columns 8-15 of a step of 16
+      const uint32_t xa = st + (my_tile * kTileRows + lane % 16) * D::X_PITCH + 16 * (lane / 16);
+      const uint32_t pa = st + D::X_BYTES;
+      float acc[RJ][4];
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D::COLS / 16 / WK; ++k) {
+        const int step = my_part * (D::COLS / 16 / WK) + k;
+        uint32_t af[4];
+        ldmatrix4(af, xa + 32 * step);
+#pragma unroll
+        for (int j = 0; j < RJ; j += 2) {
+          // ranks 8 j .. 8 j + 15 (the second eight repeat the first where RJ is odd)
+          uint32_t bf[4];
+          const int jr = j + 1 < RJ ? lane / 16 : 0;
+          if constexpr (BY_ROWS)
+            ldmatrix4(bf, pa + (8 * (j + jr) + lane % 8) * D::P_PITCH + 32 * step + 16 * (lane / 8 % 2));
+          else
+            ldmatrix4_trans(bf, pa + (16 * step + lane % 16) * D::P_PITCH + 16 * (j + jr));
+          const uint32_t b0[2] = {bf[0], bf[1]}, b1[2] = {bf[2], bf[3]};
+          mma_16816(acc[j], af, b0);
+          if (j + 1 < RJ) mma_16816(acc[j + 1 < RJ ? j + 1 : j], af, b1);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) total[j][e] += acc[j][e];
+    }
+    cp_async_wait<0>();
+    __syncthreads();                       // the ring is free
+    run = run_end;
   }
-  down_park<BY_ROWS, RJ>(acc, red[warp], g, t);
+  down_park<true, RJ>(total, red[warp], g, t);
   __syncthreads();
   // the sums of row `row` of tile `tile` over its warps; a tile without an adapter has zeros
-  auto own = [&](int tile, int row, int j) {
+  auto own = [&](int w0, int row, int j) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < WK; ++w) s += red[tile * WK + w][row][j];
+    for (int w = 0; w < WK; ++w) s += red[w0 * WK + w][row][j];
     return s;
   };
   const int owned = kTileRows / KS;      // rows of each tile that this CTA writes (KS is a power of two)
@@ -239,24 +368,23 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
     for (int e = threadIdx.x; e < WT * kTileRows * R; e += kThreads) {
-      const int tile = e / (kTileRows * R), row = e / R % kTileRows, j = e % R;
-      *cluster.map_shared_rank(&recv[tile][ks * owned + row % owned][j], row / owned) = own(tile, row, j);
+      const int w = e / (kTileRows * R), row = e / R % kTileRows, j = e % R;
+      *cluster.map_shared_rank(&recv[w][ks * owned + row % owned][j], row / owned) = own(w, row, j);
     }
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   for (int e = threadIdx.x; e < WT * owned * R; e += kThreads) {
-    const int tile = e / (owned * R), row = e / R % owned, j = e % R;
-    if (slot0 + tile >= slots) break;
-    const int m = ld_int(P.rows + (size_t)(slot0 + tile) * kTileRows + ks * owned + row);
+    const int w = e / (owned * R), row = e / R % owned, j = e % R;
+    const int m = s_row[w * kTileRows + ks * owned + row];
     if (m < 0) continue;
-    const int a = ld_int(P.tile + slot0 + tile);
-    float s = 0.f;
+    const int a = tile_of(tile, w);
+    float v = 0.f;
     if (KS > 1) {
-      for (int q = 0; q < KS; ++q) s += recv[tile][q * owned + row][j];
+      for (int q = 0; q < KS; ++q) v += recv[w][q * owned + row][j];
     } else {
-      s = own(tile, row, j);
+      v = own(w, row, j);
     }
-    out[(size_t)m * R + j] = a >= 0 && scale ? ld_f32(scale + a) * s : s;
+    out[(size_t)m * R + j] = a >= 0 && scale ? ld_f32(scale + a) * v : v;
   }
 }
 
@@ -298,10 +426,7 @@ struct UpTile {
       for (int e = 0; e < 4 * KT; ++e) top = fmaxf(top, fabsf(v[e]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // 2^k and 2^-k from the exponent bits, k kept where both are normal numbers;
-      // an infinite or NaN value stays what it is
-      int k = (int)(__float_as_uint(top) >> 23) - 127;
-      k = max(-126, min(k, 126));
+      const int k = exponent_of(__float_as_uint(top));     // an infinite or NaN value stays what it is
       const float down = __uint_as_float((uint32_t)(127 - k) << 23);
       back[h] = f * __uint_as_float((uint32_t)(127 + k) << 23);
 #pragma unroll
@@ -403,35 +528,154 @@ __device__ __forceinline__ void up_block(const __half* mat, const UpTile<RJ>& q,
   }
 }
 
+// The same for many tiles.  A CTA has four consecutive tiles, one to a warp, and a run
+// of column blocks, whose part of the matrix of up to two adapters goes through a ring
+// in shared memory: it is read once for 64 tokens, and its fragments come by ldmatrix (in
+// their natural order).  Tiles of more adapters take further passes over the blocks.
+// Sums are turned in shared memory, so that rows are read (the residual) and written in
+// whole lines.
+constexpr int kUpWarps = 4, kUpThreads = 32 * kUpWarps;
 template <bool BY_ROWS, int RJ>
-__global__ void __launch_bounds__(kThreads)
+struct UpRing {
+  static constexpr int R = 8 * RJ, KT = (RJ + 1) / 2;
+  static constexpr int STAGES = 3;
+  static constexpr int ROWS = BY_ROWS ? 64 : 16 * KT;                // rows of a block (ranks padded to 16)
+  static constexpr int CHUNKS = BY_ROWS ? 2 * KT : 8;                // 16-byte chunks of a row
+  static constexpr int PITCH = 16 * (CHUNKS + 1);                    // an odd number of them
+  static constexpr int REGION = ROWS * PITCH, STAGE = 2 * REGION;
+  static constexpr int T_PITCH = 72;                                 // of a warp's 16 x 64 sums, floats
+  static constexpr int BYTES = STAGES * STAGE + kUpWarps * kTileRows * T_PITCH * 4;
+};
+
+template <bool BY_ROWS, int RJ>
+__global__ void __launch_bounds__(kUpThreads, 4)
 q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* scale, const int32_t* plan,
-                         const __half* res, __half* out, int M, int L, int C, int tile_warps, int blocks_per_warp) {
-  constexpr int R = 8 * RJ;
+                         const __half* res, __half* out, int M, int L, int C, int blocks_per_cta) {
+  using U = UpRing<BY_ROWS, RJ>;
+  constexpr int R = U::R, KT = U::KT;
+  extern __shared__ __align__(16) unsigned char up_smem[];
   griddep_launch_dependents();
   griddep_wait();
   const PlanView P = plan_view(const_cast<int32_t*>(plan), M, L);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int slot = blockIdx.x * tile_warps + warp % tile_warps;
-  if (slot >= plan_slots(M, L)) return;
-  const int adapter = ld_int(P.tile + slot);
-  if (adapter == kNoTile) return;
-  const int blocks = (C + 63) / 64;
-  const int first = (blockIdx.y * (kWarps / tile_warps) + warp / tile_warps) * blocks_per_warp;
-  const int last = min(first + blocks_per_warp, blocks);
-  const int32_t* rows = P.rows + (size_t)slot * kTileRows;
-  const int m[2] = {ld_int(rows + g), ld_int(rows + g + 8)};
+  const int slots = plan_slots(M, L), slot0 = blockIdx.x * kUpWarps;
+  int tile[kUpWarps];
+#pragma unroll
+  for (int w = 0; w < kUpWarps; ++w) tile[w] = slot0 + w < slots ? ld_int(P.tile + slot0 + w) : kNoTile;
+  if (tile[0] == kNoTile) return;         // tiles in use come first
+  const int first = blockIdx.y * blocks_per_cta, last = min(first + blocks_per_cta, (C + 63) / 64);
+  const int mine = tile_of(tile, warp);
+  const int32_t* rows = P.rows + (size_t)(slot0 + warp) * kTileRows;
+  const int m[2] = {mine == kNoTile ? -1 : ld_int(rows + g), mine == kNoTile ? -1 : ld_int(rows + g + 8)};
   UpTile<RJ> q;
-  q.fill(adapter >= 0 && scale ? ld_f32(scale + adapter) : 1.f, [&](int h, int e, float& v0, float& v1) {
-    if (m[h] < 0 || adapter < 0) return;
-    const uint2 w = ld_v2(inter + (size_t)m[h] * R + UpTile<RJ>::rank_of(e, t));
+  // ranks 16 s + 2 t, + 1, + 8, + 9 of the lane in step s
+  q.fill(mine >= 0 && scale ? ld_f32(scale + mine) : 1.f, [&](int h, int e, float& v0, float& v1) {
+    if (m[h] < 0 || mine < 0) return;
+    const uint2 w = ld_v2(inter + (size_t)m[h] * R + 16 * (e / 4) + 4 * (e % 4) + 2 * t);
     v0 = __uint_as_float(w.x);
     v1 = __uint_as_float(w.y);
   });
-  const __half* mat = proj + (size_t)(adapter < 0 ? 0 : adapter) * R * C;
-  for (int b = first; b < last; ++b)
-    up_block<BY_ROWS, RJ>(mat, q, adapter >= 0, m, 64 * b, C, res, out, g, t);
+  // rows 4 k + lane / 8 of the tile, columns 8 (lane % 8) .. of a block: what the lane writes
+  int to[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) to[k] = mine == kNoTile ? -1 : ld_int(rows + 4 * k + lane / 8);
+  const uint32_t ring = shared_address(up_smem);
+  float* turn = reinterpret_cast<float*>(up_smem + U::STAGES * U::STAGE) + warp * kTileRows * U::T_PITCH;
+  auto write = [&](int b, bool sums) {
+    const int c = 64 * b + 8 * (lane % 8);
+    if (c >= C) return;                    // C % 8 == 0
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (to[k] < 0) continue;
+      const size_t at = (size_t)to[k] * C + c;
+      uint4 r = make_uint4(0u, 0u, 0u, 0u);
+      if (res) r = *reinterpret_cast<const uint4*>(res + at);
+      if (sums) {
+        // (the upper four of eight lanes read their halves in the other order: no bank twice)
+        const float* v = turn + (4 * k + lane / 8) * U::T_PITCH + 8 * (lane % 8);
+        const bool up = lane & 4;
+        const float4 p = *reinterpret_cast<const float4*>(v + (up ? 4 : 0)),
+                     q2 = *reinterpret_cast<const float4*>(v + (up ? 0 : 4));
+        const float4 v0 = up ? q2 : p, v1 = up ? p : q2;
+        const float2 r0 = __half22float2(u32_as_h2(r.x)), r1 = __half22float2(u32_as_h2(r.y)),
+                     r2 = __half22float2(u32_as_h2(r.z)), r3 = __half22float2(u32_as_h2(r.w));
+        r = make_uint4(h2_as_u32(__floats2half2_rn(v0.x + r0.x, v0.y + r0.y)),
+                       h2_as_u32(__floats2half2_rn(v0.z + r1.x, v0.w + r1.y)),
+                       h2_as_u32(__floats2half2_rn(v1.x + r2.x, v1.y + r2.y)),
+                       h2_as_u32(__floats2half2_rn(v1.z + r3.x, v1.w + r3.y)));
+      }
+      *reinterpret_cast<uint4*>(out + at) = r;
+    }
+  };
+  if (mine == kNoAdapter)                  // the residual, or zeros
+    for (int b = first; b < last; ++b) write(b, false);
+  // passes: two adapters of the tiles (sorted, those without one behind them) at a time
+  for (int run = 0; run < kUpWarps && tile_of(tile, run) >= 0;) {
+    const int a0 = tile_of(tile, run);
+    while (run < kUpWarps && tile_of(tile, run) == a0) ++run;
+    const int a1 = run < kUpWarps && tile_of(tile, run) >= 0 ? tile_of(tile, run) : a0;
+    while (run < kUpWarps && tile_of(tile, run) == a1) ++run;
+    const bool active = mine == a0 || mine == a1;
+    const uint32_t region = mine == a0 ? 0u : (uint32_t)U::REGION;
+    auto issue = [&](int b) {
+      if (b < last) {
+        const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE;
+        for (int e = threadIdx.x; e < U::ROWS * U::CHUNKS; e += kUpThreads) {
+          const int row = e / U::CHUNKS, k = e % U::CHUNKS;
+          // by rows: column 64 b + row, ranks 8 k ..; else rank row, columns 64 b + 8 k ..
+          const bool in = BY_ROWS ? 64 * b + row < C && k < RJ : row < R && 64 * b + 8 * k < C;
+          const size_t from = BY_ROWS ? (size_t)(64 * b + row) * R + 8 * k : (size_t)row * C + 64 * b + 8 * k;
+          const uint32_t to_smem = st + row * U::PITCH + 16 * k;
+          copy_16(to_smem, proj + (in ? (size_t)a0 * R * C + from : 0), in);
+          if (a1 != a0) copy_16(to_smem + U::REGION, proj + (in ? (size_t)a1 * R * C + from : 0), in);
+        }
+      }
+      cp_async_commit();
+    };
+    for (int i = 0; i < U::STAGES - 1; ++i) issue(first + i);
+    for (int b = first; b < last; ++b) {
+      cp_async_wait<U::STAGES - 2>();
+      __syncthreads();                     // the block has landed, and the one refilled below has been used by all
+      issue(b + U::STAGES - 1);
+      if (!active) continue;
+      const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE + region;
+      float acc[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+#pragma unroll
+      for (int s = 0; s < KT; ++s) {
+        uint32_t bf[4][4];                 // columns 16 i .. + 7 (indices 0-7, 8-15), then + 8 .. + 15
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (BY_ROWS)
+            ldmatrix4(bf[i], st + (16 * i + 8 * (lane / 16) + lane % 8) * U::PITCH + 32 * s + 16 * (lane / 8 % 2));
+          else
+            ldmatrix4_trans(bf[i], st + (16 * s + lane % 16) * U::PITCH + 32 * i + 16 * (lane / 16));
+        }
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t f[2] = {bf[i / 2][2 * (i % 2)], bf[i / 2][2 * (i % 2) + 1]};
+            mma_16816(acc[i], part ? q.hi[s] : q.lo[s], f);
+          }
+      }
+      __syncwarp();                        // the lanes have read the block before
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(turn + (g + 8 * h) * U::T_PITCH + 8 * i + 2 * t) =
+              make_float2(q.back[h] * acc[i][2 * h], q.back[h] * acc[i][2 * h + 1]);
+      __syncwarp();
+      write(b, true);
+    }
+    cp_async_wait<0>();
+    __syncthreads();                       // the ring is free
+  }
 }
 
 // ---------------------------------------------------------------- down and up in one
@@ -461,7 +705,7 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
   const int m[2] = {ld_int(rows + g), ld_int(rows + g + 8)};
   UpTile<RJ> q;
   const __half* up = mat_up + (size_t)(adapter < 0 ? 0 : adapter) * R * C_up;
-  const int blocks = (C_up + 63) / 64;
+  const int blocks = out ? (C_up + 63) / 64 : 0;      // without an output: the intermediate alone
   if (adapter >= 0) {
     if (KS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     // the first block's part of `up`'s matrix on its way to L2 meanwhile
@@ -534,28 +778,30 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
 // rows [c][r] (BY_ROWS: d_B [N, r]) or [r][c] (d_A [r, K]).  f the adapter's factor
 // (scale given) or 1.
 //
-// mma.sync m16n8k8 tf32, 16 ranks x 8 columns x 8 tokens: the activations are exact
-// in tf32, q goes in as two parts.  Column CW / 8 n + i of a block of CW columns is
-// column n of tensor-core tile i, so that a lane reads its columns of a token's row
-// as one vector, straight into the fragments.  A CTA has one block of columns of one
-// adapter; its warps take the tokens eight at a time in turn and their sums are added
-// in shared memory in a fixed order.
-__device__ __forceinline__ uint32_t to_tf32(float v) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ void mma_1688_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+// A CTA has W columns of one adapter, its warps CW each and all ranks.  Chunks of 32
+// tokens (their columns, and their rows of q) go through a ring in shared memory; each
+// rank's q of a chunk is divided by a power of two near its largest value and split
+// into two fp16 parts, once for all warps, and the chunk's sums are scaled back when
+// they are added to the fp32 registers: 2^-24 of the largest q of the chunk is lost, no
+// range, and the tensor cores' own sums are two steps long.  The Z CTAs of a cluster
+// take every Z-th chunk, and their sums are added through distributed shared memory in
+// rank order.
+constexpr int kChunk = 32;      // tokens
 
 template <int RJ>
 struct GradTile {
-  static constexpr int MT = (RJ + 1) / 2;          // tensor-core tiles of 16 ranks
-  static constexpr int CW = MT <= 2 ? 64 : 32;     // columns of a warp: at most 64 sums a lane
-  static constexpr int V = CW / 8;                 // columns of a lane
+  static constexpr int R = 8 * RJ, MT = (RJ + 1) / 2;                // tensor-core tiles of 16 ranks
+  static constexpr int CW = MT <= 2 ? 32 : 16;                       // columns of a warp
+  static constexpr int W = kWarps * CW;
+  static constexpr int STAGES = 3;
+  static constexpr int X_PITCH = 2 * W + 16;                         // an odd number of 16-byte chunks
+  static constexpr int X_BYTES = kChunk * X_PITCH, Q_BYTES = kChunk * R * 4;
+  static constexpr int STAGE = X_BYTES + Q_BYTES;
+  static constexpr int H_PITCH = 2 * 16 * MT + 16;                   // rows of the two parts, ranks padded to 16
+  static constexpr int H_BYTES = kChunk * H_PITCH;
+  static constexpr int SUMS = (W + 4) * R * 4 > W * (R + 4) * 4 ? (W + 4) * R * 4 : W * (R + 4) * 4;   // reuses the ring
+  static constexpr int RING = STAGES * STAGE > SUMS ? STAGES * STAGE : SUMS;
+  static constexpr int BYTES = RING + 2 * H_BYTES;
 };
 
 // One of the two gradients: the columns' activations and the other factor.
@@ -567,145 +813,193 @@ struct GradSide {
   int C;
 };
 
-// The CTA's sums in shared memory: rows of the output, padded by four values.
-template <int RJ, int TS>
-__host__ __device__ constexpr int grad_tile_floats() {
-  constexpr int W = kWarps / TS * GradTile<RJ>::CW, R = 8 * RJ;
-  return (W * (R + 4)) > (R * (W + 4)) ? W * (R + 4) : R * (W + 4);
-}
-
-template <bool BY_ROWS, int RJ, int TS>
-__device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P, int group, int accumulate, float* tile) {
+template <bool BY_ROWS, int RJ>
+__device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P, int group, int accumulate,
+                                           unsigned char* smem, unsigned int* s_top) {
   using T = GradTile<RJ>;
-  constexpr int R = 8 * RJ, MT = T::MT, CW = T::CW, V = T::V;
-  constexpr int CB = kWarps / TS;              // blocks of columns of the CTA
-  constexpr int W = CB * CW;
-  constexpr int PITCH = (BY_ROWS ? R : W) + 4;
+  constexpr int R = T::R, MT = T::MT, CW = T::CW, W = T::W;
+  constexpr int PITCH = (BY_ROWS ? R : W) + 4;        // of the sums in shared memory, floats
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int adapter = blockIdx.y;
+  const int adapter = blockIdx.y, Z = gridDim.z, z = blockIdx.z;
   const int base = W * group;
   const int begin = ld_int(P.first + adapter), end = ld_int(P.first + adapter + 1);
+  if (begin == end && accumulate) return;             // the whole cluster
   float* dst = a.out + (size_t)adapter * R * a.C;
-  const int split = warp / CB, block = warp % CB;
-  if (begin < end) {
-    float acc[MT][V][4];
+  const uint32_t ring = shared_address(smem), parts = ring + T::RING;
+  float* sums = reinterpret_cast<float*>(smem);
+  const int chunks = (end - begin + kChunk - 1) / kChunk;
+  const int mine = chunks > z ? (chunks - z + Z - 1) / Z : 0;      // chunks z, z + Z, ..
+  float total[MT][CW / 8][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < CW / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) total[m][i][k] = 0.f;
+  // the tokens whose rows this thread copies: rows threadIdx.x / XT + k of the columns,
+  // and of q; looked up a chunk ahead of their copies
+  constexpr int XC = W / 8, XT = kThreads / XC, XN = kChunk / XT;       // chunks of a row, rows at once, rounds
+  constexpr int QC = R / 4, QN = (kChunk * QC + kThreads - 1) / kThreads;
+  int xt[XN], qt[QN];
+  auto look_up = [&](int u) {
+    const int p0 = begin + (z + u * Z) * kChunk;
+#pragma unroll
+    for (int i = 0; i < XN; ++i) {
+      const int p = p0 + (int)threadIdx.x / XC + i * XT;
+      xt[i] = u < mine && p < end ? ld_int(P.order + p) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+      const int e = threadIdx.x + i * kThreads, p = p0 + e / QC;
+      qt[i] = u < mine && e < kChunk * QC && p < end ? ld_int(P.order + p) : -1;
+    }
+  };
+  auto issue = [&](int u) {
+    if (u < mine) {
+      const uint32_t st = ring + (uint32_t)(u % T::STAGES) * T::STAGE;
+      const int k = threadIdx.x % XC, c = base + 8 * k;
+#pragma unroll
+      for (int i = 0; i < XN; ++i) {
+        const bool in = xt[i] >= 0 && c < a.C;        // C % 8 == 0
+        copy_16(st + (threadIdx.x / XC + i * XT) * T::X_PITCH + 16 * k, a.act + (in ? (size_t)xt[i] * a.C + c : 0), in);
+      }
+#pragma unroll
+      for (int i = 0; i < QN; ++i) {
+        const int e = threadIdx.x + i * kThreads;
+        if (e < kChunk * QC)
+          copy_16(st + T::X_BYTES + 16 * e, a.q + (qt[i] >= 0 ? (size_t)qt[i] * R + 4 * (e % QC) : 0), qt[i] >= 0);
+      }
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < T::STAGES - 1; ++i) {
+    look_up(i);
+    issue(i);
+  }
+  look_up(T::STAGES - 1);
+  if (R % 16) {      // ranks past an odd eight stay zero in the parts
+    for (int e = threadIdx.x; e < 2 * kChunk * 8; e += kThreads)
+      *reinterpret_cast<__half*>(smem + T::RING + (e / 8) * T::H_PITCH + 2 * (R + e % 8)) = __float2half_rn(0.f);
+  }
+  for (int u = 0; u < mine; ++u) {
+    cp_async_wait<T::STAGES - 2>();
+    if (threadIdx.x < R) s_top[threadIdx.x] = 0u;
+    __syncthreads();                     // the chunk has landed; the parts and the stage refilled below have been used
+    issue(u + T::STAGES - 1);
+    look_up(u + T::STAGES);
+    const uint32_t st = ring + (uint32_t)(u % T::STAGES) * T::STAGE;
+    const float* q = reinterpret_cast<const float*>(smem + (u % T::STAGES) * T::STAGE + T::X_BYTES);
+    constexpr int N = kChunk * R / kThreads;       // RJ values of q a thread, of one rank where 256 is a multiple of R
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = q[threadIdx.x + i * kThreads];
+      // (patterns of non-negative floats are ordered as they are; a NaN is above all)
+      atomicMax(&s_top[(threadIdx.x + i * kThreads) % R], __float_as_uint(v[i]) & 0x7fffffffu);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      const float w = v[i] * __uint_as_float((uint32_t)(127 - exponent_of(s_top[e % R])) << 23);
+      const __half h = __float2half_rn(w);
+      unsigned char* at = smem + T::RING + (e / R) * T::H_PITCH + 2 * (e % R);
+      *reinterpret_cast<__half*>(at) = h;
+      *reinterpret_cast<__half*>(at + T::H_BYTES) = __float2half_rn(isinf(w) ? 0.f : w - __half2float(h));
+    }
+    __syncthreads();
+    float acc[MT][CW / 8][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < V; ++i)
+      for (int i = 0; i < CW / 8; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[m][i][k] = 0.f;
-    const int col = base + CW * block + V * g;
-    const bool in = col < a.C;        // C % 8 == 0, V is 4 or 8
-    // tokens of a step: rows t and t + 4 of this lane; the next step's are loaded
-    // before this one's products
-    float w[MT][4];
-    uint32_t x[2][V / 2];
-    int token[2];
-    auto index = [&](int p0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) token[h] = p0 + t + 4 * h < end ? ld_int(P.order + p0 + t + 4 * h) : -1;
-    };
-    auto load = [&] {
+    for (int k = 0; k < kChunk / 16; ++k) {
+      // columns: tokens 0-7, 8-15 of the step at columns 0-7, then at 8-15
+      uint32_t xf[CW / 16][4];
+#pragma unroll
+      for (int i = 0; i < CW / 16; ++i)
+        ldmatrix4_trans(xf[i], st + (16 * k + lane % 16) * T::X_PITCH + 2 * (CW * warp + 16 * i) + 16 * (lane / 16));
+#pragma unroll
+      for (int part = 1; part >= 0; --part)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          // ranks 0-7, 8-15 at tokens 0-7, then at 8-15
+          uint32_t af[4];
+          ldmatrix4_trans(af, parts + part * T::H_BYTES + (16 * k + 8 * (lane / 16) + lane % 8) * T::H_PITCH + 32 * m +
+                                  16 * (lane / 8 % 2));
+#pragma unroll
+          for (int i = 0; i < CW / 8; ++i) {
+            const uint32_t bf[2] = {xf[i / 2][2 * (i % 2)], xf[i / 2][2 * (i % 2) + 1]};
+            mma_16816(acc[m][i], af, bf);
+          }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int m = token[h];
+        const int j = 16 * m + 8 * h + g;
+        const float back = j < R ? __uint_as_float((uint32_t)(127 + exponent_of(s_top[j])) << 23) : 0.f;
 #pragma unroll
-        for (int b = 0; b < MT; ++b)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int j = 16 * b + g + 8 * k;
-            w[b][2 * h + k] = m >= 0 && j < R ? ld_f32(a.q + (size_t)m * R + j) : 0.f;
-          }
-        if (m >= 0 && in) {
-          load_bytes<2 * V>(x[h], a.act + (size_t)m * a.C + col);
-        } else {
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) x[h][i] = 0u;
+        for (int i = 0; i < CW / 8; ++i) {
+          total[m][i][2 * h] = fmaf(back, acc[m][i][2 * h], total[m][i][2 * h]);
+          total[m][i][2 * h + 1] = fmaf(back, acc[m][i][2 * h + 1], total[m][i][2 * h + 1]);
         }
       }
-    };
-    const int p_first = begin + 8 * split;
-    index(p_first);
-    load();
-    index(p_first + 8 * TS);
-    for (int p0 = p_first; p0 < end; p0 += 8 * TS) {
-      uint32_t hi[MT][4], lo[MT][4], now[2][V / 2];
-#pragma unroll
-      for (int b = 0; b < MT; ++b)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          hi[b][k] = to_tf32(w[b][k]);
-          lo[b][k] = to_tf32(w[b][k] - __uint_as_float(hi[b][k]));
-        }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) now[h][i] = x[h][i];
-      load();      // the next step's (nothing past the end)
-      index(p0 + 16 * TS);
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 f0 = __half22float2(u32_as_h2(now[0][i / 2])), f1 = __half22float2(u32_as_h2(now[1][i / 2]));
-          const uint32_t b0 = __float_as_uint(i % 2 ? f0.y : f0.x), b1 = __float_as_uint(i % 2 ? f1.y : f1.x);
-#pragma unroll
-          for (int b = 0; b < MT; ++b) mma_1688_tf32(acc[b][i], part ? hi[b] : lo[b], b0, b1);
-        }
-    }
-    // the splits' sums into the tile, one after another
-#pragma unroll 1
-    for (int s = 0; s < TS; ++s) {
-      if (split == s) {
-#pragma unroll
-        for (int b = 0; b < MT; ++b)
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int j = 16 * b + g + 8 * (k >> 1), c = CW * block + V * (2 * t + (k & 1)) + i;
-              if (j >= R) continue;
-              float* at = tile + (BY_ROWS ? c * PITCH + j : j * PITCH + c);
-              *at = s ? *at + acc[b][i][k] : acc[b][i][k];
-            }
-      }
-      __syncthreads();
-    }
-  } else if (accumulate) {
-    return;
+    __syncthreads();                     // every thread has read s_top
   }
+  cp_async_wait<0>();
+  __syncthreads();                       // the ring is free
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < CW / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = 16 * m + g + 8 * (k >> 1), c = CW * warp + 8 * i + 2 * t + (k & 1);
+        if (j < R) sums[BY_ROWS ? c * PITCH + j : j * PITCH + c] = total[m][i][k];
+      }
+  cg::cluster_group cluster = cg::this_cluster();
+  if (Z > 1) cluster.sync();
+  else __syncthreads();
   const float f = a.scale ? ld_f32(a.scale + adapter) : 1.f;
-  // rows of the output, four values a thread
-  for (int e = threadIdx.x; e < W * R / 4; e += kThreads) {
+  // rows of the output, four values a thread; the CTAs of a cluster take turns
+  for (int e = threadIdx.x + z * kThreads; e < W * R / 4; e += Z * kThreads) {
     const int row = BY_ROWS ? e / (R / 4) : e / (W / 4), x4 = BY_ROWS ? e % (R / 4) : e % (W / 4);
     if ((BY_ROWS ? base + row : base + 4 * x4) >= a.C) continue;
     float4* at = reinterpret_cast<float4*>(BY_ROWS ? dst + (size_t)(base + row) * R + 4 * x4
                                                    : dst + (size_t)row * a.C + base + 4 * x4);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (begin < end) {
-      v = *reinterpret_cast<const float4*>(tile + row * PITCH + 4 * x4);
-      v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
-      if (accumulate) {
-        const float4 o = *at;
-        v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
-      }
+    for (int k = 0; k < Z; ++k) {
+      const float* from = Z > 1 ? cluster.map_shared_rank(sums, k) : sums;
+      const float4 o = *reinterpret_cast<const float4*>(from + row * PITCH + 4 * x4);
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
+    if (accumulate) {
+      const float4 o = *at;
+      v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
     }
     *at = v;
   }
+  if (Z > 1) cluster.sync();             // no CTA leaves while another reads its sums
 }
 
-template <int RJ, int TS>
-__global__ void __launch_bounds__(kThreads)
+template <int RJ>
+__global__ void __launch_bounds__(kThreads, 2)
 q4gsw_adapters_grad_kernel(const GradSide da, const GradSide db, const int32_t* plan, int M, int L, int groups_a,
                            int accumulate) {
+  extern __shared__ __align__(16) unsigned char grad_smem[];
+  __shared__ unsigned int s_top[8 * RJ];
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ __align__(16) float tile[grad_tile_floats<RJ, TS>()];
   const PlanView P = plan_view(const_cast<int32_t*>(plan), M, L);
-  if ((int)blockIdx.x < groups_a) grad_block<false, RJ, TS>(da, P, blockIdx.x, accumulate, tile);
-  else grad_block<true, RJ, TS>(db, P, blockIdx.x - groups_a, accumulate, tile);
+  if ((int)blockIdx.x < groups_a) grad_block<false, RJ>(da, P, blockIdx.x, accumulate, grad_smem, s_top);
+  else grad_block<true, RJ>(db, P, blockIdx.x - groups_a, accumulate, grad_smem, s_top);
 }
 
 // The rank as a compile-time constant.
@@ -729,23 +1023,27 @@ static void serialize(cudaLaunchAttribute& a) {
 }
 
 template <bool BY_ROWS, int RJ>
-static cudaError_t down_tiles(cudaLaunchConfig_t& cfg, int wt, const __half* a, const __half* p, const float* scale,
-                              const AdaptersRef& ad, float* out, int M, int C) {
-  return wt == 1 ? cudaLaunchKernelEx(&cfg, ma::q4gsw_adapters_down_kernel<BY_ROWS, RJ, 1>, a, p, scale, ad.plan, out,
-                                      M, ad.L, C)
-                 : cudaLaunchKernelEx(&cfg, ma::q4gsw_adapters_down_kernel<BY_ROWS, RJ, 4>, a, p, scale, ad.plan, out,
-                                      M, ad.L, C);
+static cudaError_t down_form(cudaLaunchConfig_t& cfg, const __half* a, const __half* p, const float* scale,
+                             const AdaptersRef& ad, float* out, int M, int C) {
+  using D = ma::DownRing<BY_ROWS, RJ>;
+  auto kernel = ma::q4gsw_adapters_down_kernel<BY_ROWS, RJ>;
+  static PerDeviceOnce once;
+  const cudaError_t e = once_per_device(once, current_device(), [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, D::BYTES);
+  });
+  if (e != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = D::BYTES;
+  return cudaLaunchKernelEx(&cfg, kernel, a, p, scale, ad.plan, out, M, ad.L, C);
 }
 
 cudaError_t launch_adapters_down(const AdaptersRef& ad, const uint16_t* act, bool by_rows, const uint16_t* proj,
                                  const float* scale, int M, int C, float* out, cudaStream_t stream) {
   const int slots = ma::plan_slots(M, ad.L), sms = sm_count(current_device());
-  const int wt = slots >= 64 ? 4 : 1;
-  const int groups = (slots + wt - 1) / wt;
-  // contraction splits: about two CTAs per SM, a chunk of 64 columns per warp, clusters of at most 8
-  const int chunks = (C + 63) / 64;
+  const int groups = (slots + ma::kDownTiles - 1) / ma::kDownTiles;
+  // contraction splits: about two CTAs per SM, two stages each at least, clusters of at most 8
+  const int stages = (C + 127) / 128;
   int KS = 1;
-  while (KS < 8 && groups * KS < 2 * sms && chunks / (2 * KS) >= ma::kWarps / wt) KS *= 2;
+  while (KS < 8 && 2 * groups * KS <= 2 * sms && stages / (2 * KS) >= 2) KS *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(groups, KS, 1);
   cfg.blockDim = dim3(ma::kThreads, 1, 1);
@@ -760,27 +1058,39 @@ cudaError_t launch_adapters_down(const AdaptersRef& ad, const uint16_t* act, boo
   cfg.numAttrs = 2;
   const __half* a = reinterpret_cast<const __half*>(act);
   const __half* p = reinterpret_cast<const __half*>(proj);
-#define Q4_DOWN(RJ_)                                                               \
-  return by_rows ? down_tiles<true, RJ_>(cfg, wt, a, p, scale, ad, out, M, C)      \
-                 : down_tiles<false, RJ_>(cfg, wt, a, p, scale, ad, out, M, C)
+#define Q4_DOWN(RJ_)                                                            \
+  return by_rows ? down_form<true, RJ_>(cfg, a, p, scale, ad, out, M, C)        \
+                 : down_form<false, RJ_>(cfg, a, p, scale, ad, out, M, C)
   Q4_RANKS(ad.r / 8, Q4_DOWN)
 #undef Q4_DOWN
+}
+
+template <bool BY_ROWS, int RJ>
+static cudaError_t up_form(cudaLaunchConfig_t& cfg, const float* inter, const __half* p, const float* scale,
+                           const AdaptersRef& ad, const __half* res, __half* out, int M, int C, int per) {
+  using U = ma::UpRing<BY_ROWS, RJ>;
+  auto kernel = ma::q4gsw_adapters_up_kernel<BY_ROWS, RJ>;
+  static PerDeviceOnce once;
+  const cudaError_t e = once_per_device(once, current_device(), [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
+  });
+  if (e != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = U::BYTES;
+  return cudaLaunchKernelEx(&cfg, kernel, inter, p, scale, ad.plan, res, out, M, ad.L, C, per);
 }
 
 cudaError_t launch_adapters_up(const AdaptersRef& ad, const float* inter, bool by_rows, const uint16_t* proj,
                                const float* scale, int M, int C, const uint16_t* res, uint16_t* out,
                                cudaStream_t stream) {
-  const int slots = ma::plan_slots(M, ad.L), sms = sm_count(current_device());
-  int tile_warps = 1;
-  while (tile_warps < ma::kWarps && tile_warps < slots) tile_warps *= 2;
-  const int col_warps = ma::kWarps / tile_warps;
-  const int blocks = (C + 63) / 64, groups = (slots + tile_warps - 1) / tile_warps;
-  // blocks of columns of a warp, one after another: as many as leave four CTAs per SM
-  int per = (int)((long long)groups * blocks / col_warps / (4 * sms));
-  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  const int groups = (ma::plan_slots(M, ad.L) + ma::kUpWarps - 1) / ma::kUpWarps;
+  const int blocks = (C + 63) / 64;
+  // runs of blocks: four CTAs per SM
+  int runs = 4 * sm_count(current_device()) / groups;
+  runs = runs < 1 ? 1 : runs > blocks ? blocks : runs;
+  const int per = (blocks + runs - 1) / runs;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(groups, (blocks + col_warps * per - 1) / (col_warps * per), 1);
-  cfg.blockDim = dim3(ma::kThreads, 1, 1);
+  cfg.gridDim = dim3(groups, (blocks + per - 1) / per, 1);
+  cfg.blockDim = dim3(ma::kUpThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   serialize(attr[0]);
@@ -789,11 +1099,9 @@ cudaError_t launch_adapters_up(const AdaptersRef& ad, const float* inter, bool b
   const __half* p = reinterpret_cast<const __half*>(proj);
   const __half* rs = reinterpret_cast<const __half*>(res);
   __half* o = reinterpret_cast<__half*>(out);
-#define Q4_UP(RJ_)                                                                                                \
-  return by_rows ? cudaLaunchKernelEx(&cfg, ma::q4gsw_adapters_up_kernel<true, RJ_>, inter, p, scale, ad.plan, rs, o, \
-                                      M, ad.L, C, tile_warps, per)                                                \
-                 : cudaLaunchKernelEx(&cfg, ma::q4gsw_adapters_up_kernel<false, RJ_>, inter, p, scale, ad.plan, rs, o, \
-                                      M, ad.L, C, tile_warps, per)
+#define Q4_UP(RJ_)                                                              \
+  return by_rows ? up_form<true, RJ_>(cfg, inter, p, scale, ad, rs, o, M, C, per)  \
+                 : up_form<false, RJ_>(cfg, inter, p, scale, ad, rs, o, M, C, per)
   Q4_RANKS(ad.r / 8, Q4_UP)
 #undef Q4_UP
 }
@@ -852,13 +1160,26 @@ cudaError_t launch_adapters_low(const AdaptersRef& ad, bool fwd, const uint16_t*
 #undef Q4_LOW
 }
 
-template <int RJ, int TS>
-static cudaError_t grad_splits(cudaLaunchConfig_t& cfg, const AdaptersRef& ad, const ma::GradSide& da,
-                               const ma::GradSide& db, int M, bool accumulate) {
-  constexpr int W = ma::kWarps / TS * ma::GradTile<RJ>::CW;
-  const int ga = (da.C + W - 1) / W, gb = (db.C + W - 1) / W;
-  cfg.gridDim = dim3(ga + gb, ad.L, 1);
-  return cudaLaunchKernelEx(&cfg, ma::q4gsw_adapters_grad_kernel<RJ, TS>, da, db, ad.plan, M, ad.L, ga, (int)accumulate);
+template <int RJ>
+static cudaError_t grad_form(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, const AdaptersRef& ad,
+                             const ma::GradSide& da, const ma::GradSide& db, int M, bool accumulate) {
+  using T = ma::GradTile<RJ>;
+  auto kernel = ma::q4gsw_adapters_grad_kernel<RJ>;
+  static PerDeviceOnce once;
+  const cudaError_t e = once_per_device(once, current_device(), [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::BYTES);
+  });
+  if (e != cudaSuccess) return e;
+  const int ga = (da.C + T::W - 1) / T::W, gb = (db.C + T::W - 1) / T::W;
+  // token splits: about two CTAs per SM, two chunks each where the adapters have equal shares
+  int Z = 1;
+  while (Z < 8 && (long long)(ga + gb) * ad.L * Z < 2LL * sm_count(current_device()) &&
+         M / ad.L >= 4 * Z * ma::kChunk)
+    Z *= 2;
+  cfg.gridDim = dim3(ga + gb, ad.L, Z);
+  cfg.dynamicSmemBytes = T::BYTES;
+  attr->val.clusterDim.z = Z;
+  return cudaLaunchKernelEx(&cfg, kernel, da, db, ad.plan, M, ad.L, ga, (int)accumulate);
 }
 
 cudaError_t launch_adapters_grad(const AdaptersRef& ad, const uint16_t* x, const float* v, float* d_a, int K,
@@ -867,17 +1188,16 @@ cudaError_t launch_adapters_grad(const AdaptersRef& ad, const uint16_t* x, const
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(ma::kThreads, 1, 1);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   serialize(attr[0]);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const ma::GradSide da{reinterpret_cast<const __half*>(x), v, nullptr, d_a, K};
   const ma::GradSide db{reinterpret_cast<const __half*>(d_y), u, scale, d_b, N};
-  const int ts = M / ad.L >= 512 ? 8 : M / ad.L >= 128 ? 4 : 2;
-#define Q4_GRAD(RJ_)                                                        \
-  return ts == 8   ? grad_splits<RJ_, 8>(cfg, ad, da, db, M, accumulate)    \
-         : ts == 4 ? grad_splits<RJ_, 4>(cfg, ad, da, db, M, accumulate)    \
-                   : grad_splits<RJ_, 2>(cfg, ad, da, db, M, accumulate)
+#define Q4_GRAD(RJ_) return grad_form<RJ_>(cfg, &attr[1], ad, da, db, M, accumulate)
   Q4_RANKS(ad.r / 8, Q4_GRAD)
 #undef Q4_GRAD
 }

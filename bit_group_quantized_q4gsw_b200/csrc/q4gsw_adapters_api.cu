@@ -100,7 +100,7 @@ q4gsw_status adapters_bwd_impl(const void* packed, int N, int K, int gs, bool f3
     return Q4GSW_ERR_ALIGN;
   const AdaptersRef ad{static_cast<const int32_t*>(plan), L, r};
   char inner[128] = "", route[160];
-  const bool low = d_x && adapters_low_fits(ad, M);
+  const bool low = adapters_low_fits(ad, M);
   cudaError_t e;
   if (low) {
     e = launch_adapters_low(ad, false, d_y, a, b, scale, M, K, N, v, nullptr, d_x, stream);

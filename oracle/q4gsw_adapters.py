@@ -8,9 +8,11 @@ bound counts the roundings of the kernels' arithmetic:
   acc(n)  sums of n products in fp32 on the tensor cores or in registers: at most
           2^-23 of the absolute products a step (the tensor cores truncate), and
           not less than 64 steps;
-  SPLIT   2^-23 of a row's largest value: the two fp16 parts of the intermediate
-          (half a step of 2^-11 of 2^-11 of a value below two, and its neighbour);
-  TF32    2^-21 relative: the two tf32 parts (2^-12 of 2^-11) and the product;
+  SPLIT   2^-23 of the largest value of a token's row (in sums over ranks) or of a rank's
+          column (over tokens): the two fp16 parts of the intermediate over a power of
+          two with that value in [1, 2).  The first part is off by at most half a step,
+          2^-11, and the second, the rest, by half a step of a value below 2^-11: 2^-23;
+  SCALED  2^-21 relative: the products and the scaling back;
   STAT    2^-18 relative: a norm's factor.  At most 32 terms a thread, 5 shuffles
           and 32 warps are 69 roundings of 2^-24 in the sum of squares, half of
           that in its root, rsqrtf's 2^-22 and four products;
@@ -25,7 +27,7 @@ import numpy as np
 from .q4gsw_layer import HALF, TINY, _rounded, eps_of
 
 SPLIT = 2.0 ** -23
-TF32 = 2.0 ** -21
+SCALED = 2.0 ** -21
 STAT = 2.0 ** -18
 
 
@@ -102,9 +104,12 @@ def adapters_bwd(x, u, d_y, w, ids, a, b, scale=None):
         if not n:
             continue
         d_a[i] = v[at].T @ x[at]
-        e_a[i] = b_v[at].T @ np.abs(x[at]) + (TF32 + acc(n)) * ((np.abs(v[at]) + b_v[at]).T @ np.abs(x[at]))
+        top_v, top_u = (np.abs(v[at]) + b_v[at]).max(0), np.abs(u[at]).max(0)
+        e_a[i] = SPLIT * np.outer(top_v, np.abs(x[at]).sum(0))
+        e_a[i] += b_v[at].T @ np.abs(x[at]) + (SCALED + acc(n)) * ((np.abs(v[at]) + b_v[at]).T @ np.abs(x[at]))
         d_b[i] = f[i] * (d_y[at].T @ u[at])
-        e_b[i] = abs(f[i]) * (TF32 + acc(n)) * (np.abs(d_y[at]).T @ np.abs(u[at]))
+        e_b[i] = abs(f[i]) * SPLIT * np.outer(np.abs(d_y[at]).sum(0), top_u)
+        e_b[i] += abs(f[i]) * (SCALED + acc(n)) * (np.abs(d_y[at]).T @ np.abs(u[at]))
     return (d_x, _rounded(d_x, err)), (d_a, e_a), (d_b, e_b)
 
 

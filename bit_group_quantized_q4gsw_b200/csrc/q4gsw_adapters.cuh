@@ -2,7 +2,8 @@
 // device memory, shared by the kernel that writes it and those that read it.
 //
 // int32 words:
-//   head   [4]          tiles in use, 0, 0, 0
+//   head   [4]          tiles in use, M, L, kPlanMark: a kernel that is given a plan of
+//                       other sizes does nothing (its rows would lie outside the batch)
 //   first  [L + 2]      the sorted order's start of adapter a; of the tokens without
 //                       one (L); M (L + 1)
 //   order  [M]          the tokens, sorted by adapter, those without one last
@@ -24,6 +25,7 @@ constexpr int kMaxAdapters = 1024;
 constexpr int kMaxPlanTokens = 1 << 27;
 constexpr int kNoAdapter = -1;
 constexpr int kNoTile = -2;
+constexpr int kPlanMark = 0x6e616c70;
 
 struct PlanView {
   int32_t* head;

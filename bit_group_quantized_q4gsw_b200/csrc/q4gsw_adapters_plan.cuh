@@ -95,6 +95,9 @@ q4gsw_adapters_plan_kernel(const int32_t* ids, int M, int L, int32_t* plan) {
     P.first[L] = all_c;
     P.first[L + 1] = M;
     P.head[0] = all_t + none_tiles;
+    P.head[1] = M;
+    P.head[2] = L;
+    P.head[3] = kPlanMark;
     s_tile[L] = all_t;
     int at = all_c;
     for (int w = 0; w < kPlanWarps; ++w) {
@@ -131,6 +134,17 @@ q4gsw_adapters_plan_kernel(const int32_t* ids, int M, int L, int32_t* plan) {
 }
 
 }  // namespace ma
+
+// Address of the device error word on the current device, for kernels of other files.
+cudaError_t device_error_word(unsigned int** word) {
+  static PerDeviceOnce once;
+  static void* address[kMaxDevices];
+  const int dev = current_device();
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  const cudaError_t e = once_per_device(once, dev, [&] { return cudaGetSymbolAddress(&address[dev], g_device_error); });
+  *word = static_cast<unsigned int*>(address[dev]);
+  return e;
+}
 
 cudaError_t launch_adapters_plan(const int32_t* ids, int M, int L, void* plan, cudaStream_t stream) {
   const size_t smem = sizeof(int) * ((size_t)(ma::kPlanWarps + 1) * (L + 1));   // at most 135300 bytes

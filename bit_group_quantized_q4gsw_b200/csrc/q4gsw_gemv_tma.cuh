@@ -199,7 +199,11 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
     }
   } else {
     // ------------------------------------------------------------ consumers
-    if (!reads_early(out)) griddep_wait();   // outputs of this kernel may still be read by the previous one
+    // outputs of this kernel may still be read by the previous one; a product that reads
+    // early waits in its epilogue, and makes sure here that no older line of x is in L1
+    // (x by TMA comes from L2)
+    if (!reads_early(out)) griddep_wait();
+    else if (!XS) __threadfence();
     const int w = warp & 3;             // 64-column block of every stage
     const int rt0 = (warp >> 2) * RTW;  // first row tile of this warp
     // per-thread shared-memory offsets inside a stage: 16-byte code chunk t of

@@ -172,6 +172,9 @@ cudaError_t launch_distill_rows(const DistillArgs& a, bool half_logits, cudaStre
 cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStream_t stream, char* route,
                                int route_len);
 
+// The device error word (bits of q4gsw_device_error_check) of the current device.
+cudaError_t device_error_word(unsigned int** word);
+
 // Adapters of many requests (q4gsw_adapters.cu; the plan: q4gsw_adapters.cuh).
 // down: out fp32 [M][r] = (scale) act P;  up: out fp16 [M][C] = res + scale inter P;
 // grad: d_a = sums over each adapter's tokens of v^T x, d_b of scale d_y^T u, fp32.

@@ -131,15 +131,19 @@ def _out_like(t, name: str, like, index: int):
 
 
 def _norm_operands(M: int, D: int, index: int, block, w_post, gate, w_pre):
-    if block is None and (w_post is not None or gate is not None):
+    pblock = ppost = pgate = ppre = None
+    rows = 0
+    if block is not None:
+        pblock = _need(block, "block", _f16, (M, D), index)
+        if w_post is not None:
+            ppost = _need(w_post, "w_post", _f16, (D,), index)
+        if gate is not None:
+            rows = int(isinstance(gate, torch.Tensor) and gate.dim() == 2)
+            pgate = _need(gate, "gate", _f16, (M, D) if rows else (D,), index)
+    elif w_post is not None or gate is not None:
         raise ValueError("without a block there is no w_post and no gate")
-    pblock = None if block is None else _need(block, "block", _f16, (M, D), index)
-    ppost = None if w_post is None else _need(w_post, "w_post", _f16, (D,), index)
-    ppre = None if w_pre is None else _need(w_pre, "w_pre", _f16, (D,), index)
-    pgate, rows = None, 0
-    if gate is not None:
-        rows = int(isinstance(gate, torch.Tensor) and gate.dim() == 2)
-        pgate = _need(gate, "gate", _f16, (M, D) if rows else (D,), index)
+    if w_pre is not None:
+        ppre = _need(w_pre, "w_pre", _f16, (D,), index)
     return pblock, ppost, pgate, rows, ppre
 
 
@@ -151,8 +155,8 @@ def q4gsw_norms_fwd(h, block=None, w_post=None, gate=None, residual_scale: float
     residual_scale h, and h itself where that is 1 and no buffer is given; without w_pre x is None."""
     if not isinstance(h, torch.Tensor) or h.dim() != 2:
         raise ValueError("h must be a float16 tensor of 2 dims")
-    D = h.shape[1]
-    ph, M, index = _rows(h, "h", _f16, D)
+    (M, D), index = h.shape, h.get_device()
+    ph = _need(h, "h", _f16, (M, D), index)
     pblock, ppost, pgate, rows, ppre = _norm_operands(M, D, index, block, w_post, gate, w_pre)
     po = px = None
     if block is None and residual_scale == 1.0 and h_out is None:
@@ -191,39 +195,45 @@ def q4gsw_norms_bwd(h_out, d_x=None, d_h=None, block=None, w_post=None, gate=Non
     d = d_x if d_x is not None else d_h
     if not isinstance(d, torch.Tensor) or d.dim() != 2:
         raise ValueError("d_x or d_h must be a float16 tensor of 2 dims")
-    D = d.shape[1]
-    p, M, index = _rows(d, "d_x" if d_x is not None else "d_h", _f16, D)
+    (M, D), index = d.shape, d.get_device()
+    p = _need(d, "d_x" if d_x is not None else "d_h", _f16, (M, D), index)
     if (d_x is None) != (w_pre is None):
         raise ValueError("d_x and w_pre go together")
     pblock, ppost, pgate, rows, ppre = _norm_operands(M, D, index, block, w_post, gate, w_pre)
     pdx = None if d_x is None else p
     ph = None if d_x is None else _need(h_out, "h_out", _f16, (M, D), index)
-    pdh = None if d_h is None else _need(d_h, "d_h", _f16, (M, D), index)
-    for name, buffer, there in (("d_block", d_block, block), ("d_gate", d_gate, gate), ("d_w_post", d_w_post, w_post),
-                                ("d_w_pre", d_w_pre, w_pre)):
-        if buffer is not None and there is None:
-            raise ValueError(f"{name} has nothing that it would be the gradient of")
+    pdh = None if d_h is None else p if d_h is d else _need(d_h, "d_h", _f16, (M, D), index)
+    if (d_block is not None and block is None) or (d_gate is not None and gate is None) or \
+            (d_w_post is not None and w_post is None) or (d_w_pre is not None and w_pre is None):
+        raise ValueError("d_block, d_gate, d_w_post and d_w_pre are gradients of inputs that are there")
     d_residual, pr = _out_like(d_residual, "d_residual", d, index)
     pdb = pgr = pg = pwo = pwe = pws = None
     nbytes = 0
     if block is not None:
         d_block, pdb = _out_like(d_block, "d_block", d, index)
-    if want_weights:    # one allocation for the sums that have no buffer
-        want = [d_gate is None and gate is not None and not rows, d_w_post is None and w_post is not None,
-                d_w_pre is None and w_pre is not None]
-        if any(want):
-            new = iter(_new((sum(want), D), _f32, index).unbind())
-            d_gate = next(new) if want[0] else d_gate
-            d_w_post = next(new) if want[1] else d_w_post
-            d_w_pre = next(new) if want[2] else d_w_pre
     if rows:
         d_gate, pgr = _out_like(d_gate, "d_gate", d, index)
-    elif d_gate is not None:
-        pg = _need(d_gate, "d_gate", _f32, (D,), index)
-    if d_w_post is not None:
-        pwo = _need(d_w_post, "d_w_post", _f32, (D,), index)
-    if d_w_pre is not None:
-        pwe = _need(d_w_pre, "d_w_pre", _f32, (D,), index)
+    if want_weights or d_gate is not None or d_w_post is not None or d_w_pre is not None:
+        # the sums; one allocation for those that have no buffer
+        feature = gate is not None and not rows
+        new = want_weights and [t is None and there for t, there in (
+            (d_gate, feature), (d_w_post, w_post is not None), (d_w_pre, w_pre is not None))]
+        if new and any(new):
+            sums = _new((sum(new), D), _f32, index)
+            at, views = sums.data_ptr(), sums.unbind()
+            k = 0
+            if new[0]:
+                d_gate, pg, k = views[0], at, 1
+            if new[1]:
+                d_w_post, pwo, k = views[k], at + 4 * D * k, k + 1
+            if new[2]:
+                d_w_pre, pwe = views[k], at + 4 * D * k
+        if pg is None and feature and d_gate is not None:
+            pg = _need(d_gate, "d_gate", _f32, (D,), index)
+        if pwo is None and d_w_post is not None:
+            pwo = _need(d_w_post, "d_w_post", _f32, (D,), index)
+        if pwe is None and d_w_pre is not None:
+            pwe = _need(d_w_pre, "d_w_pre", _f32, (D,), index)
     if pg or pwo or pwe:
         need = _norms_bytes.get((M, D))
         if need is None:
@@ -231,9 +241,12 @@ def q4gsw_norms_bwd(h_out, d_x=None, d_h=None, block=None, w_post=None, gate=Non
             if len(_norms_bytes) < 4096:
                 _norms_bytes[M, D] = need
         if workspace is None:
-            workspace = _new(max(need, 16), _u8, index)
-        nbytes = workspace.numel()
-        pws = _need(workspace, "workspace", _u8, (nbytes,), index)
+            nbytes = max(need, 16)
+            workspace = _new(nbytes, _u8, index)
+            pws = workspace.data_ptr()
+        else:
+            nbytes = workspace.numel()
+            pws = _need(workspace, "workspace", _u8, (nbytes,), index)
     _call("q4gsw_norms_bwd", index, ph, pdx, pdh, pblock, ppost, pgate, rows, residual_scale, ppre, weight_offset, eps, M,
           D, pr, pdb, pgr, pwe, pwo, pg, pws, nbytes)
     return NormsGrad(d_residual, d_block, d_gate, d_w_post, d_w_pre)
@@ -245,7 +258,7 @@ class GradSet:
 
     def __init__(self, grads, outs, table, index: int):
         self.grads, self.outs, self.table, self.index = grads, outs, table, index
-        self.count, self.table_bytes, self.table_ptr = len(grads), table.numel(), table.data_ptr()
+        self.table_bytes, self.table_ptr = table.numel(), table.data_ptr()
 
 
 def _elements(t, name: str, index: int):
@@ -296,7 +309,7 @@ def q4gsw_grad_set(grads, outs=None) -> GradSet:
     sizes = i64(*(s[1] for s in src))
     lib = library()
     nbytes = int(lib.q4gsw_grad_table_bytes(n, sizes))
-    host = torch.empty(max(nbytes, 16), dtype=_u8)
+    host = torch.empty(max(nbytes, 1), dtype=_u8)
     _check("q4gsw_grad_table",
            lib.q4gsw_grad_table(n, ptrs(*(s[0] for s in src)), i32(*(s[2] for s in src)), ptrs(*(d[0] for d in dst)),
                                 i32(*(d[2] for d in dst)), sizes, host.data_ptr(), host.numel()))
@@ -317,8 +330,11 @@ def _grad_call(name: str, grads: GradSet, head, norm, workspace):
     norm, pn = _out(norm, "norm", _f32, (1,), grads.index)
     if workspace is None:
         workspace = _new(_grad_bytes, _u8, grads.index)
-    pw = _need(workspace, "workspace", _u8, (workspace.numel(),), grads.index)
-    _call(name, grads.index, grads.table_ptr, grads.table_bytes, grads.count, *head, pn, pw, workspace.numel())
+        pw, nbytes = workspace.data_ptr(), _grad_bytes
+    else:
+        nbytes = workspace.numel()
+        pw = _need(workspace, "workspace", _u8, (nbytes,), grads.index)
+    _call(name, grads.index, grads.table_ptr, grads.table_bytes, *head, pn, pw, nbytes)
     return norm
 
 

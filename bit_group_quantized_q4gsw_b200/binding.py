@@ -94,8 +94,8 @@ ADAPTER_SIGNATURES = [
     ("q4gsw_grad_table_bytes", _SZ, [_I, _VP]),
     ("q4gsw_grad_table", _I, [_I, _VP, _VP, _VP, _VP, _VP, _VP, _SZ]),
     ("q4gsw_grad_workspace_bytes", _SZ, []),
-    ("q4gsw_grad_norm", _I, [_VP, _SZ, _I, _F, _VP, _VP, _SZ, _VP]),
-    ("q4gsw_grad_clip", _I, [_VP, _SZ, _I, _F, _F, _VP, _VP, _SZ, _VP]),
+    ("q4gsw_grad_norm", _I, [_VP, _SZ, _F, _VP, _VP, _SZ, _VP]),
+    ("q4gsw_grad_clip", _I, [_VP, _SZ, _F, _F, _VP, _VP, _SZ, _VP]),
 ]
 
 _lib = None

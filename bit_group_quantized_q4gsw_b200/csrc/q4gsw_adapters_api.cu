@@ -315,41 +315,42 @@ q4gsw_status q4gsw_grad_table(int count, const void* const* grads, const int* ha
     }
     const size_t need = grad_table_bytes(count, sizes);
     if (need == 0 || table_bytes < need) return Q4GSW_ERR_SIZE;
-    grad_table_fill(count, grads, half_grads, outs, half_outs, sizes, table);
+    grad_table_fill(count, grads, half_grads, outs, half_outs, sizes, table, need);
     return Q4GSW_OK;
   });
 }
 
 size_t q4gsw_grad_workspace_bytes(void) { return grad_workspace_bytes(); }
 
-static q4gsw_status check_grad_call(const void* table, size_t table_bytes, int count, float inv_scale,
-                                    const float* norm, const void* workspace, size_t workspace_bytes) {
-  if (count < 1 || count > 65536 || !std::isfinite(inv_scale)) return Q4GSW_ERR_SHAPE;
+static q4gsw_status check_grad_call(const void* table, size_t table_bytes, float inv_scale, const float* norm,
+                                    const void* workspace, size_t workspace_bytes) {
+  if (!std::isfinite(inv_scale)) return Q4GSW_ERR_SHAPE;
   if (!table || !norm || !workspace) return Q4GSW_ERR_NULL;
   if (!aligned16(table) || !word(norm) || !aligned16(workspace)) return Q4GSW_ERR_ALIGN;
-  if (table_bytes < grad_table_least(count) || workspace_bytes < grad_workspace_bytes())
+  if (table_bytes < kGradRecordBytes || table_bytes % kGradRecordBytes || table_bytes / kGradRecordBytes > 0x7fffffff ||
+      workspace_bytes < grad_workspace_bytes())
     return Q4GSW_ERR_SIZE;
   return Q4GSW_OK;
 }
 
-q4gsw_status q4gsw_grad_norm(const void* table, size_t table_bytes, int count, float inv_scale, float* norm,
-                             void* workspace, size_t workspace_bytes, q4gsw_stream_t stream) {
+q4gsw_status q4gsw_grad_norm(const void* table, size_t table_bytes, float inv_scale, float* norm, void* workspace,
+                             size_t workspace_bytes, q4gsw_stream_t stream) {
   return guarded([&] {
-    const q4gsw_status st = check_grad_call(table, table_bytes, count, inv_scale, norm, workspace, workspace_bytes);
+    const q4gsw_status st = check_grad_call(table, table_bytes, inv_scale, norm, workspace, workspace_bytes);
     if (st != Q4GSW_OK) return st;
     set_route("grad_norm launches=2");
-    return from_cuda(launch_grad_norm(table, table_bytes, count, inv_scale, norm, workspace, stream));
+    return from_cuda(launch_grad_norm(table, table_bytes, inv_scale, norm, workspace, stream));
   });
 }
 
-q4gsw_status q4gsw_grad_clip(const void* table, size_t table_bytes, int count, float max_norm, float inv_scale,
-                             float* norm, void* workspace, size_t workspace_bytes, q4gsw_stream_t stream) {
+q4gsw_status q4gsw_grad_clip(const void* table, size_t table_bytes, float max_norm, float inv_scale, float* norm,
+                             void* workspace, size_t workspace_bytes, q4gsw_stream_t stream) {
   return guarded([&] {
     if (!(max_norm > 0.f)) return Q4GSW_ERR_SHAPE;
-    const q4gsw_status st = check_grad_call(table, table_bytes, count, inv_scale, norm, workspace, workspace_bytes);
+    const q4gsw_status st = check_grad_call(table, table_bytes, inv_scale, norm, workspace, workspace_bytes);
     if (st != Q4GSW_OK) return st;
     set_route("grad_clip launches=2");
-    return from_cuda(launch_grad_clip(table, table_bytes, count, max_norm, inv_scale, norm, workspace, stream));
+    return from_cuda(launch_grad_clip(table, table_bytes, max_norm, inv_scale, norm, workspace, stream));
   });
 }
 

@@ -4,7 +4,7 @@
 //   norm = |inv_scale| sqrt(sum g^2),  out = inv_scale min(1, max_norm / (norm + 1e-6)) g
 //
 // Two launches whatever the number of tensors.  The list is cut into pieces of 1024
-// elements of one tensor; a table in device memory says for every piece whose it is,
+// elements of one tensor, each with a record in a table in device memory,
 // and every CTA has an equal run of pieces, eight in flight.  The first launch leaves
 // one partial sum per CTA; the second adds them (each CTA for itself, in a fixed order,
 // so no CTA waits for another) and scales, from the end of the list, whose gradients
@@ -19,7 +19,7 @@
 // Norm of 201 M fp32 elements 118 us and of as many fp16 64 (the copy rate of those
 // bytes: 123 and 61); 224 gradients of 11.3 M elements together 12.5, their clip into
 // other buffers 24.9, of which the launches and the dependent look-ups (table, tensor,
-// data) are about five.  With a test per load (loads one after another) 34 and, over
+// data) are about three.  With a test per load (loads one after another) 34 and, over
 // fp16 views that start anywhere, 149 instead of 89 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,29 +38,27 @@ constexpr int kGroup = 4;                       // elements of a thread in a pie
 constexpr int kPiece = kThreads * kGroup;
 constexpr int kBatch = 8;                       // pieces in flight
 constexpr int kMaxCtas = 592;                   // 4 of 148 SMs
+constexpr int64_t kMaxPieces = 1 << 26;         // 2 GB of table
 
-struct Entry {
+// What a CTA needs to know of a piece, in one load.  Both pointers count from the
+// 16-byte boundary at or before the gradient's piece; `skip` elements there belong to
+// nobody (the first piece of a tensor that starts off a boundary), `left` elements from
+// there on reach the tensor's end (0: an unused record behind the list).
+struct Piece {
   const void* grad;
   void* out;
-  int64_t size;
-  int32_t first;                  // its first piece
-  int32_t shift;                  // elements between the 16-byte boundary before it and its start
-  int32_t half_grad, half_out;
+  int64_t left;
+  int32_t skip;
+  int32_t halves;                 // bit 0: the gradient, bit 1: the output; bit 2: there is no output
 };
-struct Head {
-  int64_t pieces;
-  int64_t pad;
-};
-// Head, Entry[count], int32 tensor of each piece
+static_assert(sizeof(Piece) == 32, "two loads of 16 bytes");
 
-__host__ __device__ inline size_t map_offset(int count) { return sizeof(Head) + sizeof(Entry) * (size_t)count; }
-
-// Elements at + k kPiece .. + 3 of a tensor for k < pieces <= kBatch, zero outside it;
-// `at` counts from a boundary of 16 bytes of the gradient in steps of four.  One test
-// for the whole batch, so that its loads are issued together.
-__device__ __forceinline__ void load_batch(const Entry& e, int64_t at, int pieces, float (&v)[kBatch][kGroup]) {
-  if (at >= 0 && at + (pieces - 1) * kPiece + kGroup <= e.size) {
-    if (e.half_grad) {
+// Elements at + k kPiece .. + 3 of a piece and its successors for k < pieces <= kBatch,
+// zero outside the tensor.  One test for the whole batch, so that its loads are issued
+// together.
+__device__ __forceinline__ void load_batch(const Piece& e, int at, int pieces, float (&v)[kBatch][kGroup]) {
+  if (at >= e.skip && at + (pieces - 1) * kPiece + kGroup <= e.left) {
+    if (e.halves & 1) {
       const uint2* p = reinterpret_cast<const uint2*>(static_cast<const __half*>(e.grad) + at);
       uint2 r[kBatch];
 #pragma unroll
@@ -84,17 +82,17 @@ __device__ __forceinline__ void load_batch(const Entry& e, int64_t at, int piece
   for (int k = 0; k < kBatch; ++k)
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
-      const int64_t j = at + k * kPiece + i;
-      v[k][i] = k >= pieces || j < 0 || j >= e.size ? 0.f
-                : e.half_grad                       ? __half2float(static_cast<const __half*>(e.grad)[j])
-                                                    : static_cast<const float*>(e.grad)[j];
+      const int j = at + k * kPiece + i;
+      v[k][i] = k >= pieces || j < e.skip || j >= e.left ? 0.f
+                : e.halves & 1                           ? __half2float(static_cast<const __half*>(e.grad)[j])
+                                                         : static_cast<const float*>(e.grad)[j];
     }
 }
 
 // `wide`: the output is on a boundary where the gradient is
-__device__ __forceinline__ void store_group(const Entry& e, bool wide, int64_t at, const float (&v)[kGroup]) {
-  if (wide && at >= 0 && at + kGroup <= e.size) {
-    if (e.half_out)
+__device__ __forceinline__ void store_group(const Piece& e, bool wide, int at, const float (&v)[kGroup]) {
+  if (wide && at >= e.skip && at + kGroup <= e.left) {
+    if (e.halves & 2)
       *reinterpret_cast<uint2*>(static_cast<__half*>(e.out) + at) =
           make_uint2(h2_as_u32(__floats2half2_rn(v[0], v[1])), h2_as_u32(__floats2half2_rn(v[2], v[3])));
     else
@@ -103,27 +101,39 @@ __device__ __forceinline__ void store_group(const Entry& e, bool wide, int64_t a
   }
 #pragma unroll
   for (int i = 0; i < kGroup; ++i)
-    if (at + i >= 0 && at + i < e.size) {
-      if (e.half_out) static_cast<__half*>(e.out)[at + i] = __float2half_rn(v[i]);
+    if (at + i >= e.skip && at + i < e.left) {
+      if (e.halves & 2) static_cast<__half*>(e.out)[at + i] = __float2half_rn(v[i]);
       else static_cast<float*>(e.out)[at + i] = v[i];
     }
 }
 
-// Calls body(entry, piece of the entry, pieces up to kBatch) over this CTA's run of
-// pieces.
+// Calls body(piece, pieces of its tensor up to kBatch) over this CTA's run of pieces;
+// the next record is on its way meanwhile (201 M fp16 elements: 73 us without).
 template <class F>
-__device__ __forceinline__ void for_pieces(const unsigned char* table, int count, int run, F&& body) {
-  const int64_t pieces = reinterpret_cast<const Head*>(table)->pieces;
-  const Entry* entries = reinterpret_cast<const Entry*>(table + sizeof(Head));
-  const int32_t* owner = reinterpret_cast<const int32_t*>(table + map_offset(count));
-  int64_t p = run * pieces / gridDim.x;
-  const int64_t end = (run + 1) * pieces / gridDim.x;
+__device__ __forceinline__ void for_pieces(const Piece* table, int pieces, int run, F&& body) {
+  int p = (int)((int64_t)run * pieces / gridDim.x);
+  const int end = (int)((int64_t)(run + 1) * pieces / gridDim.x);
+  if (p >= end) return;
+  const uint4* record = reinterpret_cast<const uint4*>(table + p);
+  uint4 lo = record[0], hi = record[1];
   while (p < end) {
-    const Entry e = entries[owner[p]];
-    const int64_t last = e.first + (e.size + e.shift + kPiece - 1) / kPiece;
-    const int64_t stop = end < last ? end : last;
-    for (; p < stop; p += kBatch) body(e, p - e.first, (int)(stop - p < kBatch ? stop - p : kBatch));
-    p = stop;
+    Piece e;
+    e.grad = reinterpret_cast<const void*>((uint64_t)lo.y << 32 | lo.x);
+    e.out = reinterpret_cast<void*>((uint64_t)lo.w << 32 | lo.z);
+    e.left = (int64_t)((uint64_t)hi.y << 32 | hi.x);
+    e.skip = (int)hi.z;
+    e.halves = (int)hi.w;
+    if (e.left == 0) return;             // behind the list
+    const int64_t more = (e.left + kPiece - 1) / kPiece;
+    int n = end - p < kBatch ? end - p : kBatch;
+    n = more < n ? (int)more : n;
+    p += n;
+    if (p < end) {
+      record = reinterpret_cast<const uint4*>(table + p);
+      lo = record[0];
+      hi = record[1];
+    }
+    body(e, n);
   }
 }
 
@@ -140,16 +150,15 @@ __device__ __forceinline__ double cta_sum(double v, double* s_part) {
 }
 
 __global__ void __launch_bounds__(kThreads, 4)
-q4gsw_grad_squares_kernel(const unsigned char* table, int count, double* part) {
+q4gsw_grad_squares_kernel(const Piece* table, int pieces, double* part) {
   __shared__ double s_part[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
   double sum = 0.;
-  for_pieces(table, count, blockIdx.x, [&](const Entry& e, int64_t piece, int n) {
-    const int64_t at = piece * kPiece + (int)threadIdx.x * kGroup - e.shift;
+  for_pieces(table, pieces, blockIdx.x, [&](const Piece& e, int n) {
     float v[kBatch][kGroup];
-    load_batch(e, at, n, v);
-    if (e.half_grad) {
+    load_batch(e, (int)threadIdx.x * kGroup, n, v);
+    if (e.halves & 1) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         float s = 0.f;
@@ -184,8 +193,8 @@ q4gsw_grad_norm_kernel(const double* part, int parts, float inv_scale, float* no
 }
 
 __global__ void __launch_bounds__(kThreads, 4)
-q4gsw_grad_scale_kernel(const unsigned char* table, int count, const double* part, int parts, float max_norm,
-                        float inv_scale, float* norm) {
+q4gsw_grad_scale_kernel(const Piece* table, int pieces, const double* part, int parts, float max_norm, float inv_scale,
+                        float* norm) {
   __shared__ double s_part[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
@@ -195,11 +204,10 @@ q4gsw_grad_scale_kernel(const unsigned char* table, int count, const double* par
   float clip = isinf(max_norm) && !isnan(n) ? 1.f : max_norm / (n + 1e-6f);
   if (clip > 1.f) clip = 1.f;
   const float factor = inv_scale * clip;
-  for_pieces(table, count, gridDim.x - 1 - blockIdx.x, [&](const Entry& e, int64_t piece, int n) {
-    if (factor == 1.f && e.out == e.grad && e.half_out == e.half_grad) return;
-    const uintptr_t start = reinterpret_cast<uintptr_t>(e.out) - (uintptr_t)e.shift * (e.half_out ? 2 : 4);
-    const bool wide = (start & (e.half_out ? 7u : 15u)) == 0;
-    const int64_t at = piece * kPiece + (int)threadIdx.x * kGroup - e.shift;
+  for_pieces(table, pieces, gridDim.x - 1 - blockIdx.x, [&](const Piece& e, int n) {
+    if (e.halves & 4 || (factor == 1.f && e.out == e.grad && e.halves != 1 && e.halves != 2)) return;
+    const bool wide = (reinterpret_cast<uintptr_t>(e.out) & (e.halves & 2 ? 7u : 15u)) == 0;
+    const int at = (int)threadIdx.x * kGroup;
     float v[kBatch][kGroup];
     load_batch(e, at, n, v);
 #pragma unroll
@@ -213,7 +221,7 @@ q4gsw_grad_scale_kernel(const unsigned char* table, int count, const double* par
 
 }  // namespace grads
 
-// Pieces of one tensor: without its address, with the largest shift that it may have.
+// Pieces of one tensor that starts `shift` elements behind a boundary.
 static int64_t grad_pieces(int64_t size, int64_t shift) {
   return size ? (size + shift + grads::kPiece - 1) / grads::kPiece : 0;
 }
@@ -222,47 +230,38 @@ size_t grad_table_bytes(int count, const int64_t* sizes) {
   int64_t pieces = 0;
   for (int i = 0; i < count; ++i) {
     if (sizes[i] < 0 || sizes[i] > ((int64_t)1 << 44)) return 0;
-    pieces += grad_pieces(sizes[i], 7);
-    if (pieces > 0x7fffffff) return 0;
+    pieces += grad_pieces(sizes[i], 7);      // the largest shift
+    if (pieces > grads::kMaxPieces) return 0;
   }
-  return round_up(grads::map_offset(count) + sizeof(int32_t) * (size_t)pieces, 16);
+  return sizeof(grads::Piece) * (size_t)(pieces ? pieces : 1);
 }
 
-size_t grad_table_least(int count) { return round_up(grads::map_offset(count), 16); }
-
 void grad_table_fill(int count, const void* const* grads_in, const int* half_grads, void* const* outs,
-                     const int* half_outs, const int64_t* sizes, void* table) {
+                     const int* half_outs, const int64_t* sizes, void* table, size_t table_bytes) {
   unsigned char* t = static_cast<unsigned char*>(table);
-  int64_t pieces = 0;
+  std::memset(t, 0, table_bytes);
   for (int i = 0; i < count; ++i) {
-    grads::Entry e;
-    std::memset(&e, 0, sizeof(e));
-    e.grad = grads_in[i];
-    e.out = outs ? outs[i] : nullptr;
-    e.size = sizes[i];
-    e.first = (int32_t)pieces;
-    e.shift = sizes[i] ? (int32_t)((reinterpret_cast<uintptr_t>(grads_in[i]) & 15u) / (half_grads[i] ? 2 : 4)) : 0;
-    e.half_grad = half_grads[i];
-    e.half_out = outs ? half_outs[i] : 0;
-    std::memcpy(t + sizeof(grads::Head) + sizeof(e) * (size_t)i, &e, sizeof(e));
-    const int64_t n = grad_pieces(sizes[i], e.shift);
+    const int size = half_grads[i] ? 2 : 4, out_size = outs && half_outs[i] ? 2 : 4;
+    const uintptr_t grad = reinterpret_cast<uintptr_t>(grads_in[i]);
+    const int64_t shift = sizes[i] ? (int64_t)(grad & 15u) / size : 0;
+    const int64_t n = grad_pieces(sizes[i], shift);
     for (int64_t p = 0; p < n; ++p) {
-      const int32_t who = i;
-      std::memcpy(t + grads::map_offset(count) + sizeof(int32_t) * (size_t)(pieces + p), &who, sizeof(who));
+      const int64_t first = p * grads::kPiece - shift;      // the piece's first element
+      grads::Piece e;
+      e.grad = reinterpret_cast<const void*>(grad + (uintptr_t)(first * size));
+      e.out = outs ? reinterpret_cast<void*>(reinterpret_cast<uintptr_t>(outs[i]) + (uintptr_t)(first * out_size)) : nullptr;
+      e.left = sizes[i] - first;
+      e.skip = first < 0 ? (int32_t)-first : 0;
+      e.halves = (half_grads[i] ? 1 : 0) | (!outs ? 4 : half_outs[i] ? 2 : 0);
+      std::memcpy(t, &e, sizeof(e));
+      t += sizeof(e);
     }
-    pieces += n;
   }
-  grads::Head h{pieces, 0};
-  std::memcpy(t, &h, sizeof(h));
 }
 
 size_t grad_workspace_bytes() { return sizeof(double) * grads::kMaxCtas; }
 
-static int grad_ctas(size_t table_bytes, int count) {
-  // (some of the map's words may be unused: those CTAs have no piece)
-  const size_t most = (table_bytes - grads::map_offset(count)) / sizeof(int32_t);
-  return most < 1 ? 1 : most < (size_t)grads::kMaxCtas ? (int)most : grads::kMaxCtas;
-}
+static int grad_ctas(int pieces) { return pieces < grads::kMaxCtas ? pieces : grads::kMaxCtas; }
 
 static cudaLaunchConfig_t grad_config(cudaLaunchAttribute* attr, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -276,30 +275,29 @@ static cudaLaunchConfig_t grad_config(cudaLaunchAttribute* attr, int ctas, cudaS
   return cfg;
 }
 
-cudaError_t launch_grad_norm(const void* table, size_t table_bytes, int count, float inv_scale, float* norm,
-                             void* workspace, cudaStream_t stream) {
-  const int ctas = grad_ctas(table_bytes, count);
+cudaError_t launch_grad_norm(const void* table, size_t table_bytes, float inv_scale, float* norm, void* workspace,
+                             cudaStream_t stream) {
+  const int pieces = (int)(table_bytes / sizeof(grads::Piece)), ctas = grad_ctas(pieces);
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = grad_config(attr, ctas, stream);
   double* part = static_cast<double*>(workspace);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, grads::q4gsw_grad_squares_kernel,
-                                           static_cast<const unsigned char*>(table), count, part);
+                                           static_cast<const grads::Piece*>(table), pieces, part);
   if (e != cudaSuccess) return e;
   cfg = grad_config(attr, 1, stream);
   return cudaLaunchKernelEx(&cfg, grads::q4gsw_grad_norm_kernel, (const double*)part, ctas, inv_scale, norm);
 }
 
-cudaError_t launch_grad_clip(const void* table, size_t table_bytes, int count, float max_norm, float inv_scale,
-                             float* norm, void* workspace, cudaStream_t stream) {
-  const int ctas = grad_ctas(table_bytes, count);
+cudaError_t launch_grad_clip(const void* table, size_t table_bytes, float max_norm, float inv_scale, float* norm,
+                             void* workspace, cudaStream_t stream) {
+  const int pieces = (int)(table_bytes / sizeof(grads::Piece)), ctas = grad_ctas(pieces);
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = grad_config(attr, ctas, stream);
+  const cudaLaunchConfig_t cfg = grad_config(attr, ctas, stream);
   double* part = static_cast<double*>(workspace);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, grads::q4gsw_grad_squares_kernel,
-                                           static_cast<const unsigned char*>(table), count, part);
+                                           static_cast<const grads::Piece*>(table), pieces, part);
   if (e != cudaSuccess) return e;
-  cfg = grad_config(attr, ctas, stream);
-  return cudaLaunchKernelEx(&cfg, grads::q4gsw_grad_scale_kernel, static_cast<const unsigned char*>(table), count,
+  return cudaLaunchKernelEx(&cfg, grads::q4gsw_grad_scale_kernel, static_cast<const grads::Piece*>(table), pieces,
                             (const double*)part, ctas, max_norm, inv_scale, norm);
 }
 

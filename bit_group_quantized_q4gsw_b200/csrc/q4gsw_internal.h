@@ -226,14 +226,14 @@ cudaError_t launch_norms_bwd(const NormsArgs& a, cudaStream_t stream, char* rout
 // Gradient lists (q4gsw_grads.cu): the table's bytes (0: too many pieces), its host
 // contents, and the two calls.
 size_t grad_table_bytes(int count, const int64_t* sizes);
-size_t grad_table_least(int count);   // of a list of empty tensors
 void grad_table_fill(int count, const void* const* grads, const int* half_grads, void* const* outs,
-                     const int* half_outs, const int64_t* sizes, void* table);
+                     const int* half_outs, const int64_t* sizes, void* table, size_t table_bytes);
 size_t grad_workspace_bytes();
-cudaError_t launch_grad_norm(const void* table, size_t table_bytes, int count, float inv_scale, float* norm,
+constexpr size_t kGradRecordBytes = 32;
+cudaError_t launch_grad_norm(const void* table, size_t table_bytes, float inv_scale, float* norm, void* workspace,
+                             cudaStream_t stream);
+cudaError_t launch_grad_clip(const void* table, size_t table_bytes, float max_norm, float inv_scale, float* norm,
                              void* workspace, cudaStream_t stream);
-cudaError_t launch_grad_clip(const void* table, size_t table_bytes, int count, float max_norm, float inv_scale,
-                             float* norm, void* workspace, cudaStream_t stream);
 
 // Embedding rows out[t] = dequant(W)[indices[t]] (fp32); an index outside
 // [0, N) gives a zero row and sets kIndexErrorBit in the device error word.

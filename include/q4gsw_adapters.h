@@ -162,10 +162,11 @@ Q4GSW_API q4gsw_status q4gsw_norms_bwd(const uint16_t *h_out, const uint16_t *d_
 /* Bytes and host contents of the list's table: `count` tensors (1 <= count <=
  * 65536), sizes[i] >= 0 elements at grads[i], fp32 (half_grads[i] 0) or fp16 (1),
  * each aligned to its element; outs[i] (fp32 or fp16 by half_outs[i]) may be
- * grads[i] itself where the types agree, and outs may be NULL for the norm alone.  The table is plain
- * data: the caller copies it to the device (16-byte aligned) and keeps it as
- * long as the buffers stay where they are.  No two outs may overlap.
- * Q4GSW_ERR_SIZE for a table of more than 2^31 - 1 pieces of 1024 elements. */
+ * grads[i] itself where the types agree, and outs may be NULL for the norm alone.
+ * The table is plain data, a record for every 1024 elements: the caller copies
+ * its table_bytes to the device (16-byte aligned) and keeps them as long as the
+ * buffers stay where they are.  No out may overlap another out or a gradient that
+ * is not its own.  Q4GSW_ERR_SIZE for a list of more than 2^26 records. */
 Q4GSW_API size_t q4gsw_grad_table_bytes(int count, const int64_t *sizes);
 Q4GSW_API q4gsw_status q4gsw_grad_table(int count, const void *const *grads, const int *half_grads, void *const *outs,
                               const int *half_outs, const int64_t *sizes, void *table, size_t table_bytes);
@@ -175,14 +176,14 @@ Q4GSW_API size_t q4gsw_grad_workspace_bytes(void);
 
 /* norm fp32 [1] (4-byte aligned), two launches.  table: device copy of the
  * table; table_bytes as above.  inv_scale finite (Q4GSW_ERR_SHAPE else). */
-Q4GSW_API q4gsw_status q4gsw_grad_norm(const void *table, size_t table_bytes, int count, float inv_scale, float *norm,
+Q4GSW_API q4gsw_status q4gsw_grad_norm(const void *table, size_t table_bytes, float inv_scale, float *norm,
                              void *workspace, size_t workspace_bytes, q4gsw_stream_t stream);
 
-/* The norm, and every out, two launches; the table must have been made with outs.
+/* The norm, and every out, two launches (a table made without outs gives the norm alone).
  * max_norm > 0 (Q4GSW_ERR_SHAPE else; infinity: never clipped).  A tensor that is
  * its own out and whose factor is 1 is left alone. */
-Q4GSW_API q4gsw_status q4gsw_grad_clip(const void *table, size_t table_bytes, int count, float max_norm, float inv_scale,
-                             float *norm, void *workspace, size_t workspace_bytes, q4gsw_stream_t stream);
+Q4GSW_API q4gsw_status q4gsw_grad_clip(const void *table, size_t table_bytes, float max_norm, float inv_scale, float *norm,
+                             void *workspace, size_t workspace_bytes, q4gsw_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -123,33 +123,34 @@ def _table(lib, sizes, grads=None, hg=None, outs="same", ho=None, nbytes=None, c
 def test_grad_table_arguments():
     lib = b.library()
     assert _table(lib, [5, 0, 8193])[0] == OK
-    assert _table(lib, [5, 0, 8193])[1] == 176      # head 16, three entries of 40, ten pieces of 4: 176, a multiple of 16
+    assert _table(lib, [5, 0, 8193])[1] == 32 * (1 + 0 + 9)        # a record of 32 bytes for every 1024 elements
     assert _table(lib, [5], outs=None)[0] == OK
     assert _table(lib, [5, 0], grads=[P, None])[0] == OK           # an empty tensor has no address
     for kw, st in ((dict(count=0), SHAPE), (dict(count=65537), SHAPE), (dict(hg=[2]), UNSUPPORTED), (dict(hg=[0], ho=[3]), UNSUPPORTED),
                    (dict(grads=[None]), NULL), (dict(outs=[None]), NULL), (dict(grads=[P + 2]), ALIGN),
-                   (dict(grads=[P + 1], hg=[1]), ALIGN), (dict(outs=[P + 2]), ALIGN), (dict(nbytes=15), SIZE)):
+                   (dict(grads=[P + 1], hg=[1]), ALIGN), (dict(outs=[P + 2]), ALIGN), (dict(nbytes=31), SIZE)):
         assert _table(lib, [5], **kw)[0] == st, kw
     assert _table(lib, [5], grads=[P + 2], hg=[1])[0] == OK
     assert _table(lib, [-1], nbytes=1)[0] == SHAPE
     assert _table(lib, [1 << 45]) == (SIZE, 0)
-    assert _table(lib, [1024 << 31])[1] == 0
+    assert _table(lib, [1024 << 26])[1] == 0
     assert lib.q4gsw_grad_table_bytes(0, None) == 0
 
 
 def test_grad_call_arguments():
     lib = b.library()
     w = lib.q4gsw_grad_workspace_bytes()
-    for kw, st in ((dict(count=0), SHAPE), (dict(inv=float("nan")), SHAPE), (dict(inv=float("inf")), SHAPE),
+    for kw, st in ((dict(inv=float("nan")), SHAPE), (dict(inv=float("inf")), SHAPE),
                    (dict(table=None), NULL), (dict(norm=None), NULL), (dict(ws=None), NULL), (dict(table=P + 8), ALIGN),
-                   (dict(norm=P + 2), ALIGN), (dict(ws=P + 8), ALIGN), (dict(tb=16), SIZE), (dict(wb=w - 1), SIZE)):
-        a = dict(table=P, tb=1 << 20, count=3, inv=1.0, norm=P, ws=P, wb=w)
+                   (dict(norm=P + 2), ALIGN), (dict(ws=P + 8), ALIGN), (dict(tb=16), SIZE), (dict(tb=48), SIZE),
+                   (dict(tb=0), SIZE), (dict(tb=32 << 31), SIZE), (dict(wb=w - 1), SIZE)):
+        a = dict(table=P, tb=1 << 20, inv=1.0, norm=P, ws=P, wb=w)
         a.update(kw)
         tail = (a["norm"], a["ws"], a["wb"], None)
-        assert lib.q4gsw_grad_norm(a["table"], a["tb"], a["count"], a["inv"], *tail) == st, kw
-        assert lib.q4gsw_grad_clip(a["table"], a["tb"], a["count"], 1.0, a["inv"], *tail) == st, kw
+        assert lib.q4gsw_grad_norm(a["table"], a["tb"], a["inv"], *tail) == st, kw
+        assert lib.q4gsw_grad_clip(a["table"], a["tb"], 1.0, a["inv"], *tail) == st, kw
     for m in (0.0, -1.0, float("nan")):
-        assert lib.q4gsw_grad_clip(P, 1 << 20, 3, m, 1.0, P, P, w, None) == SHAPE
+        assert lib.q4gsw_grad_clip(P, 1 << 20, m, 1.0, P, P, w, None) == SHAPE
 
 
 def test_python_entry_points_refuse_tensors_off_the_device():

@@ -224,7 +224,7 @@ def test_python_checks():
         with pytest.raises(ValueError, match=what):
             m.q4gsw_norms_fwd(h, **kw)
     for kw, what in ((dict(d_x=h), "go together"), (dict(d_h=h, w_pre=w), "go together"), (dict(), "d_x or d_h"),
-                     (dict(d_h=h, d_block=h), "d_block"), (dict(d_x=h, w_pre=w, d_gate=w), "d_gate")):
+                     (dict(d_h=h, d_block=h), "d_block"), (dict(d_x=h, w_pre=w, d_gate=w), "d_gate"), (dict(d_h=h, d_w_post=w), "d_w_post")):
         with pytest.raises(ValueError, match=what):
             m.q4gsw_norms_bwd(h, **kw)
     with pytest.raises(m.Q4gswError, match="SHAPE"):

@@ -229,23 +229,12 @@ __device__ __forceinline__ void down_park(const float (&acc)[RJ][4], float (*red
 // out[m][j] = f sum_c act[m][c] P(c, j) for the tokens m of a tile, P and f (where scale
 // is given) of the tile's adapter, for many tiles (few: q4gsw_adapters_low_kernel).
 //
-// A CTA has WT = 2 consecutive tiles (with four: 40 us in place of 29 at 4096 x 4096, rank
-// 64), eight warps 8 / WT to a tile.  Stages of 128 columns
-// of the tiles' tokens and of the matrix of one adapter go through a ring in shared
-// memory (cp.async), from which the warps take their fragments by ldmatrix: the matrix
-// is read once a CTA.  Tiles of several adapters take turns, one pass over the stages
-// each.  The warps of a tile and the KS CTAs of the cluster (grid = (slots / WT, KS))
+// A CTA has a pair of tiles of one adapter, four warps to a tile.  Stages of 128 columns
+// of the tiles' tokens and of the adapter's matrix go through a ring in shared memory
+// (cp.async), from which the warps take their fragments by ldmatrix: the matrix is read
+// once a CTA.  The warps of a tile and the KS CTAs of the cluster (grid = (pairs, KS))
 // split the contraction; sums go to fp32 registers stage by stage (the tensor cores
 // truncate theirs), and the warps' and the CTAs' are added in a fixed order.
-// tile[w] by a run-time w, without an array in local memory
-template <int WT>
-__device__ __forceinline__ int tile_of(const int (&tile)[WT], int w) {
-  int v = tile[0];
-#pragma unroll
-  for (int i = 1; i < WT; ++i) v = w == i ? tile[i] : v;
-  return v;
-}
-
 constexpr int kDownTiles = 2;
 template <bool BY_ROWS, int RJ>
 struct DownRing {
@@ -282,18 +271,19 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
   const int KS = gridDim.y, ks = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int slots = plan_slots(M, L), slot0 = blockIdx.x * WT;
-  int tile[WT];
-#pragma unroll
-  for (int w = 0; w < WT; ++w) tile[w] = slot0 + w < slots ? ld_int(P.tile + slot0 + w) : kNoTile;
-  if (!plan_fits(P, M, L, error)) return;
-  // tiles in use come first: where the first is unused, so is the whole cluster
-  if (tile[0] == kNoTile) return;
-  if (KS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int slot0 = ld_int(P.pair + blockIdx.x);
+  if (!plan_fits(P, M, L, error) || slot0 < 0) return;      // the whole cluster
+  const int adapter = ld_int(P.tile + slot0);
+  const bool two = slot0 + 1 < plan_slots(M, L) && ld_int(P.tile + slot0 + 1) == adapter;
   if (threadIdx.x < WT * kTileRows)
-    s_row[threadIdx.x] = slot0 + (int)threadIdx.x / kTileRows < slots
-                             ? ld_int(P.rows + (size_t)slot0 * kTileRows + threadIdx.x) : -1;
+    s_row[threadIdx.x] = two || threadIdx.x < kTileRows ? ld_int(P.rows + (size_t)slot0 * kTileRows + threadIdx.x) : -1;
   __syncthreads();
+  if (adapter < 0) {
+    for (int e = threadIdx.x + ks * kThreads; e < WT * kTileRows * R; e += KS * kThreads)
+      if (s_row[e / R] >= 0) out[(size_t)s_row[e / R] * R + e % R] = 0.f;
+    return;
+  }
+  if (KS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int stages = (C + D::COLS - 1) / D::COLS;
   const int it_begin = (int)((long long)ks * stages / KS), it_end = (int)((long long)(ks + 1) * stages / KS);
   const int my_tile = warp / WK, my_part = warp % WK;
@@ -302,86 +292,75 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
   for (int j = 0; j < RJ; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) total[j][e] = 0.f;
-  for (int run = 0; run < WT;) {
-    const int adapter = tile_of(tile, run);
-    int run_end = run + 1;
-    while (run_end < WT && tile_of(tile, run_end) == adapter) ++run_end;
-    if (adapter < 0) {
-      run = run_end;
-      continue;
-    }
-    const __half* mat = proj + (size_t)adapter * R * C;
-    auto issue = [&](int it) {
-      if (it < it_end) {
-        const uint32_t st = ring + (uint32_t)(it % D::STAGES) * D::STAGE;
-        const int c0 = it * D::COLS;
-        const int q = threadIdx.x % 16, c = c0 + 8 * q;         // C % 8 == 0: a chunk is wholly in or out
-#pragma unroll
-        for (int i = 0; i < WT; ++i) {
-          const int row = 16 * i + threadIdx.x / 16, m = s_row[row];
-          const bool in = i >= run && i < run_end && m >= 0 && c < C;
-          copy_16(st + row * D::X_PITCH + 16 * q, act + (in ? (size_t)m * C + c : 0), in);
-        }
-        const uint32_t sp = st + D::X_BYTES;
-        if constexpr (BY_ROWS) {
-          for (int row = threadIdx.x / 16; row < R; row += kThreads / 16)
-            copy_16(sp + row * D::P_PITCH + 16 * q, mat + (c < C ? (size_t)row * C + c : 0), c < C);
-        } else {
-          for (int e = threadIdx.x; e < D::P_ROWS * RJ; e += kThreads) {
-            const int row = e / RJ, k = e % RJ;
-            const bool in = c0 + row < C;
-            copy_16(sp + row * D::P_PITCH + 16 * k, mat + (in ? (size_t)(c0 + row) * R + 8 * k : 0), in);
-          }
-        }
-      }
-      cp_async_commit();
-    };
-    for (int i = 0; i < D::STAGES - 1; ++i) issue(it_begin + i);
-    for (int it = it_begin; it < it_end; ++it) {
-      cp_async_wait<D::STAGES - 2>();
-      __syncthreads();                     // the stage has landed, and the one refilled below has been used by all
-      issue(it + D::STAGES - 1);
-      if (my_tile < run || my_tile >= run_end) continue;
+  const __half* mat = proj + (size_t)adapter * R * C;
+  auto issue = [&](int it) {
+    if (it < it_end) {
       const uint32_t st = ring + (uint32_t)(it % D::STAGES) * D::STAGE;
-      // rows 0-7, 8-15 at columns 0-7, then both at columns 8-15 of a step of 16
-      const uint32_t xa = st + (my_tile * kTileRows + lane % 16) * D::X_PITCH + 16 * (lane / 16);
-      const uint32_t pa = st + D::X_BYTES;
-      float acc[RJ][4];
+      const int c0 = it * D::COLS;
+      const int q = threadIdx.x % 16, c = c0 + 8 * q;         // C % 8 == 0: a chunk is wholly in or out
 #pragma unroll
-      for (int j = 0; j < RJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < D::COLS / 16 / WK; ++k) {
-        const int step = my_part * (D::COLS / 16 / WK) + k;
-        uint32_t af[4];
-        ldmatrix4(af, xa + 32 * step);
-#pragma unroll
-        for (int j = 0; j < RJ; j += 2) {
-          // ranks 8 j .. 8 j + 15 (the second eight repeat the first where RJ is odd)
-          uint32_t bf[4];
-          const int jr = j + 1 < RJ ? lane / 16 : 0;
-          if constexpr (BY_ROWS)
-            ldmatrix4(bf, pa + (8 * (j + jr) + lane % 8) * D::P_PITCH + 32 * step + 16 * (lane / 8 % 2));
-          else
-            ldmatrix4_trans(bf, pa + (16 * step + lane % 16) * D::P_PITCH + 16 * (j + jr));
-          const uint32_t b0[2] = {bf[0], bf[1]}, b1[2] = {bf[2], bf[3]};
-          mma_16816(acc[j], af, b0);
-          if (j + 1 < RJ) mma_16816(acc[j + 1 < RJ ? j + 1 : j], af, b1);
+      for (int i = 0; i < WT; ++i) {
+        const int row = 16 * i + threadIdx.x / 16, m = s_row[row];
+        const bool in = m >= 0 && c < C;
+        copy_16(st + row * D::X_PITCH + 16 * q, act + (in ? (size_t)m * C + c : 0), in);
+      }
+      const uint32_t sp = st + D::X_BYTES;
+      if constexpr (BY_ROWS) {
+        for (int row = threadIdx.x / 16; row < R; row += kThreads / 16)
+          copy_16(sp + row * D::P_PITCH + 16 * q, mat + (c < C ? (size_t)row * C + c : 0), c < C);
+      } else {
+        for (int e = threadIdx.x; e < D::P_ROWS * RJ; e += kThreads) {
+          const int row = e / RJ, k = e % RJ;
+          const bool in = c0 + row < C;
+          copy_16(sp + row * D::P_PITCH + 16 * k, mat + (in ? (size_t)(c0 + row) * R + 8 * k : 0), in);
         }
       }
-#pragma unroll
-      for (int j = 0; j < RJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) total[j][e] += acc[j][e];
     }
-    cp_async_wait<0>();
-    __syncthreads();                       // the ring is free
-    run = run_end;
+    cp_async_commit();
+  };
+  for (int i = 0; i < D::STAGES - 1; ++i) issue(it_begin + i);
+  for (int it = it_begin; it < it_end; ++it) {
+    cp_async_wait<D::STAGES - 2>();
+    __syncthreads();                     // the stage has landed, and the one refilled below has been used by all
+    issue(it + D::STAGES - 1);
+    const uint32_t st = ring + (uint32_t)(it % D::STAGES) * D::STAGE;
+    // rows 0-7, 8-15 at columns 0-7, then both at columns 8-15 of a step of 16
+    const uint32_t xa = st + (my_tile * kTileRows + lane % 16) * D::X_PITCH + 16 * (lane / 16);
+    const uint32_t pa = st + D::X_BYTES;
+    float acc[RJ][4];
+#pragma unroll
+    for (int j = 0; j < RJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D::COLS / 16 / WK; ++k) {
+      const int step = my_part * (D::COLS / 16 / WK) + k;
+      uint32_t af[4];
+      ldmatrix4(af, xa + 32 * step);
+#pragma unroll
+      for (int j = 0; j < RJ; j += 2) {
+        // ranks 8 j .. 8 j + 15 (the second eight repeat the first where RJ is odd)
+        uint32_t bf[4];
+        const int jr = j + 1 < RJ ? lane / 16 : 0;
+        if constexpr (BY_ROWS)
+          ldmatrix4(bf, pa + (8 * (j + jr) + lane % 8) * D::P_PITCH + 32 * step + 16 * (lane / 8 % 2));
+        else
+          ldmatrix4_trans(bf, pa + (16 * step + lane % 16) * D::P_PITCH + 16 * (j + jr));
+        const uint32_t b0[2] = {bf[0], bf[1]}, b1[2] = {bf[2], bf[3]};
+        mma_16816(acc[j], af, b0);
+        if (j + 1 < RJ) mma_16816(acc[j + 1 < RJ ? j + 1 : j], af, b1);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < RJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) total[j][e] += acc[j][e];
   }
+  cp_async_wait<0>();
+  __syncthreads();                       // the ring is free
   down_park<true, RJ>(total, red[warp], g, t);
   __syncthreads();
-  // the sums of row `row` of tile `tile` over its warps; a tile without an adapter has zeros
+  // the sums of row `row` of tile `w0` over its warps
   auto own = [&](int w0, int row, int j) {
     float s = 0.f;
 #pragma unroll
@@ -403,14 +382,13 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
     const int w = e / (owned * R), row = e / R % owned, j = e % R;
     const int m = s_row[w * kTileRows + ks * owned + row];
     if (m < 0) continue;
-    const int a = tile_of(tile, w);
     float v = 0.f;
     if (KS > 1) {
       for (int q = 0; q < KS; ++q) v += recv[w][q * owned + row][j];
     } else {
       v = own(w, row, j);
     }
-    out[(size_t)m * R + j] = a >= 0 && scale ? ld_f32(scale + a) * v : v;
+    out[(size_t)m * R + j] = scale ? ld_f32(scale + adapter) * v : v;
   }
 }
 
@@ -554,12 +532,11 @@ __device__ __forceinline__ void up_block(const __half* mat, const UpTile<RJ>& q,
   }
 }
 
-// The same for many tiles.  A CTA has four consecutive tiles, one to a warp, and a run
-// of column blocks, whose part of the matrix of up to two adapters goes through a ring
-// in shared memory: it is read once for 64 tokens, and its fragments come by ldmatrix (in
-// their natural order).  Tiles of more adapters take further passes over the blocks.
-// Sums are turned in shared memory, so that rows are read (the residual) and written in
-// whole lines.
+// The same for many tiles.  A CTA has two pairs of tiles, a tile to a warp, and a run of
+// column blocks, whose part of the matrices of the one or two adapters goes through a
+// ring in shared memory: it is read once for 64 (or 32) tokens, and its fragments come by
+// ldmatrix (in their natural order).  Sums are turned in shared memory, so that rows are
+// read (the residual) and written in whole lines.
 constexpr int kUpWarps = 4, kUpThreads = 32 * kUpWarps;
 template <bool BY_ROWS, int RJ>
 struct UpRing {
@@ -585,14 +562,15 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
   const PlanView P = plan_view(const_cast<int32_t*>(plan), M, L);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int slots = plan_slots(M, L), slot0 = blockIdx.x * kUpWarps;
-  int tile[kUpWarps];
-#pragma unroll
-  for (int w = 0; w < kUpWarps; ++w) tile[w] = slot0 + w < slots ? ld_int(P.tile + slot0 + w) : kNoTile;
-  if (!plan_fits(P, M, L) || tile[0] == kNoTile) return;         // tiles in use come first
+  // the two pairs' first tiles, their adapters, and this warp's tile
+  const int pairs = plan_pairs(M, L);
+  const int s0 = ld_int(P.pair + 2 * blockIdx.x), s1 = 2 * (int)blockIdx.x + 1 < pairs ? ld_int(P.pair + 2 * blockIdx.x + 1) : -1;
+  if (!plan_fits(P, M, L) || s0 < 0) return;       // pairs in use come first
+  const int a0 = ld_int(P.tile + s0), a1 = s1 >= 0 ? ld_int(P.tile + s1) : kNoTile;
+  const int slot = (warp < 2 ? s0 : s1) + (warp & 1), theirs = warp < 2 ? a0 : a1;
+  const int mine = theirs == kNoTile || slot >= plan_slots(M, L) || ld_int(P.tile + slot) != theirs ? kNoTile : theirs;
   const int first = blockIdx.y * blocks_per_cta, last = min(first + blocks_per_cta, (C + 63) / 64);
-  const int mine = tile_of(tile, warp);
-  const int32_t* rows = P.rows + (size_t)(slot0 + warp) * kTileRows;
+  const int32_t* rows = P.rows + (size_t)(mine == kNoTile ? s0 : slot) * kTileRows;
   const int m[2] = {mine == kNoTile ? -1 : ld_int(rows + g), mine == kNoTile ? -1 : ld_int(rows + g + 8)};
   UpTile<RJ> q;
   // ranks 16 s + 2 t, + 1, + 8, + 9 of the lane in step s
@@ -636,72 +614,65 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
   };
   if (mine == kNoAdapter)                  // the residual, or zeros
     for (int b = first; b < last; ++b) write(b, false);
-  // passes: two adapters of the tiles (sorted, those without one behind them) at a time
-  for (int run = 0; run < kUpWarps && tile_of(tile, run) >= 0;) {
-    const int a0 = tile_of(tile, run);
-    while (run < kUpWarps && tile_of(tile, run) == a0) ++run;
-    const int a1 = run < kUpWarps && tile_of(tile, run) >= 0 ? tile_of(tile, run) : a0;
-    while (run < kUpWarps && tile_of(tile, run) == a1) ++run;
-    const bool active = mine == a0 || mine == a1;
-    const uint32_t region = mine == a0 ? 0u : (uint32_t)U::REGION;
-    auto issue = [&](int b) {
-      if (b < last) {
-        const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE;
-        for (int e = threadIdx.x; e < U::ROWS * U::CHUNKS; e += kUpThreads) {
-          const int row = e / U::CHUNKS, k = e % U::CHUNKS;
-          // by rows: column 64 b + row, ranks 8 k ..; else rank row, columns 64 b + 8 k ..
-          const bool in = BY_ROWS ? 64 * b + row < C && k < RJ : row < R && 64 * b + 8 * k < C;
-          const size_t from = BY_ROWS ? (size_t)(64 * b + row) * R + 8 * k : (size_t)row * C + 64 * b + 8 * k;
-          const uint32_t to_smem = st + row * U::PITCH + 16 * k;
-          copy_16(to_smem, proj + (in ? (size_t)a0 * R * C + from : 0), in);
-          if (a1 != a0) copy_16(to_smem + U::REGION, proj + (in ? (size_t)a1 * R * C + from : 0), in);
-        }
+  if (a0 < 0) return;                      // (sorted: the second pair has no adapter, either)
+  const bool other = a1 >= 0 && a1 != a0;  // a second matrix, in the second region
+  const uint32_t region = mine == a1 && other ? (uint32_t)U::REGION : 0u;
+  auto issue = [&](int b) {
+    if (b < last) {
+      const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE;
+      for (int e = threadIdx.x; e < U::ROWS * U::CHUNKS; e += kUpThreads) {
+        const int row = e / U::CHUNKS, k = e % U::CHUNKS;
+        // by rows: column 64 b + row, ranks 8 k ..; else rank row, columns 64 b + 8 k ..
+        const bool in = BY_ROWS ? 64 * b + row < C && k < RJ : row < R && 64 * b + 8 * k < C;
+        const size_t from = BY_ROWS ? (size_t)(64 * b + row) * R + 8 * k : (size_t)row * C + 64 * b + 8 * k;
+        const uint32_t to_smem = st + row * U::PITCH + 16 * k;
+        copy_16(to_smem, proj + (in ? (size_t)a0 * R * C + from : 0), in);
+        if (other) copy_16(to_smem + U::REGION, proj + (in ? (size_t)a1 * R * C + from : 0), in);
       }
-      cp_async_commit();
-    };
-    for (int i = 0; i < U::STAGES - 1; ++i) issue(first + i);
-    for (int b = first; b < last; ++b) {
-      cp_async_wait<U::STAGES - 2>();
-      __syncthreads();                     // the block has landed, and the one refilled below has been used by all
-      issue(b + U::STAGES - 1);
-      if (!active) continue;
-      const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE + region;
-      float acc[8][4];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-#pragma unroll
-      for (int s = 0; s < KT; ++s) {
-        uint32_t bf[4][4];                 // columns 16 i .. + 7 (indices 0-7, 8-15), then + 8 .. + 15
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (BY_ROWS)
-            ldmatrix4(bf[i], st + (16 * i + 8 * (lane / 16) + lane % 8) * U::PITCH + 32 * s + 16 * (lane / 8 % 2));
-          else
-            ldmatrix4_trans(bf[i], st + (16 * s + lane % 16) * U::PITCH + 32 * i + 16 * (lane / 16));
-        }
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t f[2] = {bf[i / 2][2 * (i % 2)], bf[i / 2][2 * (i % 2) + 1]};
-            mma_16816(acc[i], part ? q.hi[s] : q.lo[s], f);
-          }
-      }
-      __syncwarp();                        // the lanes have read the block before
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(turn + (g + 8 * h) * U::T_PITCH + 8 * i + 2 * t) =
-              make_float2(q.back[h] * acc[i][2 * h], q.back[h] * acc[i][2 * h + 1]);
-      __syncwarp();
-      write(b, true);
     }
-    cp_async_wait<0>();
-    __syncthreads();                       // the ring is free
+    cp_async_commit();
+  };
+  for (int i = 0; i < U::STAGES - 1; ++i) issue(first + i);
+  for (int b = first; b < last; ++b) {
+    cp_async_wait<U::STAGES - 2>();
+    __syncthreads();                     // the block has landed, and the one refilled below has been used by all
+    issue(b + U::STAGES - 1);
+    if (mine < 0) continue;
+    const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE + region;
+    float acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+#pragma unroll
+    for (int s = 0; s < KT; ++s) {
+      uint32_t bf[4][4];                 // columns 16 i .. + 7 (indices 0-7, 8-15), then + 8 .. + 15
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (BY_ROWS)
+          ldmatrix4(bf[i], st + (16 * i + 8 * (lane / 16) + lane % 8) * U::PITCH + 32 * s + 16 * (lane / 8 % 2));
+        else
+          ldmatrix4_trans(bf[i], st + (16 * s + lane % 16) * U::PITCH + 32 * i + 16 * (lane / 16));
+      }
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t f[2] = {bf[i / 2][2 * (i % 2)], bf[i / 2][2 * (i % 2) + 1]};
+          mma_16816(acc[i], part ? q.hi[s] : q.lo[s], f);
+        }
+    }
+    __syncwarp();                        // the lanes have read the block before
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(turn + (g + 8 * h) * U::T_PITCH + 8 * i + 2 * t) =
+            make_float2(q.back[h] * acc[i][2 * h], q.back[h] * acc[i][2 * h + 1]);
+    __syncwarp();
+    write(b, true);
   }
+  cp_async_wait<0>();                      // no thread leaves with copies in flight
 }
 
 // ---------------------------------------------------------------- down and up in one
@@ -916,19 +887,27 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
     look_up(u + T::STAGES);
     const uint32_t st = ring + (uint32_t)(u % T::STAGES) * T::STAGE;
     const float* q = reinterpret_cast<const float*>(smem + (u % T::STAGES) * T::STAGE + T::X_BYTES);
-    constexpr int N = kChunk * R / kThreads;       // RJ values of q a thread, of one rank where 256 is a multiple of R
+    // RJ values of q a thread; of one rank where the threads are a multiple of the ranks
+    constexpr int N = kChunk * R / kThreads;
+    constexpr bool kOneRank = kThreads % R == 0;
     float v[N];
+    uint32_t most = 0u;      // (patterns of non-negative floats are ordered as they are; a NaN is above all)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       v[i] = q[threadIdx.x + i * kThreads];
-      // (patterns of non-negative floats are ordered as they are; a NaN is above all)
-      atomicMax(&s_top[(threadIdx.x + i * kThreads) % R], __float_as_uint(v[i]) & 0x7fffffffu);
+      const uint32_t size = __float_as_uint(v[i]) & 0x7fffffffu;
+      if (kOneRank) most = max(most, size);
+      else atomicMax(&s_top[(threadIdx.x + i * kThreads) % R], size);
     }
+    if (kOneRank) atomicMax(&s_top[threadIdx.x % R], most);
     __syncthreads();
+    float down = 0.f;
+    if (kOneRank) down = __uint_as_float((uint32_t)(127 - exponent_of(s_top[threadIdx.x % R])) << 23);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = threadIdx.x + i * kThreads;
-      const float w = v[i] * __uint_as_float((uint32_t)(127 - exponent_of(s_top[e % R])) << 23);
+      if (!kOneRank) down = __uint_as_float((uint32_t)(127 - exponent_of(s_top[e % R])) << 23);
+      const float w = v[i] * down;
       const __half h = __float2half_rn(w);
       unsigned char* at = smem + T::RING + (e / R) * T::H_PITCH + 2 * (e % R);
       *reinterpret_cast<__half*>(at) = h;
@@ -1068,8 +1047,7 @@ static cudaError_t down_form(cudaLaunchConfig_t& cfg, const __half* a, const __h
 
 cudaError_t launch_adapters_down(const AdaptersRef& ad, const uint16_t* act, bool by_rows, const uint16_t* proj,
                                  const float* scale, int M, int C, float* out, cudaStream_t stream) {
-  const int slots = ma::plan_slots(M, ad.L), sms = sm_count(current_device());
-  const int groups = (slots + ma::kDownTiles - 1) / ma::kDownTiles;
+  const int groups = ma::plan_pairs(M, ad.L), sms = sm_count(current_device());
   // contraction splits: about two CTAs per SM, two stages each at least, clusters of at most 8
   const int stages = (C + 127) / 128;
   int KS = 1;
@@ -1112,10 +1090,10 @@ static cudaError_t up_form(cudaLaunchConfig_t& cfg, const float* inter, const __
 cudaError_t launch_adapters_up(const AdaptersRef& ad, const float* inter, bool by_rows, const uint16_t* proj,
                                const float* scale, int M, int C, const uint16_t* res, uint16_t* out,
                                cudaStream_t stream) {
-  const int groups = (ma::plan_slots(M, ad.L) + ma::kUpWarps - 1) / ma::kUpWarps;
+  const int groups = (ma::plan_pairs(M, ad.L) + 1) / 2;
   const int blocks = (C + 63) / 64;
-  // runs of blocks: four CTAs per SM
-  int runs = 4 * sm_count(current_device()) / groups;
+  // runs of blocks: eight CTAs per SM, so that those without an adapter leave room
+  int runs = 8 * sm_count(current_device()) / groups;
   runs = runs < 1 ? 1 : runs > blocks ? blocks : runs;
   const int per = (blocks + runs - 1) / runs;
   cudaLaunchConfig_t cfg = {};
@@ -1210,6 +1188,7 @@ static cudaError_t grad_form(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr,
          M / ad.L >= 4 * Z * ma::kChunk)
     Z *= 2;
   cfg.gridDim = dim3(ga + gb, ad.L, Z);
+  cfg.blockDim = dim3(ma::kThreads, 1, 1);
   cfg.dynamicSmemBytes = T::BYTES;
   attr->val.clusterDim.z = Z;
   return cudaLaunchKernelEx(&cfg, kernel, da, db, ad.plan, M, ad.L, ga, (int)accumulate);
@@ -1219,7 +1198,6 @@ cudaError_t launch_adapters_grad(const AdaptersRef& ad, const uint16_t* x, const
                                  const uint16_t* d_y, const float* u, const float* scale, float* d_b, int N, int M,
                                  bool accumulate, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(ma::kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   serialize(attr[0]);

@@ -9,9 +9,12 @@
 //   order  [M]          the tokens, sorted by adapter, those without one last
 //   tile   [slots]      the adapter of each tile, kNoAdapter, or kNoTile past the last
 //   rows   [slots][16]  the tokens of each tile, -1 where it has fewer
+//   pair   [pairs]      the first of two tiles of one adapter (of the second there may be
+//                       none: the next tile is another's then), -1 past the last
 // (each part padded to 16 bytes).  The number of slots follows from M and L alone,
 // so that grids are known on the host: a group of c tokens has ceil(c / 16) tiles,
-// together at most (M + 15 g) / 16 for g = min(L + 1, M) groups.
+// together at most (M + 15 g) / 16 for g = min(L + 1, M) groups, and t tiles have
+// ceil(t / 2) pairs, together at most (slots + g) / 2.
 #pragma once
 
 #include <cstddef>
@@ -33,11 +36,16 @@ struct PlanView {
   int32_t* order;
   int32_t* tile;
   int32_t* rows;
+  int32_t* pair;
 };
 
 __host__ __device__ inline int plan_slots(int M, int L) {
   const int g = L + 1 < M ? L + 1 : M;
   return (int)(((long long)M + 15LL * g) / kTileRows);
+}
+__host__ __device__ inline int plan_pairs(int M, int L) {
+  const int g = L + 1 < M ? L + 1 : M;
+  return (plan_slots(M, L) + g) / 2;
 }
 __host__ __device__ inline size_t plan_pad(size_t words) { return (words + 3) / 4 * 4; }
 
@@ -48,11 +56,13 @@ __host__ __device__ inline PlanView plan_view(int32_t* p, int M, int L) {
   v.order = v.first + plan_pad((size_t)L + 2);
   v.tile = v.order + plan_pad((size_t)M);
   v.rows = v.tile + plan_pad((size_t)plan_slots(M, L));
+  v.pair = v.rows + (size_t)plan_slots(M, L) * kTileRows;
   return v;
 }
 __host__ __device__ inline size_t plan_words(int M, int L) {
   const size_t s = (size_t)plan_slots(M, L);
-  return 4 + plan_pad((size_t)L + 2) + plan_pad((size_t)M) + plan_pad(s) + s * kTileRows;
+  return 4 + plan_pad((size_t)L + 2) + plan_pad((size_t)M) + plan_pad(s) + s * kTileRows +
+         plan_pad((size_t)plan_pairs(M, L));
 }
 
 }  // namespace ma

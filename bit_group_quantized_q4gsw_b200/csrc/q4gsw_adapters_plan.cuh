@@ -25,7 +25,7 @@ __device__ __forceinline__ int plan_group(int id, int L) { return id >= 0 && id 
 __global__ void __launch_bounds__(kPlanThreads)
 q4gsw_adapters_plan_kernel(const int32_t* ids, int M, int L, int32_t* plan) {
   extern __shared__ int s_hist[];          // [kPlanWarps][G], then the tiles before each group [G + 1]
-  __shared__ int s_sum[2][kPlanWarps];
+  __shared__ int s_sum[3][kPlanWarps];
   griddep_launch_dependents();
   griddep_wait();
   const PlanView P = plan_view(plan, M, L);
@@ -57,28 +57,34 @@ q4gsw_adapters_plan_kernel(const int32_t* ids, int M, int L, int32_t* plan) {
   if (threadIdx.x < L)
     for (int w = 0; w < kPlanWarps; ++w) count += s_hist[w * G + threadIdx.x];
   const int tiles = (count + kTileRows - 1) / kTileRows;
-  // inclusive scans of counts and tiles over the threads
-  int c = count, t = tiles;
+  const int pairs = (tiles + 1) / 2;
+  // inclusive scans of counts, tiles and pairs over the threads
+  int c = count, t = tiles, d = pairs;
   for (int o = 1; o < 32; o *= 2) {
-    const int cu = __shfl_up_sync(0xffffffffu, c, o), tu = __shfl_up_sync(0xffffffffu, t, o);
+    const int cu = __shfl_up_sync(0xffffffffu, c, o), tu = __shfl_up_sync(0xffffffffu, t, o),
+              du = __shfl_up_sync(0xffffffffu, d, o);
     if (lane >= o) {
       c += cu;
       t += tu;
+      d += du;
     }
   }
   if (lane == 31) {
     s_sum[0][warp] = c;
     s_sum[1][warp] = t;
+    s_sum[2][warp] = d;
   }
   __syncthreads();
-  int all_c = 0, all_t = 0;
+  int all_c = 0, all_t = 0, all_d = 0;
   for (int w = 0; w < kPlanWarps; ++w) {
     if (w == warp) {
       c += all_c;
       t += all_t;
+      d += all_d;
     }
     all_c += s_sum[0][w];
     all_t += s_sum[1][w];
+    all_d += s_sum[2][w];
   }
   if (threadIdx.x < L) {
     P.first[threadIdx.x] = c - count;
@@ -110,10 +116,14 @@ q4gsw_adapters_plan_kernel(const int32_t* ids, int M, int L, int32_t* plan) {
   const int slots = plan_slots(M, L);
   for (int i = threadIdx.x; i < slots; i += kPlanThreads) P.tile[i] = kNoTile;
   for (int i = threadIdx.x; i < slots * kTileRows; i += kPlanThreads) P.rows[i] = -1;
+  for (int i = threadIdx.x; i < plan_pairs(M, L); i += kPlanThreads) P.pair[i] = -1;
   __syncthreads();
-  if (threadIdx.x < L)
-    for (int i = 0; i < tiles; ++i) P.tile[s_tile[threadIdx.x] + i] = threadIdx.x;
+  if (threadIdx.x < L) {
+    for (int i = 0; i < tiles; ++i) P.tile[t - tiles + i] = threadIdx.x;
+    for (int i = 0; i < pairs; ++i) P.pair[d - pairs + i] = t - tiles + 2 * i;
+  }
   for (int i = threadIdx.x; i < none_tiles; i += kPlanThreads) P.tile[all_t + i] = kNoAdapter;
+  for (int i = threadIdx.x; i < (none_tiles + 1) / 2; i += kPlanThreads) P.pair[all_d + i] = all_t + 2 * i;
   // place the tokens: in the sorted order, and in the 16 rows of their group's tiles
   for (int m0 = begin; m0 < end; m0 += 32) {
     const int m = m0 + lane;

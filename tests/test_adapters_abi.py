@@ -30,8 +30,8 @@ def test_plan_arguments_and_size():
         assert lib.q4gsw_adapters_plan_bytes(M, L) == 0
         assert lib.q4gsw_adapters_plan(P, M, L, P, BIG, None) == SHAPE
     need = lib.q4gsw_adapters_plan_bytes(100, 7)
-    # head 4, first 9 -> 12, order 100, (100 + 15 * 8) / 16 = 13 -> 16 tiles, 13 * 16 rows
-    assert need == 4 * (4 + 12 + 100 + 16 + 13 * 16)
+    # head 4, first 9 -> 12, order 100, (100 + 15 * 8) / 16 = 13 -> 16 tiles, 13 * 16 rows, (13 + 8) / 2 = 10 -> 12 pairs
+    assert need == 4 * (4 + 12 + 100 + 16 + 13 * 16 + 12)
     assert lib.q4gsw_adapters_plan(P, 100, 7, P, need - 1, None) == SIZE
     assert lib.q4gsw_adapters_plan(None, 100, 7, P, need, None) == NULL
     assert lib.q4gsw_adapters_plan(P, 100, 7, None, need, None) == NULL

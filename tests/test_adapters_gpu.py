@@ -68,7 +68,8 @@ def read_plan(plan, M, L):
     at += pad(M)
     tile = p[at:at + slots]
     at += pad(slots)
-    return p[0], first, order, tile, p[at:at + 16 * slots].reshape(slots, 16)
+    pairs = (slots + min(L + 1, M)) // 2
+    return p[0], first, order, tile, p[at:at + 16 * slots].reshape(slots, 16), p[at + 16 * slots:at + 16 * slots + pairs]
 
 
 @pytest.mark.parametrize("M,L", [(1, 1), (1, 1024), (2, 3), (16, 16), (17, 1), (33, 5), (512, 8), (1000, 1024), (1021, 40),
@@ -86,7 +87,7 @@ def test_plan(M, L, kind):
         with pytest.raises(m.Q4gswError, match="INDEX"):
             m.q4gsw_device_error_check()
     m.q4gsw_device_error_check()
-    tiles, first, order, tile, rows = read_plan(plan, M, L)
+    tiles, first, order, tile, rows, pair = read_plan(plan, M, L)
     ids = clean(ids, L)
     group = np.where(ids < 0, L, ids)
     want = np.argsort(group, kind="stable")
@@ -101,6 +102,8 @@ def test_plan(M, L, kind):
         assert np.array_equal(flat[:counts[a]], want[first[a]:first[a] + counts[a]]) and (flat[counts[a]:] == -1).all()
         at += n
     assert tiles == at and (tile[at:] == -2).all()
+    starts = [i for i in range(at) if (i - int(np.argmax(tile[:at] == tile[i]))) % 2 == 0]      # every other tile of an adapter
+    assert np.array_equal(pair[:len(starts)], starts) and (pair[len(starts):] == -1).all()
 
 
 # ---------------------------------------------------------------- forward and backward
@@ -416,3 +419,49 @@ def test_a_plan_of_another_batch_computes_nothing():
         assert (d_a == 5).all() and (d_b == 5).all() and (u == 7).all()
         m.q4gsw_adapters_fwd(blob, N, K, gs, plan, a, b, x)
         m.q4gsw_device_error_check()
+
+
+@pytest.mark.parametrize("gemm", ["ts", "ss1", "ss2"])
+@pytest.mark.parametrize("M", [40, 600])
+def test_every_gemm_route_behind_the_low_rank_kernels(M, gemm):
+    m = q()
+    c = make(M, 264, 320, 32, 3, 16, runs(M, 3, M))
+    m.q4gsw_debug_pin_routes(gemm=gemm)
+    try:
+        check(c, residual=np.random.default_rng(2).standard_normal((M, 264)).astype(np.float16))
+    finally:
+        m.q4gsw_debug_pin_routes()
+
+
+@pytest.mark.parametrize("M,N,K,L,r,kind", [(3000, 72, 192, 700, 8, "random"), (5000, 136, 128, 1, 64, "one"), (4100, 264, 64, 2, 24, "runs"),
+                                            (2049, 200, 128, 130, 32, "random"), (1500, 64, 4160, 5, 40, "runs")])
+def test_many_tiles(M, N, K, L, r, kind):
+    # the ring kernels: pairs with one and two tiles, one and two adapters to a CTA, token splits of the gradients
+    g = np.random.default_rng(M)
+    ids = {"random": g.integers(-1, L, M), "one": np.zeros(M), "runs": runs(M, L, M)}[kind]
+    check(make(M, N, K, 32, L, r, ids), residual=g.standard_normal((M, N)).astype(np.float16))
+
+
+def test_two_streams_share_a_plan_and_the_adapters():
+    m = q()
+    c = make(700, 264, 512, 32, 4, 32, runs(700, 4, 1))
+    args, s = head(c), cuda(c["scale"])
+    xs = [torch.randn(700, 512, device="cuda").half() for _ in range(2)]
+    d_y = cuda(c["d_y"])
+
+    def both(x):
+        y, u = m.q4gsw_adapters_fwd(*args, x, scale=s, save_u=True)
+        return (y, u, *m.q4gsw_adapters_bwd(*args, x, u, d_y, scale=s))
+
+    want = [both(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for k, side in enumerate(streams):
+            with torch.cuda.stream(side):
+                got[k].append(both(xs[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for run in got[k]:
+            assert all(torch.equal(v, w) for v, w in zip(run, want[k]))

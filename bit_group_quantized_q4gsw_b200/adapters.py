@@ -259,6 +259,7 @@ class GradSet:
     def __init__(self, grads, outs, table, index: int):
         self.grads, self.outs, self.table, self.index = grads, outs, table, index
         self.table_bytes, self.table_ptr = table.numel(), table.data_ptr()
+        self.long = self.table_bytes > 64 * 32      # records of 32 bytes; up to 64 need no workspace
 
 
 def _elements(t, name: str, index: int):
@@ -318,22 +319,23 @@ def q4gsw_grad_set(grads, outs=None) -> GradSet:
     return GradSet(grads, outs, table, index)
 
 
-_grad_bytes = None
+_grad_bytes = None   # of a workspace
 
 
 def _grad_call(name: str, grads: GradSet, head, norm, workspace):
     global _grad_bytes
     if not isinstance(grads, GradSet):
         raise TypeError("grads must be a GradSet (q4gsw_grad_set)")
-    if _grad_bytes is None:
-        _grad_bytes = int(library().q4gsw_grad_workspace_bytes())
     norm, pn = _out(norm, "norm", _f32, (1,), grads.index)
-    if workspace is None:
-        workspace = _new(_grad_bytes, _u8, grads.index)
-        pw, nbytes = workspace.data_ptr(), _grad_bytes
-    else:
+    pw, nbytes = None, 0
+    if workspace is not None:
         nbytes = workspace.numel()
         pw = _need(workspace, "workspace", _u8, (nbytes,), grads.index)
+    elif grads.long:
+        if _grad_bytes is None:
+            _grad_bytes = int(library().q4gsw_grad_workspace_bytes())
+        workspace, nbytes = _new(_grad_bytes, _u8, grads.index), _grad_bytes
+        pw = workspace.data_ptr()
     _call(name, grads.index, grads.table_ptr, grads.table_bytes, *head, pn, pw, nbytes)
     return norm
 

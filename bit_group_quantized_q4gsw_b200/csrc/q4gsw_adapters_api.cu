@@ -325,10 +325,11 @@ size_t q4gsw_grad_workspace_bytes(void) { return grad_workspace_bytes(); }
 static q4gsw_status check_grad_call(const void* table, size_t table_bytes, float inv_scale, const float* norm,
                                     const void* workspace, size_t workspace_bytes) {
   if (!std::isfinite(inv_scale)) return Q4GSW_ERR_SHAPE;
-  if (!table || !norm || !workspace) return Q4GSW_ERR_NULL;
+  const bool few = table_bytes <= kGradRecordBytes * kGradFewRecords;
+  if (!table || !norm || (!workspace && !few)) return Q4GSW_ERR_NULL;
   if (!aligned16(table) || !word(norm) || !aligned16(workspace)) return Q4GSW_ERR_ALIGN;
   if (table_bytes < kGradRecordBytes || table_bytes % kGradRecordBytes || table_bytes / kGradRecordBytes > 0x7fffffff ||
-      workspace_bytes < grad_workspace_bytes())
+      (!few && workspace_bytes < grad_workspace_bytes()))
     return Q4GSW_ERR_SIZE;
   return Q4GSW_OK;
 }
@@ -338,8 +339,10 @@ q4gsw_status q4gsw_grad_norm(const void* table, size_t table_bytes, float inv_sc
   return guarded([&] {
     const q4gsw_status st = check_grad_call(table, table_bytes, inv_scale, norm, workspace, workspace_bytes);
     if (st != Q4GSW_OK) return st;
-    set_route("grad_norm launches=2");
-    return from_cuda(launch_grad_norm(table, table_bytes, inv_scale, norm, workspace, stream));
+    char route[160] = "";
+    const cudaError_t e = launch_grad_norm(table, table_bytes, inv_scale, norm, workspace, stream, route, sizeof(route));
+    set_route(route);
+    return from_cuda(e);
   });
 }
 
@@ -349,8 +352,10 @@ q4gsw_status q4gsw_grad_clip(const void* table, size_t table_bytes, float max_no
     if (!(max_norm > 0.f)) return Q4GSW_ERR_SHAPE;
     const q4gsw_status st = check_grad_call(table, table_bytes, inv_scale, norm, workspace, workspace_bytes);
     if (st != Q4GSW_OK) return st;
-    set_route("grad_clip launches=2");
-    return from_cuda(launch_grad_clip(table, table_bytes, max_norm, inv_scale, norm, workspace, stream));
+    char route[160] = "";
+    const cudaError_t e = launch_grad_clip(table, table_bytes, max_norm, inv_scale, norm, workspace, stream, route, sizeof(route));
+    set_route(route);
+    return from_cuda(e);
   });
 }
 

@@ -230,10 +230,11 @@ void grad_table_fill(int count, const void* const* grads, const int* half_grads,
                      const int* half_outs, const int64_t* sizes, void* table, size_t table_bytes);
 size_t grad_workspace_bytes();
 constexpr size_t kGradRecordBytes = 32;
+constexpr int kGradFewRecords = 64;      // up to here one launch, without a workspace
 cudaError_t launch_grad_norm(const void* table, size_t table_bytes, float inv_scale, float* norm, void* workspace,
-                             cudaStream_t stream);
+                             cudaStream_t stream, char* route, int route_len);
 cudaError_t launch_grad_clip(const void* table, size_t table_bytes, float max_norm, float inv_scale, float* norm,
-                             void* workspace, cudaStream_t stream);
+                             void* workspace, cudaStream_t stream, char* route, int route_len);
 
 // Embedding rows out[t] = dequant(W)[indices[t]] (fp32); an index outside
 // [0, N) gives a zero row and sets kIndexErrorBit in the device error word.

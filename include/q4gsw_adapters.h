@@ -171,15 +171,16 @@ Q4GSW_API size_t q4gsw_grad_table_bytes(int count, const int64_t *sizes);
 Q4GSW_API q4gsw_status q4gsw_grad_table(int count, const void *const *grads, const int *half_grads, void *const *outs,
                               const int *half_outs, const int64_t *sizes, void *table, size_t table_bytes);
 
-/* Bytes of the device workspace of the calls below. */
+/* Bytes of the device workspace of the calls below, which they need for tables of
+ * more than 64 records (NULL else). */
 Q4GSW_API size_t q4gsw_grad_workspace_bytes(void);
 
-/* norm fp32 [1] (4-byte aligned), two launches.  table: device copy of the
+/* norm fp32 [1] (4-byte aligned), two launches (one up to 64 records).  table: device copy of the
  * table; table_bytes as above.  inv_scale finite (Q4GSW_ERR_SHAPE else). */
 Q4GSW_API q4gsw_status q4gsw_grad_norm(const void *table, size_t table_bytes, float inv_scale, float *norm,
                              void *workspace, size_t workspace_bytes, q4gsw_stream_t stream);
 
-/* The norm, and every out, two launches (a table made without outs gives the norm alone).
+/* The norm, and every out, launches as above (a table made without outs gives the norm alone).
  * max_norm > 0 (Q4GSW_ERR_SHAPE else; infinity: never clipped).  A tensor that is
  * its own out and whose factor is 1 is left alone. */
 Q4GSW_API q4gsw_status q4gsw_grad_clip(const void *table, size_t table_bytes, float max_norm, float inv_scale, float *norm,

@@ -149,6 +149,10 @@ def test_grad_call_arguments():
         tail = (a["norm"], a["ws"], a["wb"], None)
         assert lib.q4gsw_grad_norm(a["table"], a["tb"], a["inv"], *tail) == st, kw
         assert lib.q4gsw_grad_clip(a["table"], a["tb"], 1.0, a["inv"], *tail) == st, kw
+    # up to 64 records no workspace is looked at; one more needs it (and its size)
+    assert lib.q4gsw_grad_norm(P, 65 * 32, 1.0, P, None, 0, None) == NULL
+    assert lib.q4gsw_grad_clip(P, 65 * 32, 1.0, 1.0, P, P, 0, None) == SIZE
+    assert lib.q4gsw_grad_norm(P, 64 * 32, 1.0, P, P + 8, 0, None) == ALIGN
     for m in (0.0, -1.0, float("nan")):
         assert lib.q4gsw_grad_clip(P, 1 << 20, m, 1.0, P, P, w, None) == SHAPE
 

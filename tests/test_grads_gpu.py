@@ -203,3 +203,17 @@ def test_a_training_step_of_a_feed_forward_block():
     assert abs(norm.item() - total) <= 1e-6 * total
     for k in ("w1", "a", "b", "w2", "w3"):
         assert torch.allclose(mine[k], want[k] * min(1.0, 0.1 / (total + 1e-6)), rtol=1e-6, atol=0)
+
+
+@pytest.mark.parametrize("n", [1024 * 55, 1024 * 56, 1024 * 57, 1024 * 64, 1024 * 65 + 1])
+def test_around_the_length_where_one_launch_becomes_two(n):
+    # a record more than the tensor's own may stand in the table (the largest offset it may start at)
+    m = q()
+    g = lists([n - 5000, 5000], [0, 1], n)
+    check(g, [torch.zeros(n - 5000, device="cuda"), torch.zeros(5000, device="cuda")], max_norm=2.0)
+    s = m.q4gsw_grad_set(g)
+    a = m.q4gsw_grad_norm(s)
+    one = "launches=1" in m.q4gsw_last_route()
+    assert one == (s.table_bytes <= 64 * 32)
+    ws = torch.empty(8192, dtype=torch.uint8, device="cuda")
+    assert torch.equal(m.q4gsw_grad_norm(s, workspace=ws), a)

@@ -343,7 +343,8 @@ q4gsw_norms_bwd_kernel(const NormsArgs a) {
     float s[3] = {add_up(q0), add_up(q1), add_up(q2)};
     row_sum3<R>(s, buf, turn);
     const float r2 = rsqrtf(s[0] * inv_d + a.eps), r1 = a.w_post ? rsqrtf(s[2] * inv_d + a.eps) : 1.f;
-    const float pull = a.d_x ? r2 * r2 * r2 * (s[1] * inv_d) : 0.f;
+    // (in this order: a row of zeros has no pull, however large its factor's cube is)
+    const float pull = a.d_x ? r2 * (r2 * (r2 * (s[1] * inv_d))) : 0.f;
     unsigned long long q4 = 0;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
@@ -388,7 +389,7 @@ q4gsw_norms_bwd_kernel(const NormsArgs a) {
     if (!a.block) continue;
     float pull_b = 0.f;
     if (a.w_post) {
-      pull_b = r1 * r1 * r1 * (row_sum<R>(add_up(q4), buf, turn) * inv_d);
+      pull_b = r1 * (r1 * (r1 * (row_sum<R>(add_up(q4), buf, turn) * inv_d)));
     }
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {

@@ -114,6 +114,14 @@ def test_rows_of_zeros_and_extreme_rows():
     check(c)
 
 
+@pytest.mark.parametrize("D", [512, 16384])
+def test_rows_of_zeros_and_an_eps_whose_factor_leaves_fp32_in_its_cube(D):
+    c = make(4, D, eps=1e-30)               # rsqrt(eps)^3 = 1e45
+    c["h"][1], c["block"][1] = 0, 0         # both norms' rows
+    c["block"][2] = 0
+    check(c)
+
+
 def test_a_row_that_is_not_finite_stays_alone():
     m = q()
     c = make(8, 264)

@@ -258,6 +258,8 @@ class GradSet:
 
     def __init__(self, grads, outs, table, index: int):
         self.grads, self.outs, self.table, self.index = grads, outs, table, index
+        # the table has addresses: the storages live as long as it, also where a tensor is given another one
+        self._storages = [t.detach() for t in grads] + ([] if outs is grads else [t.detach() for t in outs])
         self.table_bytes, self.table_ptr = table.numel(), table.data_ptr()
         self.long = self.table_bytes > 64 * 32      # records of 32 bytes; up to 64 need no workspace
 

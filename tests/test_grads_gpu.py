@@ -81,6 +81,20 @@ def test_values_whose_squares_leave_fp32():
     check(lists([4], [0], sigma=1e-44), max_norm=1.0)          # subnormal gradients
 
 
+def test_a_set_keeps_the_storages_it_has_addresses_of():
+    m = q()
+    g = lists([3000], [0])
+    s, old = m.q4gsw_grad_set(g), g[0].detach()
+    where, copy = old.data_ptr(), old.clone()
+    del old
+    g[0].data = torch.zeros(3000, device="cuda")          # another storage; the set has the old one
+    torch.cuda.synchronize()
+    fresh = [torch.zeros(3000, device="cuda") for _ in range(8)]
+    assert all(t.data_ptr() != where for t in fresh)
+    want = float(copy.double().pow(2).sum().sqrt())
+    assert abs(float(m.q4gsw_grad_norm(s)) - want) <= want * 2 ** -23
+
+
 def test_factor_of_one_leaves_the_gradients_alone():
     m = q()
     g = lists([1000, 50], [0, 1])

@@ -11,8 +11,8 @@
 // and with either kind of scales.  The first kernel lets the next start only behind its
 // own wait; the product, launched behind them, then knows its activations to be
 // complete, reads them at once and waits for the low-rank term in its epilogue alone: one
-// token of 8192 x 2048 takes 6.8 us, as the product without an adapter does (10.4 with
-// two kernels in a row in front of it).
+// token of 8192 x 2048 takes 7.3 us (10.4 with two kernels in a row in front of it and a
+// product that waits for them).
 //
 // The intermediate stays in fp32: rounded to fp16 it would put 2^-11 of error into
 // fp32 gradients, and small gradients would fall below fp16's range.  It goes to the
@@ -779,7 +779,7 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
 // tokens (their columns, and their rows of q) go through a ring in shared memory; each
 // rank's q of a chunk is divided by a power of two near its largest value and split
 // into two fp16 parts, once for all warps, and the chunk's sums are scaled back when
-// they are added to the fp32 registers: 2^-24 of the largest q of the chunk is lost, no
+// they are added to the fp32 registers: 2^-23 of the largest q of the chunk is lost, no
 // range, and the tensor cores' own sums are two steps long.  The Z CTAs of a cluster
 // take every Z-th chunk, and their sums are added through distributed shared memory in
 // rank order.
@@ -821,8 +821,17 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
   const int adapter = blockIdx.y, Z = gridDim.z, z = blockIdx.z;
   const int base = W * group;
   const int begin = ld_int(P.first + adapter), end = ld_int(P.first + adapter + 1);
-  if (begin == end && accumulate) return;             // the whole cluster
   float* dst = a.out + (size_t)adapter * R * a.C;
+  if (begin == end) {                                 // no tokens: zeros (the whole cluster leaves here)
+    if (accumulate) return;
+    for (int e = threadIdx.x + z * kThreads; e < W * R / 4; e += Z * kThreads) {
+      const int row = BY_ROWS ? e / (R / 4) : e / (W / 4), x4 = BY_ROWS ? e % (R / 4) : e % (W / 4);
+      if ((BY_ROWS ? base + row : base + 4 * x4) < a.C)
+        *reinterpret_cast<float4*>(BY_ROWS ? dst + (size_t)(base + row) * R + 4 * x4
+                                           : dst + (size_t)row * a.C + base + 4 * x4) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
   const uint32_t ring = shared_address(smem), parts = ring + T::RING;
   float* sums = reinterpret_cast<float*>(smem);
   const int chunks = (end - begin + kChunk - 1) / kChunk;

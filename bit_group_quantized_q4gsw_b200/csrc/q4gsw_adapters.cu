@@ -541,13 +541,14 @@ constexpr int kUpWarps = 4, kUpThreads = 32 * kUpWarps;
 template <bool BY_ROWS, int RJ>
 struct UpRing {
   static constexpr int R = 8 * RJ, KT = (RJ + 1) / 2;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = 2;
   static constexpr int ROWS = BY_ROWS ? 64 : 16 * KT;                // rows of a block (ranks padded to 16)
   static constexpr int CHUNKS = BY_ROWS ? 2 * KT : 8;                // 16-byte chunks of a row
   static constexpr int PITCH = 16 * (CHUNKS + 1);                    // an odd number of them
   static constexpr int REGION = ROWS * PITCH, STAGE = 2 * REGION;
   static constexpr int T_PITCH = 72;                                 // of a warp's 16 x 64 sums, floats
-  static constexpr int BYTES = STAGES * STAGE + kUpWarps * kTileRows * T_PITCH * 4;
+  static constexpr int BYTES = STAGES * STAGE + kUpWarps * kTileRows * T_PITCH * 2;    // without a residual: as fp16
+  static constexpr int BYTES_RES = STAGES * STAGE + kUpWarps * kTileRows * T_PITCH * 4;
 };
 
 template <bool BY_ROWS, int RJ>
@@ -570,6 +571,26 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
   const int slot = (warp < 2 ? s0 : s1) + (warp & 1), theirs = warp < 2 ? a0 : a1;
   const int mine = theirs == kNoTile || slot >= plan_slots(M, L) || ld_int(P.tile + slot) != theirs ? kNoTile : theirs;
   const int first = blockIdx.y * blocks_per_cta, last = min(first + blocks_per_cta, (C + 63) / 64);
+  const uint32_t ring = shared_address(up_smem);
+  const bool other = a1 >= 0 && a1 != a0;  // a second matrix, in the second region
+  const uint32_t region = mine == a1 && other ? (uint32_t)U::REGION : 0u;
+  auto issue = [&](int b) {
+    if (b < last) {
+      const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE;
+      for (int e = threadIdx.x; e < U::ROWS * U::CHUNKS; e += kUpThreads) {
+        const int row = e / U::CHUNKS, k = e % U::CHUNKS;
+        // by rows: column 64 b + row, ranks 8 k ..; else rank row, columns 64 b + 8 k ..
+        const bool in = BY_ROWS ? 64 * b + row < C && k < RJ : row < R && 64 * b + 8 * k < C;
+        const size_t from = BY_ROWS ? (size_t)(64 * b + row) * R + 8 * k : (size_t)row * C + 64 * b + 8 * k;
+        const uint32_t to_smem = st + row * U::PITCH + 16 * k;
+        copy_16(to_smem, proj + (in ? (size_t)a0 * R * C + from : 0), in);
+        if (other) copy_16(to_smem + U::REGION, proj + (in ? (size_t)a1 * R * C + from : 0), in);
+      }
+    }
+    cp_async_commit();
+  };
+  if (a0 >= 0)
+    for (int i = 0; i < U::STAGES - 1; ++i) issue(first + i);
   const int32_t* rows = P.rows + (size_t)(mine == kNoTile ? s0 : slot) * kTileRows;
   const int m[2] = {mine == kNoTile ? -1 : ld_int(rows + g), mine == kNoTile ? -1 : ld_int(rows + g + 8)};
   UpTile<RJ> q;
@@ -584,8 +605,8 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
   int to[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) to[k] = mine == kNoTile ? -1 : ld_int(rows + 4 * k + lane / 8);
-  const uint32_t ring = shared_address(up_smem);
   float* turn = reinterpret_cast<float*>(up_smem + U::STAGES * U::STAGE) + warp * kTileRows * U::T_PITCH;
+  __half* turn_half = reinterpret_cast<__half*>(up_smem + U::STAGES * U::STAGE) + warp * kTileRows * U::T_PITCH;
   auto write = [&](int b, bool sums) {
     const int c = 64 * b + 8 * (lane % 8);
     if (c >= C) return;                    // C % 8 == 0
@@ -615,24 +636,6 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
   if (mine == kNoAdapter)                  // the residual, or zeros
     for (int b = first; b < last; ++b) write(b, false);
   if (a0 < 0) return;                      // (sorted: the second pair has no adapter, either)
-  const bool other = a1 >= 0 && a1 != a0;  // a second matrix, in the second region
-  const uint32_t region = mine == a1 && other ? (uint32_t)U::REGION : 0u;
-  auto issue = [&](int b) {
-    if (b < last) {
-      const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE;
-      for (int e = threadIdx.x; e < U::ROWS * U::CHUNKS; e += kUpThreads) {
-        const int row = e / U::CHUNKS, k = e % U::CHUNKS;
-        // by rows: column 64 b + row, ranks 8 k ..; else rank row, columns 64 b + 8 k ..
-        const bool in = BY_ROWS ? 64 * b + row < C && k < RJ : row < R && 64 * b + 8 * k < C;
-        const size_t from = BY_ROWS ? (size_t)(64 * b + row) * R + 8 * k : (size_t)row * C + 64 * b + 8 * k;
-        const uint32_t to_smem = st + row * U::PITCH + 16 * k;
-        copy_16(to_smem, proj + (in ? (size_t)a0 * R * C + from : 0), in);
-        if (other) copy_16(to_smem + U::REGION, proj + (in ? (size_t)a1 * R * C + from : 0), in);
-      }
-    }
-    cp_async_commit();
-  };
-  for (int i = 0; i < U::STAGES - 1; ++i) issue(first + i);
   for (int b = first; b < last; ++b) {
     cp_async_wait<U::STAGES - 2>();
     __syncthreads();                     // the block has landed, and the one refilled below has been used by all
@@ -663,6 +666,22 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
         }
     }
     __syncwarp();                        // the lanes have read the block before
+    if (!res) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<uint32_t*>(turn_half + (g + 8 * h) * U::T_PITCH + 8 * i + 2 * t) =
+              h2_as_u32(__floats2half2_rn(q.back[h] * acc[i][2 * h], q.back[h] * acc[i][2 * h + 1]));
+      __syncwarp();
+      const int c = 64 * b + 8 * (lane % 8);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (to[k] >= 0 && c < C)
+          *reinterpret_cast<uint4*>(out + (size_t)to[k] * C + c) =
+              *reinterpret_cast<const uint4*>(turn_half + (4 * k + lane / 8) * U::T_PITCH + 8 * (lane % 8));
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -788,8 +807,9 @@ constexpr int kChunk = 32;      // tokens
 template <int RJ>
 struct GradTile {
   static constexpr int R = 8 * RJ, MT = (RJ + 1) / 2;                // tensor-core tiles of 16 ranks
-  static constexpr int CW = MT <= 2 ? 32 : 16;                       // columns of a warp
-  static constexpr int W = kWarps * CW;
+  static constexpr int RW = MT == 4 ? 2 : 1, WT = MT / RW;            // warps beside each other over the ranks, tiles of each
+  static constexpr int CW = MT == 3 ? 16 : 32;                       // columns of a warp
+  static constexpr int W = kWarps / RW * CW;
   static constexpr int STAGES = 3;
   static constexpr int X_PITCH = 2 * W + 16;                         // an odd number of 16-byte chunks
   static constexpr int X_BYTES = kChunk * X_PITCH, Q_BYTES = kChunk * R * 4;
@@ -814,9 +834,10 @@ template <bool BY_ROWS, int RJ>
 __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P, int group, int accumulate,
                                            unsigned char* smem, unsigned int* s_top) {
   using T = GradTile<RJ>;
-  constexpr int R = T::R, MT = T::MT, CW = T::CW, W = T::W;
+  constexpr int R = T::R, WT = T::WT, CW = T::CW, W = T::W;
   constexpr int PITCH = (BY_ROWS ? R : W) + 4;        // of the sums in shared memory, floats
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) / T::RW;      // of the columns
+  const int rank0 = 16 * WT * ((threadIdx.x >> 5) % T::RW);                  // this warp's ranks
   const int g = lane >> 2, t = lane & 3;
   const int adapter = blockIdx.y, Z = gridDim.z, z = blockIdx.z;
   const int base = W * group;
@@ -836,9 +857,9 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
   float* sums = reinterpret_cast<float*>(smem);
   const int chunks = (end - begin + kChunk - 1) / kChunk;
   const int mine = chunks > z ? (chunks - z + Z - 1) / Z : 0;      // chunks z, z + Z, ..
-  float total[MT][CW / 8][4];
+  float total[WT][CW / 8][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < WT; ++m)
 #pragma unroll
     for (int i = 0; i < CW / 8; ++i)
 #pragma unroll
@@ -888,10 +909,12 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
     for (int e = threadIdx.x; e < 2 * kChunk * 8; e += kThreads)
       *reinterpret_cast<__half*>(smem + T::RING + (e / 8) * T::H_PITCH + 2 * (R + e % 8)) = __float2half_rn(0.f);
   }
+  if (threadIdx.x < R) s_top[threadIdx.x] = 0u;       // of the first chunk
   for (int u = 0; u < mine; ++u) {
     cp_async_wait<T::STAGES - 2>();
-    if (threadIdx.x < R) s_top[threadIdx.x] = 0u;
     __syncthreads();                     // the chunk has landed; the parts and the stage refilled below have been used
+    unsigned int* top = s_top + u % 2 * R;
+    if (threadIdx.x < R) s_top[(u + 1) % 2 * R + threadIdx.x] = 0u;
     issue(u + T::STAGES - 1);
     look_up(u + T::STAGES);
     const uint32_t st = ring + (uint32_t)(u % T::STAGES) * T::STAGE;
@@ -906,16 +929,16 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
       v[i] = q[threadIdx.x + i * kThreads];
       const uint32_t size = __float_as_uint(v[i]) & 0x7fffffffu;
       if (kOneRank) most = max(most, size);
-      else atomicMax(&s_top[(threadIdx.x + i * kThreads) % R], size);
+      else atomicMax(&top[(threadIdx.x + i * kThreads) % R], size);
     }
-    if (kOneRank) atomicMax(&s_top[threadIdx.x % R], most);
+    if (kOneRank) atomicMax(&top[threadIdx.x % R], most);
     __syncthreads();
     float down = 0.f;
-    if (kOneRank) down = __uint_as_float((uint32_t)(127 - exponent_of(s_top[threadIdx.x % R])) << 23);
+    if (kOneRank) down = __uint_as_float((uint32_t)(127 - exponent_of(top[threadIdx.x % R])) << 23);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = threadIdx.x + i * kThreads;
-      if (!kOneRank) down = __uint_as_float((uint32_t)(127 - exponent_of(s_top[e % R])) << 23);
+      if (!kOneRank) down = __uint_as_float((uint32_t)(127 - exponent_of(top[e % R])) << 23);
       const float w = v[i] * down;
       const __half h = __float2half_rn(w);
       unsigned char* at = smem + T::RING + (e / R) * T::H_PITCH + 2 * (e % R);
@@ -923,9 +946,9 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
       *reinterpret_cast<__half*>(at + T::H_BYTES) = __float2half_rn(isinf(w) ? 0.f : w - __half2float(h));
     }
     __syncthreads();
-    float acc[MT][CW / 8][4];
+    float acc[WT][CW / 8][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < WT; ++m)
 #pragma unroll
       for (int i = 0; i < CW / 8; ++i)
 #pragma unroll
@@ -940,11 +963,11 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
 #pragma unroll
       for (int part = 1; part >= 0; --part)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int m = 0; m < WT; ++m) {
           // ranks 0-7, 8-15 at tokens 0-7, then at 8-15
           uint32_t af[4];
-          ldmatrix4_trans(af, parts + part * T::H_BYTES + (16 * k + 8 * (lane / 16) + lane % 8) * T::H_PITCH + 32 * m +
-                                  16 * (lane / 8 % 2));
+          ldmatrix4_trans(af, parts + part * T::H_BYTES + (16 * k + 8 * (lane / 16) + lane % 8) * T::H_PITCH + 2 * rank0 +
+                                  32 * m + 16 * (lane / 8 % 2));
 #pragma unroll
           for (int i = 0; i < CW / 8; ++i) {
             const uint32_t bf[2] = {xf[i / 2][2 * (i % 2)], xf[i / 2][2 * (i % 2) + 1]};
@@ -953,28 +976,27 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
         }
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < WT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int j = 16 * m + 8 * h + g;
-        const float back = j < R ? __uint_as_float((uint32_t)(127 + exponent_of(s_top[j])) << 23) : 0.f;
+        const int j = rank0 + 16 * m + 8 * h + g;
+        const float back = j < R ? __uint_as_float((uint32_t)(127 + exponent_of(top[j])) << 23) : 0.f;
 #pragma unroll
         for (int i = 0; i < CW / 8; ++i) {
           total[m][i][2 * h] = fmaf(back, acc[m][i][2 * h], total[m][i][2 * h]);
           total[m][i][2 * h + 1] = fmaf(back, acc[m][i][2 * h + 1], total[m][i][2 * h + 1]);
         }
       }
-    __syncthreads();                     // every thread has read s_top
   }
   cp_async_wait<0>();
   __syncthreads();                       // the ring is free
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < WT; ++m)
 #pragma unroll
     for (int i = 0; i < CW / 8; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int j = 16 * m + g + 8 * (k >> 1), c = CW * warp + 8 * i + 2 * t + (k & 1);
+        const int j = rank0 + 16 * m + g + 8 * (k >> 1), c = CW * warp + 8 * i + 2 * t + (k & 1);
         if (j < R) sums[BY_ROWS ? c * PITCH + j : j * PITCH + c] = total[m][i][k];
       }
   cg::cluster_group cluster = cg::this_cluster();
@@ -1008,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 q4gsw_adapters_grad_kernel(const GradSide da, const GradSide db, const int32_t* plan, int M, int L, int groups_a,
                            int accumulate) {
   extern __shared__ __align__(16) unsigned char grad_smem[];
-  __shared__ unsigned int s_top[8 * RJ];
+  __shared__ unsigned int s_top[2 * 8 * RJ];     // of this chunk and the next
   griddep_launch_dependents();
   griddep_wait();
   const PlanView P = plan_view(const_cast<int32_t*>(plan), M, L);
@@ -1089,10 +1111,10 @@ static cudaError_t up_form(cudaLaunchConfig_t& cfg, const float* inter, const __
   auto kernel = ma::q4gsw_adapters_up_kernel<BY_ROWS, RJ>;
   static PerDeviceOnce once;
   const cudaError_t e = once_per_device(once, current_device(), [&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, U::BYTES);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, U::BYTES_RES);
   });
   if (e != cudaSuccess) return e;
-  cfg.dynamicSmemBytes = U::BYTES;
+  cfg.dynamicSmemBytes = res ? U::BYTES_RES : U::BYTES;
   return cudaLaunchKernelEx(&cfg, kernel, inter, p, scale, ad.plan, res, out, M, ad.L, C, per);
 }
 

@@ -233,13 +233,14 @@ __device__ __forceinline__ void down_park(const float (&acc)[RJ][4], float (*red
 // of the tiles' tokens and of the adapter's matrix go through a ring in shared memory
 // (cp.async), from which the warps take their fragments by ldmatrix: the matrix is read
 // once a CTA.  The warps of a tile and the KS CTAs of the cluster (grid = (pairs, KS))
-// split the contraction; sums go to fp32 registers stage by stage (the tensor cores
+// split the contraction; sums go to fp32 registers every few stages (the tensor cores
 // truncate theirs), and the warps' and the CTAs' are added in a fixed order.
 constexpr int kDownTiles = 2;
 template <bool BY_ROWS, int RJ>
 struct DownRing {
   static constexpr int R = 8 * RJ, WT = kDownTiles, WK = kWarps / WT;
   static constexpr int COLS = 128;                                   // columns of a stage
+  static constexpr int FLUSH = 4;                                    // stages whose sums stay in the tensor cores
   static constexpr int STAGES = 3;
   // rows of 16-byte chunks, an odd number of them: ldmatrix meets no bank twice
   static constexpr int X_PITCH = 2 * COLS + 16;
@@ -273,10 +274,11 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
   const int g = lane >> 2, t = lane & 3;
   const int slot0 = ld_int(P.pair + blockIdx.x);
   if (!plan_fits(P, M, L, error) || slot0 < 0) return;      // the whole cluster
-  const int adapter = ld_int(P.tile + slot0);
-  const bool two = slot0 + 1 < plan_slots(M, L) && ld_int(P.tile + slot0 + 1) == adapter;
-  if (threadIdx.x < WT * kTileRows)
-    s_row[threadIdx.x] = two || threadIdx.x < kTileRows ? ld_int(P.rows + (size_t)slot0 * kTileRows + threadIdx.x) : -1;
+  const bool more = slot0 + 1 < plan_slots(M, L);           // (loads that do not wait for one another)
+  const int adapter = ld_int(P.tile + slot0), behind = more ? ld_int(P.tile + slot0 + 1) : kNoTile;
+  int my_row = -1;
+  if (threadIdx.x < (more ? WT : 1) * kTileRows) my_row = ld_int(P.rows + (size_t)slot0 * kTileRows + threadIdx.x);
+  if (threadIdx.x < WT * kTileRows) s_row[threadIdx.x] = behind == adapter || threadIdx.x < kTileRows ? my_row : -1;
   __syncthreads();
   if (adapter < 0) {
     for (int e = threadIdx.x + ks * kThreads; e < WT * kTileRows * R; e += KS * kThreads)
@@ -292,46 +294,63 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
   for (int j = 0; j < RJ; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) total[j][e] = 0.f;
+  // what this thread copies of a stage: 16 bytes of a row of each tile, and of the matrix rows
+  // 16 apart (by rows) or pieces kThreads apart of the stage's contiguous columns
+  const int q16 = threadIdx.x % 16, row16 = threadIdx.x / 16;
+  const __half* x_from[WT];
+#pragma unroll
+  for (int i = 0; i < WT; ++i) {
+    const int m = s_row[16 * i + row16];
+    x_from[i] = m >= 0 ? act + (size_t)m * C + 8 * q16 : nullptr;
+  }
   const __half* mat = proj + (size_t)adapter * R * C;
-  auto issue = [&](int it) {
+  const __half* p_from = BY_ROWS ? mat + (size_t)row16 * C + 8 * q16 : mat + 8 * threadIdx.x;
+  auto issue = [&](int it, uint32_t st) {
     if (it < it_end) {
-      const uint32_t st = ring + (uint32_t)(it % D::STAGES) * D::STAGE;
       const int c0 = it * D::COLS;
-      const int q = threadIdx.x % 16, c = c0 + 8 * q;         // C % 8 == 0: a chunk is wholly in or out
+      const bool in = c0 + 8 * q16 < C;                       // C % 8 == 0: a chunk is wholly in or out
 #pragma unroll
       for (int i = 0; i < WT; ++i) {
-        const int row = 16 * i + threadIdx.x / 16, m = s_row[row];
-        const bool in = m >= 0 && c < C;
-        copy_16(st + row * D::X_PITCH + 16 * q, act + (in ? (size_t)m * C + c : 0), in);
+        const bool live = in && x_from[i];
+        copy_16(st + (16 * i + row16) * D::X_PITCH + 16 * q16, live ? x_from[i] + c0 : act, live);
       }
       const uint32_t sp = st + D::X_BYTES;
       if constexpr (BY_ROWS) {
-        for (int row = threadIdx.x / 16; row < R; row += kThreads / 16)
-          copy_16(sp + row * D::P_PITCH + 16 * q, mat + (c < C ? (size_t)row * C + c : 0), c < C);
+        const __half* from = in ? p_from + c0 : proj;
+        const size_t step = in ? (size_t)16 * C : 0;
+#pragma unroll
+        for (int i = 0; i < (R + 15) / 16; ++i)
+          if (R % 16 == 0 || row16 + 16 * i < R)
+            copy_16(sp + (row16 + 16 * i) * D::P_PITCH + 16 * q16, from + i * step, in);
       } else {
-        for (int e = threadIdx.x; e < D::P_ROWS * RJ; e += kThreads) {
-          const int row = e / RJ, k = e % RJ;
-          const bool in = c0 + row < C;
-          copy_16(sp + row * D::P_PITCH + 16 * k, mat + (in ? (size_t)(c0 + row) * R + 8 * k : 0), in);
+        const __half* from = p_from + (size_t)c0 * R;
+#pragma unroll
+        for (int i = 0; i < (D::P_ROWS * RJ + kThreads - 1) / kThreads; ++i) {
+          const int e = threadIdx.x + i * kThreads;
+          if (D::P_ROWS * RJ % kThreads && e >= D::P_ROWS * RJ) break;
+          const bool live = c0 + e / RJ < C;
+          copy_16(sp + e / RJ * D::P_PITCH + 16 * (e % RJ), live ? from + 8 * i * kThreads : proj, live);
         }
       }
     }
     cp_async_commit();
   };
-  for (int i = 0; i < D::STAGES - 1; ++i) issue(it_begin + i);
-  for (int it = it_begin; it < it_end; ++it) {
+  uint32_t used = ring, filled = ring;      // the stages' places, in turn
+  auto next = [&](uint32_t st) { return st + D::STAGE == ring + D::STAGES * D::STAGE ? ring : st + D::STAGE; };
+  for (int i = 0; i < D::STAGES - 1; ++i, filled = next(filled)) issue(it_begin + i, filled);
+  float acc[RJ][4];
+#pragma unroll
+  for (int j = 0; j < RJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+  for (int it = it_begin; it < it_end; ++it, used = next(used), filled = next(filled)) {
     cp_async_wait<D::STAGES - 2>();
     __syncthreads();                     // the stage has landed, and the one refilled below has been used by all
-    issue(it + D::STAGES - 1);
-    const uint32_t st = ring + (uint32_t)(it % D::STAGES) * D::STAGE;
+    issue(it + D::STAGES - 1, filled);
+    const uint32_t st = used;
     // rows 0-7, 8-15 at columns 0-7, then both at columns 8-15 of a step of 16
     const uint32_t xa = st + (my_tile * kTileRows + lane % 16) * D::X_PITCH + 16 * (lane / 16);
     const uint32_t pa = st + D::X_BYTES;
-    float acc[RJ][4];
-#pragma unroll
-    for (int j = 0; j < RJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 #pragma unroll
     for (int k = 0; k < D::COLS / 16 / WK; ++k) {
       const int step = my_part * (D::COLS / 16 / WK) + k;
@@ -351,10 +370,15 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
         if (j + 1 < RJ) mma_16816(acc[j + 1 < RJ ? j + 1 : j], af, b1);
       }
     }
+    if ((it - it_begin) % D::FLUSH == D::FLUSH - 1 || it == it_end - 1) {
 #pragma unroll
-    for (int j = 0; j < RJ; ++j)
+      for (int j = 0; j < RJ; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) total[j][e] += acc[j][e];
+        for (int e = 0; e < 4; ++e) {
+          total[j][e] += acc[j][e];
+          acc[j][e] = 0.f;
+        }
+    }
   }
   cp_async_wait<0>();
   __syncthreads();                       // the ring is free
@@ -568,8 +592,18 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
   const int s0 = ld_int(P.pair + 2 * blockIdx.x), s1 = 2 * (int)blockIdx.x + 1 < pairs ? ld_int(P.pair + 2 * blockIdx.x + 1) : -1;
   if (!plan_fits(P, M, L) || s0 < 0) return;       // pairs in use come first
   const int a0 = ld_int(P.tile + s0), a1 = s1 >= 0 ? ld_int(P.tile + s1) : kNoTile;
-  const int slot = (warp < 2 ? s0 : s1) + (warp & 1), theirs = warp < 2 ? a0 : a1;
-  const int mine = theirs == kNoTile || slot >= plan_slots(M, L) || ld_int(P.tile + slot) != theirs ? kNoTile : theirs;
+  const int base_slot = warp < 2 ? s0 : s1, theirs = warp < 2 ? a0 : a1;
+  const bool there = base_slot >= 0 && base_slot + (warp & 1) < plan_slots(M, L);
+  const int slot = there ? base_slot + (warp & 1) : s0;      // (loads that do not wait for one another)
+  const int its = ld_int(P.tile + slot);
+  const int32_t* rows = P.rows + (size_t)slot * kTileRows;
+  int m[2] = {ld_int(rows + g), ld_int(rows + g + 8)};
+  // rows 4 k + lane / 8 of the tile, columns 8 (lane % 8) .. of a block: what the lane writes
+  int to[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) to[k] = ld_int(rows + 4 * k + lane / 8);
+  const int mine = there && its == theirs ? its : kNoTile;
+  if (mine == kNoTile) m[0] = m[1] = to[0] = to[1] = to[2] = to[3] = -1;
   const int first = blockIdx.y * blocks_per_cta, last = min(first + blocks_per_cta, (C + 63) / 64);
   const uint32_t ring = shared_address(up_smem);
   const bool other = a1 >= 0 && a1 != a0;  // a second matrix, in the second region
@@ -591,8 +625,6 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
   };
   if (a0 >= 0)
     for (int i = 0; i < U::STAGES - 1; ++i) issue(first + i);
-  const int32_t* rows = P.rows + (size_t)(mine == kNoTile ? s0 : slot) * kTileRows;
-  const int m[2] = {mine == kNoTile ? -1 : ld_int(rows + g), mine == kNoTile ? -1 : ld_int(rows + g + 8)};
   UpTile<RJ> q;
   // ranks 16 s + 2 t, + 1, + 8, + 9 of the lane in step s
   q.fill(mine >= 0 && scale ? ld_f32(scale + mine) : 1.f, [&](int h, int e, float& v0, float& v1) {
@@ -601,10 +633,6 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
     v0 = __uint_as_float(w.x);
     v1 = __uint_as_float(w.y);
   });
-  // rows 4 k + lane / 8 of the tile, columns 8 (lane % 8) .. of a block: what the lane writes
-  int to[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) to[k] = mine == kNoTile ? -1 : ld_int(rows + 4 * k + lane / 8);
   float* turn = reinterpret_cast<float*>(up_smem + U::STAGES * U::STAGE) + warp * kTileRows * U::T_PITCH;
   __half* turn_half = reinterpret_cast<__half*>(up_smem + U::STAGES * U::STAGE) + warp * kTileRows * U::T_PITCH;
   auto write = [&](int b, bool sums) {
@@ -919,31 +947,48 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
     look_up(u + T::STAGES);
     const uint32_t st = ring + (uint32_t)(u % T::STAGES) * T::STAGE;
     const float* q = reinterpret_cast<const float*>(smem + (u % T::STAGES) * T::STAGE + T::X_BYTES);
-    // RJ values of q a thread; of one rank where the threads are a multiple of the ranks
-    constexpr int N = kChunk * R / kThreads;
-    constexpr bool kOneRank = kThreads % R == 0;
-    float v[N];
-    uint32_t most = 0u;      // (patterns of non-negative floats are ordered as they are; a NaN is above all)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] = q[threadIdx.x + i * kThreads];
-      const uint32_t size = __float_as_uint(v[i]) & 0x7fffffffu;
-      if (kOneRank) most = max(most, size);
-      else atomicMax(&top[(threadIdx.x + i * kThreads) % R], size);
-    }
-    if (kOneRank) atomicMax(&top[threadIdx.x % R], most);
-    __syncthreads();
-    float down = 0.f;
-    if (kOneRank) down = __uint_as_float((uint32_t)(127 - exponent_of(top[threadIdx.x % R])) << 23);
+    // pairs of ranks, RJ / 2 on average to a thread; of one pair where the threads are a
+    // multiple of the pairs
+    constexpr int PAIRS = kChunk * R / 2, N = (PAIRS + kThreads - 1) / kThreads;
+    constexpr bool kOnePair = kThreads % (R / 2) == 0;
+    float2 v[N];
+    uint32_t most[2] = {0u, 0u};      // (patterns of non-negative floats are ordered as they are; a NaN is above all)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = threadIdx.x + i * kThreads;
-      if (!kOneRank) down = __uint_as_float((uint32_t)(127 - exponent_of(top[e % R])) << 23);
-      const float w = v[i] * down;
-      const __half h = __float2half_rn(w);
-      unsigned char* at = smem + T::RING + (e / R) * T::H_PITCH + 2 * (e % R);
-      *reinterpret_cast<__half*>(at) = h;
-      *reinterpret_cast<__half*>(at + T::H_BYTES) = __float2half_rn(isinf(w) ? 0.f : w - __half2float(h));
+      if (PAIRS % kThreads && e >= PAIRS) break;
+      v[i] = reinterpret_cast<const float2*>(q)[e];
+      const uint32_t size[2] = {__float_as_uint(v[i].x) & 0x7fffffffu, __float_as_uint(v[i].y) & 0x7fffffffu};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (kOnePair) most[h] = max(most[h], size[h]);
+        else atomicMax(&top[2 * (e % (R / 2)) + h], size[h]);
+      }
+    }
+    if (kOnePair) {
+      atomicMax(&top[2 * (threadIdx.x % (R / 2))], most[0]);
+      atomicMax(&top[2 * (threadIdx.x % (R / 2)) + 1], most[1]);
+    }
+    __syncthreads();
+    float down[2] = {0.f, 0.f};
+    auto look = [&](int e) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        down[h] = __uint_as_float((uint32_t)(127 - exponent_of(top[2 * (e % (R / 2)) + h])) << 23);
+    };
+    if (kOnePair) look(threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = threadIdx.x + i * kThreads;
+      if (PAIRS % kThreads && e >= PAIRS) break;
+      if (!kOnePair) look(e);
+      const float w0 = v[i].x * down[0], w1 = v[i].y * down[1];
+      const __half2 p = __floats2half2_rn(w0, w1);
+      const float2 f = __half22float2(p);
+      unsigned char* at = smem + T::RING + (e / (R / 2)) * T::H_PITCH + 4 * (e % (R / 2));
+      *reinterpret_cast<uint32_t*>(at) = h2_as_u32(p);
+      // (an infinity leaves any finite rest: fmaxf takes the number beside a NaN)
+      *reinterpret_cast<uint32_t*>(at + T::H_BYTES) = h2_as_u32(__floats2half2_rn(fmaxf(w0 - f.x, -8.f), fmaxf(w1 - f.y, -8.f)));
     }
     __syncthreads();
     float acc[WT][CW / 8][4];

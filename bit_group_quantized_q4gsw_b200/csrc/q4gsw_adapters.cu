@@ -235,6 +235,12 @@ __device__ __forceinline__ void down_park(const float (&acc)[RJ][4], float (*red
 // once a CTA.  The warps of a tile and the KS CTAs of the cluster (grid = (pairs, KS))
 // split the contraction; sums go to fp32 registers every few stages (the tensor cores
 // truncate theirs), and the warps' and the CTAs' are added in a fixed order.
+//
+// 4096 tokens of 4096 with 16 adapters of rank 64: 21 us (the bytes alone 6.4); 1021 of
+// 14336 with four: 17.5.  Bound by the latency of a stage's steps at 16 warps an SM
+// (issue slots 40 % busy, tensor pipe 17 %, DRAM 15 %).  Four tiles to a CTA read the
+// matrix half as often and leave too few CTAs (40 us where two took 29), a deeper ring
+// gains nothing; fp32 sums at every stage cost 2 us.
 constexpr int kDownTiles = 2;
 template <bool BY_ROWS, int RJ>
 struct DownRing {
@@ -425,7 +431,7 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
 // block, s(2 t) = t and s(2 t + 1) = 4 + t, is column n of tensor-core tile i, so that a
 // lane's results are columns of its two rows in two vectors of 16 bytes, which the
 // four lanes of a quad read (the residual, by columns also the matrix) and write side by
-// side, and nothing goes through shared memory.
+// side, and nothing goes through shared memory (few tiles: up_block).
 
 // The intermediate's fragments: a lane has 2 RJ ranks in parts of PART, the parts of
 // the four lanes of a quad side by side (whole sectors); its ranks e = 4 s .. 4 s + 3 are
@@ -560,7 +566,12 @@ __device__ __forceinline__ void up_block(const __half* mat, const UpTile<RJ>& q,
 // column blocks, whose part of the matrices of the one or two adapters goes through a
 // ring in shared memory: it is read once for 64 (or 32) tokens, and its fragments come by
 // ldmatrix (in their natural order).  Sums are turned in shared memory, so that rows are
-// read (the residual) and written in whole lines.
+// read (the residual) and written in whole lines: as fp16 where there is no residual, else
+// in fp32, to which it is added before the one rounding.
+//
+// 4096 x 14336, rank 64, no residual: 49.5 us (60 with every turn in fp32 and a third
+// stage, which left three CTAs an SM; the writes alone 18).  The two parts keep the tensor
+// pipe half busy; the rest is latency that 16 warps an SM do not cover.
 constexpr int kUpWarps = 4, kUpThreads = 32 * kUpWarps;
 template <bool BY_ROWS, int RJ>
 struct UpRing {
@@ -728,6 +739,9 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
 // shared memory, added in rank order), and they split the columns of `up`.  One launch
 // and one exchange in place of two launches and a trip through memory; `inter` is
 // written for the backward pass.  FWD: x, A, B; else d_y, B, A.
+//
+// 512 tokens of 8 adapters, rank 16, 2048 <-> 8192: 8.7 us, of which the launch, the plan
+// and the exchange are five; bound by latency (a chain of loads, the exchange, loads).
 template <bool FWD, int RJ, int U>
 __global__ void __launch_bounds__(kThreads, U == 1 && RJ <= 2 ? 3 : 1)
 q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __half* mat_up, const float* scale,
@@ -822,7 +836,7 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
 // rows [c][r] (BY_ROWS: d_B [N, r]) or [r][c] (d_A [r, K]).  f the adapter's factor
 // (scale given) or 1.
 //
-// A CTA has W columns of one adapter, its warps CW each and all ranks.  Chunks of 32
+// A CTA has W columns of one adapter, its warps CW each and all ranks (half of them from 56 on).  Chunks of 32
 // tokens (their columns, and their rows of q) go through a ring in shared memory; each
 // rank's q of a chunk is divided by a power of two near its largest value and split
 // into two fp16 parts, once for all warps, and the chunk's sums are scaled back when
@@ -830,6 +844,12 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
 // range, and the tensor cores' own sums are two steps long.  The Z CTAs of a cluster
 // take every Z-th chunk, and their sums are added through distributed shared memory in
 // rank order.
+//
+// 1021 tokens of four adapters, 4096 and 14336 columns, rank 64: 24.2 us (the bytes alone
+// 8.6); 512 of eight, 8192 and 2048, rank 16: 8.7.  Bound by the steps of a chunk (three
+// barriers, the split, then the products: issue slots 44 % busy, tensor pipe 25 %).  With
+// all ranks to every warp 26.7; chunks of 64 tokens, CTAs of 512 threads and tf32
+// products were slower (47.5 against 43.5, 40 against 29, 43 against 28).
 constexpr int kChunk = 32;      // tokens
 
 template <int RJ>
@@ -1168,10 +1188,10 @@ cudaError_t launch_adapters_up(const AdaptersRef& ad, const float* inter, bool b
                                cudaStream_t stream) {
   const int groups = (ma::plan_pairs(M, ad.L) + 1) / 2;
   const int blocks = (C + 63) / 64;
-  // runs of two blocks or more: up to eight CTAs per SM, so that those without an adapter
-  // leave room (4096 x 14336, rank 64: 60 us, 72 with four; 1021 x 4096: 10.8 with single
-  // blocks, 8.8 with two)
-  int runs = 8 * sm_count(current_device()) / groups;
+  // runs of two blocks or more: up to 16 CTAs per SM, so that those without an adapter
+  // leave room (4096 x 14336, rank 64: 49.5 us, 51.3 with eight, 55.8 with four; 1021 x
+  // 4096: 8.8 with single blocks, 7.3 with two)
+  int runs = 16 * sm_count(current_device()) / groups;
   runs = runs < 1 ? 1 : runs > (blocks + 1) / 2 ? (blocks + 1) / 2 : runs;
   const int per = (blocks + runs - 1) / runs;
   cudaLaunchConfig_t cfg = {};

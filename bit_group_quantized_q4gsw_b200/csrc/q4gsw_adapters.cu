@@ -742,15 +742,16 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
 //
 // 512 tokens of 8 adapters, rank 16, 2048 <-> 8192: 8.7 us, of which the launch, the plan
 // and the exchange are five; bound by latency (a chain of loads, the exchange, loads).
-template <bool FWD, int RJ, int U>
-__global__ void __launch_bounds__(kThreads, U == 1 && RJ <= 2 ? 3 : 1)
+// W warps: eight, or four beside the product of 9 to 16 tokens (launch_adapters_low).
+template <bool FWD, int RJ, int U, int W>
+__global__ void __launch_bounds__(32 * W, W == 4 && RJ <= 2 ? 6 : U == 1 && RJ <= 2 ? 3 : 1)
 q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __half* mat_up, const float* scale,
                           const int32_t* plan, float* inter, const __half* res, __half* out, int M, int L, int C_down,
                           int C_up, unsigned int* error) {
   constexpr int R = 8 * RJ;
   extern __shared__ __align__(16) float low_smem[];
-  auto red = reinterpret_cast<float (*)[kTileRows][R]>(low_smem);                       // [kWarps]
-  auto recv = reinterpret_cast<float (*)[kTileRows][R]>(low_smem + kWarps * kTileRows * R);   // [KS], by sender
+  auto red = reinterpret_cast<float (*)[kTileRows][R]>(low_smem);                       // [W]
+  auto recv = reinterpret_cast<float (*)[kTileRows][R]>(low_smem + W * kTileRows * R);   // [KS], by sender
   griddep_wait();
   griddep_launch_dependents();     // behind the wait: what ran before has been written when the next kernel starts
   const PlanView P = plan_view(const_cast<int32_t*>(plan), M, L);
@@ -767,7 +768,7 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
   if (adapter >= 0) {
     if (KS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     // the first block's part of `up`'s matrix on its way to L2 meanwhile
-    const int b0 = ks * kWarps + warp;
+    const int b0 = ks * W + warp;
     if (b0 < blocks) {
       const int cols = min(64, C_up - 64 * b0);
       if (FWD) {
@@ -779,7 +780,7 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
     const int r0 = ld_int(rows);
     const __half* a0 = act + (size_t)(m[0] < 0 ? r0 : m[0]) * C_down;
     const __half* a1 = act + (size_t)(m[1] < 0 ? r0 : m[1]) * C_down;
-    const int chunks = (C_down + 63) / 64, parts = KS * kWarps, part = ks * kWarps + warp;
+    const int chunks = (C_down + 63) / 64, parts = KS * W, part = ks * W + warp;
     const int s_begin = (int)((long long)part * chunks / parts), s_end = (int)((long long)(part + 1) * chunks / parts);
     float acc[RJ][4];
 #pragma unroll
@@ -793,22 +794,22 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
       // every CTA of the cluster has started (arrived above): remote stores are safe
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
       cg::cluster_group cluster = cg::this_cluster();
-      for (int e = threadIdx.x; e < kTileRows * R; e += kThreads) {
+      for (int e = threadIdx.x; e < kTileRows * R; e += 32 * W) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += red[w][e / R][e % R];
+        for (int w = 0; w < W; ++w) s += red[w][e / R][e % R];
         for (int k = 0; k < KS; ++k) *cluster.map_shared_rank(&recv[ks][e / R][e % R], k) = s;
       }
       asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
     const float f = scale ? ld_f32(scale + adapter) : 1.f;
-    for (int e = threadIdx.x; e < kTileRows * R; e += kThreads) {
+    for (int e = threadIdx.x; e < kTileRows * R; e += 32 * W) {
       float s = 0.f;
       if (KS > 1) {
         for (int k = 0; k < KS; ++k) s += recv[k][e / R][e % R];
       } else {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += red[w][e / R][e % R];
+        for (int w = 0; w < W; ++w) s += red[w][e / R][e % R];
       }
       if (!FWD) s *= f;
       red[0][e / R][e % R] = s;      // (each element is read and written by one thread)
@@ -822,12 +823,12 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
       v1 = v[1];
     });
   } else if (ks == 0) {
-    for (int e = threadIdx.x; e < kTileRows * R; e += kThreads) {
+    for (int e = threadIdx.x; e < kTileRows * R; e += 32 * W) {
       const int to = ld_int(rows + e / R);
       if (to >= 0) inter[(size_t)to * R + e % R] = 0.f;
     }
   }
-  for (int b = ks * kWarps + warp; b < blocks; b += KS * kWarps)
+  for (int b = ks * W + warp; b < blocks; b += KS * W)
     up_block<FWD, RJ>(up, q, adapter >= 0, m, 64 * b, C_up, res, out, g, t);
 }
 
@@ -1212,18 +1213,24 @@ cudaError_t launch_adapters_up(const AdaptersRef& ad, const float* inter, bool b
 #undef Q4_UP
 }
 
-template <bool FWD, int RJ, int U>
+template <bool FWD, int RJ, int U, int W>
 static cudaError_t low_form(cudaLaunchConfig_t& cfg, int KS, const __half* act, const __half* down, const __half* up,
                             const float* scale, const AdaptersRef& ad, float* inter, const __half* res, __half* out,
                             int M, int C_down, int C_up) {
   constexpr int kTile = (int)sizeof(float) * ma::kTileRows * 8 * RJ;
-  auto kernel = ma::q4gsw_adapters_low_kernel<FWD, RJ, U>;
+  auto kernel = ma::q4gsw_adapters_low_kernel<FWD, RJ, U, W>;
   static PerDeviceOnce once;
   const cudaError_t e = once_per_device(once, current_device(), [&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (ma::kWarps + 8) * kTile);
+    if (W == 4) {      // runs beside the product's CTAs: with their division of shared memory
+      const cudaError_t c =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+      if (c != cudaSuccess) return c;
+    }
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (W + 8) * kTile);
   });
   if (e != cudaSuccess) return e;
-  cfg.dynamicSmemBytes = (ma::kWarps + (KS > 1 ? KS : 0)) * kTile;
+  cfg.dynamicSmemBytes = (W + (KS > 1 ? KS : 0)) * kTile;
+  cfg.blockDim = dim3(32 * W, 1, 1);
   unsigned int* error = nullptr;
   const cudaError_t w = device_error_word(&error);
   if (w != cudaSuccess) return w;
@@ -1240,9 +1247,15 @@ cudaError_t launch_adapters_low(const AdaptersRef& ad, bool fwd, const uint16_t*
   const int slots = ma::plan_slots(M, ad.L);
   const int KS = 8;
   const bool deep = ((fwd ? K : N) + 63) / 64 > KS * ma::kWarps;      // more than a chunk a warp
+  // The forward product of 9 to 16 tokens has two CTAs of 288 threads on every SM at once,
+  // and one that starts late ends late.  CTAs of four warps with 80 registers a thread leave
+  // them room (10240 of 65536) and run beside them, where the product is long enough for
+  // their own pace: 16 tokens on 4096 x 14336 22.5 -> 18.1 us, on 14336 x 4096 23.2 -> 18.8
+  // (9 tokens 17.6 -> 18.4), on 4096 x 4096 13.3 -> 11.0; but on 8192 x 2048 14.1 -> 15.5.
+  // (Backward: 30.7 -> 25.6, 29.4 -> 31.6, 17.0 -> 19.3 and 20.7 -> 17.0: eight warps.)
+  const bool beside = fwd && M > 8 && M <= 16 && (long long)N * K >= 2048LL * (N + K);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(slots, KS, 1);
-  cfg.blockDim = dim3(ma::kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   serialize(attr[0]);
@@ -1260,10 +1273,13 @@ cudaError_t launch_adapters_low(const AdaptersRef& ad, bool fwd, const uint16_t*
 #define Q4_LOW(RJ_)                                                                                                   \
   {                                                                                                                   \
     constexpr int U = RJ_ <= 2 ? 4 : RJ_ <= 4 ? 2 : 1;                                                                \
-    return fwd ? (deep ? low_form<true, RJ_, U>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N)                 \
-                       : low_form<true, RJ_, 1>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N))                \
-               : (deep ? low_form<false, RJ_, U>(cfg, KS, x, pb, pa, scale, ad, inter, rs, o, M, N, K)                \
-                       : low_form<false, RJ_, 1>(cfg, KS, x, pb, pa, scale, ad, inter, rs, o, M, N, K));              \
+    if constexpr (RJ_ <= 2) {                                                                                         \
+      if (beside) return low_form<true, RJ_, 1, 4>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N);             \
+    }                                                                                                                 \
+    return fwd ? (deep ? low_form<true, RJ_, U, 8>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N)              \
+                       : low_form<true, RJ_, 1, 8>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N))             \
+               : (deep ? low_form<false, RJ_, U, 8>(cfg, KS, x, pb, pa, scale, ad, inter, rs, o, M, N, K)             \
+                       : low_form<false, RJ_, 1, 8>(cfg, KS, x, pb, pa, scale, ad, inter, rs, o, M, N, K));           \
   }
   Q4_RANKS(ad.r / 8, Q4_LOW)
 #undef Q4_LOW

@@ -465,3 +465,33 @@ def test_two_streams_share_a_plan_and_the_adapters():
     for k in range(2):
         for run in got[k]:
             assert all(torch.equal(v, w) for v, w in zip(run, want[k]))
+
+
+@pytest.mark.parametrize("M,N,K,gs,r,f32s", [(9, 4160, 4096, 64, 8, False), (16, 4096, 4160, 64, 16, True), (12, 14336, 2432, 128, 16, False)])
+def test_low_rank_kernels_beside_the_product(M, N, K, gs, r, f32s):
+    # 9 to 16 tokens of a large projection: the low-rank CTAs run while the product's stream the weight; the
+    # residual in place, many steps behind one another on the same buffers
+    m = q()
+    L = 6
+    c = make(M, N, K, gs, L, r, np.arange(M) % (L + 1) - 1, f32s)
+    g = np.random.default_rng(M)
+    res = g.standard_normal((M, N)).astype(np.float16)
+    check(c, bias=g.standard_normal(N).astype(np.float16), residual=res)
+    args, s = head(c), cuda(c["scale"])
+    xs = [torch.randn(M, K, device="cuda").half() for _ in range(4)]
+    want = []
+    for x in xs:
+        y = m.q4gsw_adapters_fwd(*args, x, scale=s, residual=cuda(res), f32s=f32s)
+        torch.cuda.synchronize()
+        want.append(y)
+    first, u = cuda(res), torch.empty(M, r, device="cuda")
+    buf = [torch.empty_like(first) for _ in range(2)]
+    wrong = torch.zeros((), device="cuda", dtype=torch.int64)
+    for i in range(200):
+        y = buf[i % 2]
+        m.q4gsw_norms_fwd(first, residual_scale=1.0, h_out=y)                # the residual's buffer, which the call overwrites
+        m.q4gsw_adapters_fwd(*args, xs[i % 4], scale=s, residual=y, y=y, u=u, f32s=f32s)
+        if i % 5 == 0:
+            wrong += (y != want[i % 4]).sum()
+    assert wrong.item() == 0
+    m.q4gsw_device_error_check()

@@ -742,9 +742,9 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
 //
 // 512 tokens of 8 adapters, rank 16, 2048 <-> 8192: 8.7 us, of which the launch, the plan
 // and the exchange are five; bound by latency (a chain of loads, the exchange, loads).
-// W warps: eight, or four beside the product of 9 to 16 tokens (launch_adapters_low).
+// W warps: eight, or four beside the product of up to 16 tokens (launch_adapters_low).
 template <bool FWD, int RJ, int U, int W>
-__global__ void __launch_bounds__(32 * W, W == 4 && RJ <= 2 ? 6 : U == 1 && RJ <= 2 ? 3 : 1)
+__global__ void __launch_bounds__(32 * W, W == 4 && RJ <= 2 ? (U == 1 ? 6 : 4) : U == 1 && RJ <= 2 ? 3 : 1)
 q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __half* mat_up, const float* scale,
                           const int32_t* plan, float* inter, const __half* res, __half* out, int M, int L, int C_down,
                           int C_up, unsigned int* error) {
@@ -1254,6 +1254,11 @@ cudaError_t launch_adapters_low(const AdaptersRef& ad, bool fwd, const uint16_t*
   // (9 tokens 17.6 -> 18.4), on 4096 x 4096 13.3 -> 11.0; but on 8192 x 2048 14.1 -> 15.5.
   // (Backward: 30.7 -> 25.6, 29.4 -> 31.6, 17.0 -> 19.3 and 20.7 -> 17.0: eight warps.)
   const bool beside = fwd && M > 8 && M <= 16 && (long long)N * K >= 2048LL * (N + K);
+  // Up to 8 tokens the product's CTAs are smaller and leave a few places free: four warps
+  // with two chunks in flight, where `down` is at least as long as `up` (4 and 6 tokens on
+  // 4096 x 14336 17.8 -> 14.3 and 18.3 -> 14.8, on 4096 x 4096 9.4 -> 9.4 and 11.9 -> 9.7; but
+  // on 8192 x 2048 10.5 -> 11.2 and 12.7 -> 11.4, on 14336 x 4096 15.4 -> 16.0 and 15.5 -> 16.4).
+  const bool slim = fwd && M <= 8 && K >= N;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(slots, KS, 1);
   cfg.stream = stream;
@@ -1275,6 +1280,7 @@ cudaError_t launch_adapters_low(const AdaptersRef& ad, bool fwd, const uint16_t*
     constexpr int U = RJ_ <= 2 ? 4 : RJ_ <= 4 ? 2 : 1;                                                                \
     if constexpr (RJ_ <= 2) {                                                                                         \
       if (beside) return low_form<true, RJ_, 1, 4>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N);             \
+      if (slim) return low_form<true, RJ_, 2, 4>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N);               \
     }                                                                                                                 \
     return fwd ? (deep ? low_form<true, RJ_, U, 8>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N)              \
                        : low_form<true, RJ_, 1, 8>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N))             \

@@ -467,9 +467,10 @@ def test_two_streams_share_a_plan_and_the_adapters():
             assert all(torch.equal(v, w) for v, w in zip(run, want[k]))
 
 
-@pytest.mark.parametrize("M,N,K,gs,r,f32s", [(9, 4160, 4096, 64, 8, False), (16, 4096, 4160, 64, 16, True), (12, 14336, 2432, 128, 16, False)])
+@pytest.mark.parametrize("M,N,K,gs,r,f32s", [(9, 4160, 4096, 64, 8, False), (16, 4096, 4160, 64, 16, True), (12, 14336, 2432, 128, 16, False),
+                                               (6, 1032, 8192, 128, 16, False), (8, 4096, 4096, 32, 8, True), (1, 264, 4160, 64, 16, False)])
 def test_low_rank_kernels_beside_the_product(M, N, K, gs, r, f32s):
-    # 9 to 16 tokens of a large projection: the low-rank CTAs run while the product's stream the weight; the
+    # up to 16 tokens of a large projection: the low-rank CTAs run while the product's stream the weight; the
     # residual in place, many steps behind one another on the same buffers
     m = q()
     L = 6

@@ -851,6 +851,8 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
 // barriers, the split, then the products: issue slots 44 % busy, tensor pipe 25 %).  With
 // all ranks to every warp 26.7; chunks of 64 tokens, CTAs of 512 threads and tf32
 // products were slower (47.5 against 43.5, 40 against 29, 43 against 28).
+// Up to rank 16 three CTAs an SM: 128 adapters of one token each, 4096 and 4096, 38.6 ->
+// 31.4 us; rank 32 in 80 registers gains 7 % there and loses 5 % with six adapters.
 constexpr int kChunk = 32;      // tokens
 
 template <int RJ>
@@ -1092,7 +1094,7 @@ __device__ __forceinline__ void grad_block(const GradSide& a, const PlanView& P,
 }
 
 template <int RJ>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, RJ <= 2 ? 3 : 2)
 q4gsw_adapters_grad_kernel(const GradSide da, const GradSide db, const int32_t* plan, int M, int L, int groups_a,
                            int accumulate) {
   extern __shared__ __align__(16) unsigned char grad_smem[];

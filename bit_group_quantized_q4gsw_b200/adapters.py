@@ -90,6 +90,8 @@ def q4gsw_adapters_fwd(packed, N: int, K: int, group_size: int, plan, a, b, x, s
     pr = None if residual is None else _need(residual, "residual", _f16, (M, N), index)
     give = save_u or u is not None
     y, py = _out(y, "y", _f16, (M, N), index)
+    if py == px and M:
+        raise ValueError("y must not be x's buffer")
     u, pu = _out(u, "u", _f32, (M, r), index)
     _call("q4gsw_adapters_fwd_f32s" if f32s else "q4gsw_adapters_fwd", index, pw, N, K, group_size, pp, pa, pb, ps, L, r,
           px, M, pbias, pr, py, pu)
@@ -117,6 +119,8 @@ def q4gsw_adapters_bwd(packed, N: int, K: int, group_size: int, plan, a, b, x, u
         d_a, pda = _out(d_a, "d_a", _f32, (L, r, K), index)
         d_b, pdb = _out(d_b, "d_b", _f32, (L, N, r), index)
     v, pv = _out(v, "v", _f32, (M, r), index)
+    if M and (pdx == pd or (pda and (pdx == px or pv == pu))):
+        raise ValueError("d_x must not be d_y's or x's buffer, nor v u's")
     _call("q4gsw_adapters_bwd_f32s" if f32s else "q4gsw_adapters_bwd", index, pw, N, K, group_size, pp, pa, pb, ps, L, r,
           px, pu, pd, M, int(accumulate), pv, pdx, pda, pdb)
     return d_x, d_a, d_b

@@ -58,6 +58,7 @@ q4gsw_status adapters_fwd_impl(const void* packed, int N, int K, int gs, bool f3
   if (!aligned16(packed) || !aligned16(plan) || !aligned16(a) || !aligned16(b) || !aligned16(x) || !aligned16(bias) ||
       !aligned16(residual) || !aligned16(y) || !aligned16(u) || !word(scale))
     return Q4GSW_ERR_ALIGN;
+  if (y == x) return Q4GSW_ERR_UNSUPPORTED;      // the term is there before the product reads x
   const AdaptersRef ad{static_cast<const int32_t*>(plan), L, r};
   const bool low = adapters_low_fits(ad, M);
   cudaError_t e;
@@ -98,6 +99,8 @@ q4gsw_status adapters_bwd_impl(const void* packed, int N, int K, int gs, bool f3
   if (!aligned16(packed) || !aligned16(plan) || !aligned16(a) || !aligned16(b) || !aligned16(x) || !aligned16(u) ||
       !aligned16(d_y) || !aligned16(v) || !aligned16(d_x) || !word(scale))
     return Q4GSW_ERR_ALIGN;
+  // d_x has v A before the product reads d_y and the gradients read x
+  if (d_x == d_y || (grads && ((d_x && d_x == x) || v == u))) return Q4GSW_ERR_UNSUPPORTED;
   const AdaptersRef ad{static_cast<const int32_t*>(plan), L, r};
   char inner[128] = "", route[160];
   const bool low = adapters_low_fits(ad, M);

@@ -63,7 +63,8 @@ Q4GSW_API q4gsw_status q4gsw_adapters_plan(const int32_t *ids, int M, int L, voi
  *             q4gsw_device_error_check returns Q4GSW_ERR_INDEX
  *   scale     fp32 [L] (4-byte aligned) or NULL (1 for every adapter)
  *   bias      fp16 [N] or NULL
- *   residual  fp16 [M, N] or NULL; y may be the residual's buffer
+ *   residual  fp16 [M, N] or NULL; y may be the residual's buffer (but not x's, also
+ *             where the residual is x: Q4GSW_ERR_UNSUPPORTED)
  * The low-rank term, with the residual, is rounded to fp16 once before the base
  * product is added to it and the sum rounded: y is off by at most half a unit in
  * the last place of each beside the error of q4gsw_linear_act_fwd.
@@ -87,7 +88,8 @@ Q4GSW_API q4gsw_status q4gsw_adapters_fwd_f32s(const void *packed, int N, int K,
  *        the sums are added to what the buffers hold (micro-batches; an adapter
  *        without tokens keeps its values).
  * At least one of d_x and (d_a, d_b) must be given; x and u are read for d_a and
- * d_b alone and may be NULL without them.
+ * d_b alone and may be NULL without them.  d_x in the buffer of d_y, or with d_a and
+ * d_b in that of x, and v in that of u are refused (Q4GSW_ERR_UNSUPPORTED).
  */
 Q4GSW_API q4gsw_status q4gsw_adapters_bwd(const void *packed, int N, int K, int group_size, const void *plan,
                                 const uint16_t *a, const uint16_t *b, const float *scale, int L, int r,

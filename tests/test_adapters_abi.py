@@ -71,6 +71,16 @@ def test_adapters_arguments(suffix):
     assert bwd(M=0, acc=1, packed=None, plan=None, a=None, bb=None, x=None, u=None, d_y=None, v=None) == OK
 
 
+@pytest.mark.parametrize("suffix", ["", "_f32s"])
+def test_outputs_in_the_place_of_what_is_read_behind_them_are_refused(suffix):
+    lib = b.library()
+    f, g = getattr(lib, "q4gsw_adapters_fwd" + suffix), getattr(lib, "q4gsw_adapters_bwd" + suffix)
+    q = P + 4096
+    assert f(P, 64, 64, 32, P, P, P, None, 3, 16, q, 4, None, q, q, P, None) == UNSUPPORTED      # y = x = the residual
+    for x, u, d_y, v, d_x, d_a in ((P, P, q, q, q, P), (P, P, q, q, q, None), (q, P, P, q, q, P), (P, q, P, q, None, P)):
+        assert g(P, 64, 64, 32, P, P, P, None, 3, 16, x, u, d_y, 4, 0, v, d_x, d_a, d_a, None) == UNSUPPORTED
+
+
 def test_norms_arguments():
     lib = b.library()
 

@@ -413,10 +413,11 @@ def test_a_plan_of_another_batch_computes_nothing():
             m.q4gsw_device_error_check()
         assert (u == 7).all()
         d_a, d_b = torch.full((3, 8, K), 5.0, device="cuda"), torch.full((3, N, 8), 5.0, device="cuda")
-        m.q4gsw_adapters_bwd(blob, N, K, gs, wrong, a, b, x, u, cuda(c["d_y"]), d_a=d_a, d_b=d_b, v=u)
+        v = u.clone()
+        m.q4gsw_adapters_bwd(blob, N, K, gs, wrong, a, b, x, u, cuda(c["d_y"]), d_a=d_a, d_b=d_b, v=v)
         with pytest.raises(m.Q4gswError, match="INDEX"):
             m.q4gsw_device_error_check()
-        assert (d_a == 5).all() and (d_b == 5).all() and (u == 7).all()
+        assert (d_a == 5).all() and (d_b == 5).all() and (v == 7).all()
         m.q4gsw_adapters_fwd(blob, N, K, gs, plan, a, b, x)
         m.q4gsw_device_error_check()
 
@@ -496,3 +497,19 @@ def test_low_rank_kernels_beside_the_product(M, N, K, gs, r, f32s):
             wrong += (y != want[i % 4]).sum()
     assert wrong.item() == 0
     m.q4gsw_device_error_check()
+
+
+def test_outputs_over_inputs_that_are_read_later_are_refused():
+    m = q()
+    c = make(20, 128, 128, 32, 2, 8, runs(20, 2, 0))
+    args, x, d_y = head(c), cuda(c["x"]), cuda(c["d_y"])
+    before = x.clone()
+    with pytest.raises(ValueError, match="y must not be x's buffer"):
+        m.q4gsw_adapters_fwd(*args, x, residual=x, y=x)
+    y, u = m.q4gsw_adapters_fwd(*args, x, residual=x, save_u=True)
+    for kw in (dict(d_x=d_y), dict(d_x=x), dict(v=u)):
+        with pytest.raises(ValueError, match="must not be"):
+            m.q4gsw_adapters_bwd(*args, x, u, d_y, **kw)
+    assert torch.equal(x, before)
+    close(m.q4gsw_adapters_bwd(*args, x, u, d_y, d_x=x, want_adapters=False)[0],      # x is not read without d_a and d_b
+          oa.adapters_bwd(before.cpu().numpy(), u.cpu().numpy(), c["d_y"], c["w"], clean(c["ids"], 2), c["a"], c["b"], None)[0], "d_x")

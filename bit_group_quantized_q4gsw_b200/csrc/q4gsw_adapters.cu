@@ -127,7 +127,8 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) {
 constexpr unsigned int kPlanErrorBit = 0x100u;      // as an index out of range
 
 // Whether the plan is one of M tokens over L adapters; the first kernel of a call
-// records that it is not.
+// records that it is not.  Looked at before anything else of the plan is read: the
+// parts of a plan lie where M and L say, and a plan of fewer tokens ends before them.
 __device__ __forceinline__ bool plan_fits(const PlanView& P, int M, int L, unsigned int* error = nullptr) {
   const uint4 h = ld_v4(P.head);
   const bool fits = (int)h.y == M && (int)h.z == L && (int)h.w == kPlanMark;
@@ -278,8 +279,9 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
   const int KS = gridDim.y, ks = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  if (!plan_fits(P, M, L, error)) return;                   // the whole cluster
   const int slot0 = ld_int(P.pair + blockIdx.x);
-  if (!plan_fits(P, M, L, error) || slot0 < 0) return;      // the whole cluster
+  if (slot0 < 0) return;                                    // the whole cluster
   const bool more = slot0 + 1 < plan_slots(M, L);           // (loads that do not wait for one another)
   const int adapter = ld_int(P.tile + slot0), behind = more ? ld_int(P.tile + slot0 + 1) : kNoTile;
   int my_row = -1;
@@ -599,9 +601,10 @@ q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* sc
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   // the two pairs' first tiles, their adapters, and this warp's tile
+  if (!plan_fits(P, M, L)) return;
   const int pairs = plan_pairs(M, L);
   const int s0 = ld_int(P.pair + 2 * blockIdx.x), s1 = 2 * (int)blockIdx.x + 1 < pairs ? ld_int(P.pair + 2 * blockIdx.x + 1) : -1;
-  if (!plan_fits(P, M, L) || s0 < 0) return;       // pairs in use come first
+  if (s0 < 0) return;                              // pairs in use come first
   const int a0 = ld_int(P.tile + s0), a1 = s1 >= 0 ? ld_int(P.tile + s1) : kNoTile;
   const int base_slot = warp < 2 ? s0 : s1, theirs = warp < 2 ? a0 : a1;
   const bool there = base_slot >= 0 && base_slot + (warp & 1) < plan_slots(M, L);
@@ -758,10 +761,11 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
   const int KS = gridDim.y, ks = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  if (!plan_fits(P, M, L, error)) return;
   const int adapter = ld_int(P.tile + blockIdx.x);
   const int32_t* rows = P.rows + (size_t)blockIdx.x * kTileRows;
   const int m[2] = {ld_int(rows + g), ld_int(rows + g + 8)};
-  if (!plan_fits(P, M, L, error) || adapter == kNoTile) return;
+  if (adapter == kNoTile) return;
   UpTile<RJ> q;
   const __half* up = mat_up + (size_t)(adapter < 0 ? 0 : adapter) * R * C_up;
   const int blocks = out ? (C_up + 63) / 64 : 0;      // without an output: the intermediate alone

@@ -3,21 +3,19 @@
 //
 // Over the tiles of a plan (16 tokens of one adapter each):
 //   down   u = x A^T (forward), v = s d_y B (backward): the intermediate, fp32 [M][r]
-//   up     the low-rank term s u B^T (or v A) with the residual, fp16 [M][C], left in
-//          the output's place: the base product then adds itself as to any residual
-//   low    both in one launch, for few tiles
+//   few    the same for few tiles
 //   grad   d_A = v^T x, d_B = s d_y^T u over the tokens of each adapter, fp32
-// so that the base product runs on its own routes unchanged, at any number of tokens
-// and with either kind of scales.  The first kernel lets the next start only behind its
-// own wait; the product, launched behind them, then knows its activations to be
-// complete, reads them at once and waits for the low-rank term in its epilogue alone: one
-// token of 8192 x 2048 takes 7.3 us (10.4 with two kernels in a row in front of it and a
-// product that waits for them).
+// The base product adds s u B^T (or v A) to its own sums while they are fp32
+// (q4gsw_lowrank.cuh), on its routes at any number of tokens and with either kind of
+// scales.  The first kernel lets the next start only behind its own wait; the product,
+// launched behind it, then knows its activations to be complete, reads them at once and
+// waits for the intermediate in its epilogue alone.
 //
 // The intermediate stays in fp32: rounded to fp16 it would put 2^-11 of error into
 // fp32 gradients, and small gradients would fall below fp16's range.  It goes to the
 // tensor cores as two fp16 parts over a power of two near the largest value of the
-// token's row (`up`) or of the rank's chunk of tokens (`grad`): 2^-23 of that is lost.
+// token's row (in the product) or of the rank's chunk of tokens (`grad`): 2^-23 of that
+// is lost.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -59,7 +57,6 @@ __device__ __forceinline__ uint32_t ld_u16(const void* p) {
   asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ int ld_int(const int32_t* p) { return (int)ld_u32(p); }
 __device__ __forceinline__ float ld_f32(const float* p) { return __uint_as_float(ld_u32(p)); }
 
@@ -228,7 +225,7 @@ __device__ __forceinline__ void down_park(const float (&acc)[RJ][4], float (*red
 }
 
 // out[m][j] = f sum_c act[m][c] P(c, j) for the tokens m of a tile, P and f (where scale
-// is given) of the tile's adapter, for many tiles (few: q4gsw_adapters_low_kernel).
+// is given) of the tile's adapter, for many tiles (few: q4gsw_adapters_few_kernel).
 //
 // A CTA has a pair of tiles of one adapter, four warps to a tile.  Stages of 128 columns
 // of the tiles' tokens and of the adapter's matrix go through a ring in shared memory
@@ -424,337 +421,20 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
   }
 }
 
-// ---------------------------------------------------------------- up
-// out[m][c] = fp16(res[m][c] + f sum_j q[m][j] P(c, j)): P(c, j) = proj[c][j] when
-// BY_ROWS (B [N, r]), proj[j][c] else (A [r, K]).  Tokens without an adapter get
-// their residual, or zeros.
+// ---------------------------------------------------------------- few
+// The same for few tiles: a cluster of KS CTAs has one tile, and its CTAs split the
+// contraction.  Each gets the sums of all of them for its share of the tile's rows (every
+// CTA writes to every other's shared memory, added in rank order).
 //
-// A warp has one tile's 16 tokens and blocks of 64 columns.  Column 8 s(n) + i of a
-// block, s(2 t) = t and s(2 t + 1) = 4 + t, is column n of tensor-core tile i, so that a
-// lane's results are columns of its two rows in two vectors of 16 bytes, which the
-// four lanes of a quad read (the residual, by columns also the matrix) and write side by
-// side, and nothing goes through shared memory (few tiles: up_block).
-
-// The intermediate's fragments: a lane has 2 RJ ranks in parts of PART, the parts of
-// the four lanes of a quad side by side (whole sectors); its ranks e = 4 s .. 4 s + 3 are
-// the indices 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of step s.  Two fp16 parts, hi and lo, of the
-// row over 2^k, k the exponent of its largest value.
-template <int RJ>
-struct UpTile {
-  static constexpr int KT = (RJ + 1) / 2;    // tensor-core steps of 16 ranks
-  static constexpr int PART = RJ % 4 == 0 ? 8 : RJ % 2 == 0 ? 4 : 2;     // ranks
-  static constexpr int PARTS = 2 * RJ / PART;
-  uint32_t hi[KT][4], lo[KT][4];
-  float back[2];      // f 2^k of rows g and g + 8
-  __device__ __forceinline__ static int rank_of(int e, int t) { return 4 * PART * (e / PART) + PART * t + e % PART; }
-  // `load(h, e, v0, v1)`: ranks rank_of(e), + 1 (e even) of row g + 8 h
-  template <class F>
-  __device__ __forceinline__ void fill(float f, F&& load) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[4 * KT];
-#pragma unroll
-      for (int e = 0; e < 4 * KT; ++e) v[e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2 * RJ; e += 2) load(h, e, v[e], v[e + 1]);
-      float top = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4 * KT; ++e) top = fmaxf(top, fabsf(v[e]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int k = exponent_of(__float_as_uint(top));     // an infinite or NaN value stays what it is
-      const float down = __uint_as_float((uint32_t)(127 - k) << 23);
-      back[h] = f * __uint_as_float((uint32_t)(127 + k) << 23);
-#pragma unroll
-      for (int s = 0; s < KT; ++s)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float w0 = v[4 * s + 2 * q] * down, w1 = v[4 * s + 2 * q + 1] * down;
-          const __half2 p = __floats2half2_rn(w0, w1);
-          const float2 pf = __half22float2(p);
-          hi[s][2 * q + h] = h2_as_u32(p);
-          // (an infinity leaves no rest)
-          lo[s][2 * q + h] = h2_as_u32(__floats2half2_rn(isinf(w0) ? 0.f : w0 - pf.x, isinf(w1) ? 0.f : w1 - pf.y));
-        }
-    }
-  }
-};
-
-// One block of 64 columns from `base` on, of tokens m[0] (row g) and m[1] (row g + 8).
-template <bool BY_ROWS, int RJ>
-__device__ __forceinline__ void up_block(const __half* mat, const UpTile<RJ>& q, bool adapted, const int (&m)[2],
-                                         int base, int C, const __half* res, __half* out, int g, int t) {
-  using T = UpTile<RJ>;
-  constexpr int R = 8 * RJ, KT = T::KT, PART = T::PART;
-  const int sg = (g >> 1) + 4 * (g & 1);
-  float acc[8][4];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-  if (adapted) {
-    const bool in = base + 8 * sg < C;     // C % 8 == 0
-    if constexpr (BY_ROWS) {
-      uint32_t w[8][RJ];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int p = 0; p < T::PARTS; ++p) {
-          uint32_t part[PART / 2];
-#pragma unroll
-          for (int e = 0; e < PART / 2; ++e) part[e] = 0u;
-          if (in) load_bytes<2 * PART>(part, mat + (size_t)(base + 8 * sg + i) * R + T::rank_of(p * PART, t));
-#pragma unroll
-          for (int e = 0; e < PART / 2; ++e) w[i][p * (PART / 2) + e] = part[e];
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < KT; ++s)
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t bf[2] = {w[i][2 * s], 2 * s + 1 < RJ ? w[i][2 * s + 1 < RJ ? 2 * s + 1 : 0] : 0u};
-            mma_16816(acc[i], part ? q.hi[s] : q.lo[s], bf);
-          }
-    } else {
-#pragma unroll
-      for (int s = 0; s < KT; ++s) {
-        uint4 w[4];     // ranks 4 s .. 4 s + 3 of the lane, 8 columns each
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = in && 4 * s + e < 2 * RJ ? ld_v4(mat + (size_t)T::rank_of(4 * s + e, t) * C + base + 8 * sg)
-                                          : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&w[0]);
-        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&w[1]);
-        const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&w[2]);
-        const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&w[3]);
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t bf[2] = {pair_halves(w0[i / 2], w1[i / 2], i % 2), pair_halves(w2[i / 2], w3[i / 2], i % 2)};
-            mma_16816(acc[i], part ? q.hi[s] : q.lo[s], bf);
-          }
-      }
-    }
-  }
-  // columns base + 8 t + i (acc[i][0], row g; [2], row g + 8) and + 32 + i ([1], [3])
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (m[h] < 0) continue;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c = base + 8 * t + 32 * e;
-      if (c >= C) continue;
-      const size_t at = (size_t)m[h] * C + c;
-      uint4 r = make_uint4(0u, 0u, 0u, 0u);
-      if (res) r = *reinterpret_cast<const uint4*>(res + at);
-      const uint32_t rw[4] = {r.x, r.y, r.z, r.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 rf = __half22float2(u32_as_h2(rw[i]));
-        o[i] = !adapted ? rw[i]
-                        : h2_as_u32(__floats2half2_rn(fmaf(q.back[h], acc[2 * i][2 * h + e], rf.x),
-                                                      fmaf(q.back[h], acc[2 * i + 1][2 * h + e], rf.y)));
-      }
-      *reinterpret_cast<uint4*>(out + at) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  }
-}
-
-// The same for many tiles.  A CTA has two pairs of tiles, a tile to a warp, and a run of
-// column blocks, whose part of the matrices of the one or two adapters goes through a
-// ring in shared memory: it is read once for 64 (or 32) tokens, and its fragments come by
-// ldmatrix (in their natural order).  Sums are turned in shared memory, so that rows are
-// read (the residual) and written in whole lines: as fp16 where there is no residual, else
-// in fp32, to which it is added before the one rounding.
-//
-// 4096 x 14336, rank 64, no residual: 49.5 us (60 with every turn in fp32 and a third
-// stage, which left three CTAs an SM; the writes alone 18).  The two parts keep the tensor
-// pipe half busy; the rest is latency that 16 warps an SM do not cover.
-constexpr int kUpWarps = 4, kUpThreads = 32 * kUpWarps;
-template <bool BY_ROWS, int RJ>
-struct UpRing {
-  static constexpr int R = 8 * RJ, KT = (RJ + 1) / 2;
-  static constexpr int STAGES = 2;
-  static constexpr int ROWS = BY_ROWS ? 64 : 16 * KT;                // rows of a block (ranks padded to 16)
-  static constexpr int CHUNKS = BY_ROWS ? 2 * KT : 8;                // 16-byte chunks of a row
-  static constexpr int PITCH = 16 * (CHUNKS + 1);                    // an odd number of them
-  static constexpr int REGION = ROWS * PITCH, STAGE = 2 * REGION;
-  static constexpr int T_PITCH = 72;                                 // of a warp's 16 x 64 sums, floats
-  static constexpr int BYTES = STAGES * STAGE + kUpWarps * kTileRows * T_PITCH * 2;    // without a residual: as fp16
-  static constexpr int BYTES_RES = STAGES * STAGE + kUpWarps * kTileRows * T_PITCH * 4;
-};
-
-template <bool BY_ROWS, int RJ>
-__global__ void __launch_bounds__(kUpThreads, 4)
-q4gsw_adapters_up_kernel(const float* inter, const __half* proj, const float* scale, const int32_t* plan,
-                         const __half* res, __half* out, int M, int L, int C, int blocks_per_cta) {
-  using U = UpRing<BY_ROWS, RJ>;
-  constexpr int R = U::R, KT = U::KT;
-  extern __shared__ __align__(16) unsigned char up_smem[];
-  griddep_launch_dependents();
-  griddep_wait();
-  const PlanView P = plan_view(const_cast<int32_t*>(plan), M, L);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  // the two pairs' first tiles, their adapters, and this warp's tile
-  if (!plan_fits(P, M, L)) return;
-  const int pairs = plan_pairs(M, L);
-  const int s0 = ld_int(P.pair + 2 * blockIdx.x), s1 = 2 * (int)blockIdx.x + 1 < pairs ? ld_int(P.pair + 2 * blockIdx.x + 1) : -1;
-  if (s0 < 0) return;                              // pairs in use come first
-  const int a0 = ld_int(P.tile + s0), a1 = s1 >= 0 ? ld_int(P.tile + s1) : kNoTile;
-  const int base_slot = warp < 2 ? s0 : s1, theirs = warp < 2 ? a0 : a1;
-  const bool there = base_slot >= 0 && base_slot + (warp & 1) < plan_slots(M, L);
-  const int slot = there ? base_slot + (warp & 1) : s0;      // (loads that do not wait for one another)
-  const int its = ld_int(P.tile + slot);
-  const int32_t* rows = P.rows + (size_t)slot * kTileRows;
-  int m[2] = {ld_int(rows + g), ld_int(rows + g + 8)};
-  // rows 4 k + lane / 8 of the tile, columns 8 (lane % 8) .. of a block: what the lane writes
-  int to[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) to[k] = ld_int(rows + 4 * k + lane / 8);
-  const int mine = there && its == theirs ? its : kNoTile;
-  if (mine == kNoTile) m[0] = m[1] = to[0] = to[1] = to[2] = to[3] = -1;
-  const int first = blockIdx.y * blocks_per_cta, last = min(first + blocks_per_cta, (C + 63) / 64);
-  const uint32_t ring = shared_address(up_smem);
-  const bool other = a1 >= 0 && a1 != a0;  // a second matrix, in the second region
-  const uint32_t region = mine == a1 && other ? (uint32_t)U::REGION : 0u;
-  auto issue = [&](int b) {
-    if (b < last) {
-      const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE;
-      for (int e = threadIdx.x; e < U::ROWS * U::CHUNKS; e += kUpThreads) {
-        const int row = e / U::CHUNKS, k = e % U::CHUNKS;
-        // by rows: column 64 b + row, ranks 8 k ..; else rank row, columns 64 b + 8 k ..
-        const bool in = BY_ROWS ? 64 * b + row < C && k < RJ : row < R && 64 * b + 8 * k < C;
-        const size_t from = BY_ROWS ? (size_t)(64 * b + row) * R + 8 * k : (size_t)row * C + 64 * b + 8 * k;
-        const uint32_t to_smem = st + row * U::PITCH + 16 * k;
-        copy_16(to_smem, proj + (in ? (size_t)a0 * R * C + from : 0), in);
-        if (other) copy_16(to_smem + U::REGION, proj + (in ? (size_t)a1 * R * C + from : 0), in);
-      }
-    }
-    cp_async_commit();
-  };
-  if (a0 >= 0)
-    for (int i = 0; i < U::STAGES - 1; ++i) issue(first + i);
-  UpTile<RJ> q;
-  // ranks 16 s + 2 t, + 1, + 8, + 9 of the lane in step s
-  q.fill(mine >= 0 && scale ? ld_f32(scale + mine) : 1.f, [&](int h, int e, float& v0, float& v1) {
-    if (m[h] < 0 || mine < 0) return;
-    const uint2 w = ld_v2(inter + (size_t)m[h] * R + 16 * (e / 4) + 4 * (e % 4) + 2 * t);
-    v0 = __uint_as_float(w.x);
-    v1 = __uint_as_float(w.y);
-  });
-  float* turn = reinterpret_cast<float*>(up_smem + U::STAGES * U::STAGE) + warp * kTileRows * U::T_PITCH;
-  __half* turn_half = reinterpret_cast<__half*>(up_smem + U::STAGES * U::STAGE) + warp * kTileRows * U::T_PITCH;
-  auto write = [&](int b, bool sums) {
-    const int c = 64 * b + 8 * (lane % 8);
-    if (c >= C) return;                    // C % 8 == 0
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (to[k] < 0) continue;
-      const size_t at = (size_t)to[k] * C + c;
-      uint4 r = make_uint4(0u, 0u, 0u, 0u);
-      if (res) r = *reinterpret_cast<const uint4*>(res + at);
-      if (sums) {
-        // (the upper four of eight lanes read their halves in the other order: no bank twice)
-        const float* v = turn + (4 * k + lane / 8) * U::T_PITCH + 8 * (lane % 8);
-        const bool up = lane & 4;
-        const float4 p = *reinterpret_cast<const float4*>(v + (up ? 4 : 0)),
-                     q2 = *reinterpret_cast<const float4*>(v + (up ? 0 : 4));
-        const float4 v0 = up ? q2 : p, v1 = up ? p : q2;
-        const float2 r0 = __half22float2(u32_as_h2(r.x)), r1 = __half22float2(u32_as_h2(r.y)),
-                     r2 = __half22float2(u32_as_h2(r.z)), r3 = __half22float2(u32_as_h2(r.w));
-        r = make_uint4(h2_as_u32(__floats2half2_rn(v0.x + r0.x, v0.y + r0.y)),
-                       h2_as_u32(__floats2half2_rn(v0.z + r1.x, v0.w + r1.y)),
-                       h2_as_u32(__floats2half2_rn(v1.x + r2.x, v1.y + r2.y)),
-                       h2_as_u32(__floats2half2_rn(v1.z + r3.x, v1.w + r3.y)));
-      }
-      *reinterpret_cast<uint4*>(out + at) = r;
-    }
-  };
-  if (mine == kNoAdapter)                  // the residual, or zeros
-    for (int b = first; b < last; ++b) write(b, false);
-  if (a0 < 0) return;                      // (sorted: the second pair has no adapter, either)
-  for (int b = first; b < last; ++b) {
-    cp_async_wait<U::STAGES - 2>();
-    __syncthreads();                     // the block has landed, and the one refilled below has been used by all
-    issue(b + U::STAGES - 1);
-    if (mine < 0) continue;
-    const uint32_t st = ring + (uint32_t)((b - first) % U::STAGES) * U::STAGE + region;
-    float acc[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-#pragma unroll
-    for (int s = 0; s < KT; ++s) {
-      uint32_t bf[4][4];                 // columns 16 i .. + 7 (indices 0-7, 8-15), then + 8 .. + 15
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (BY_ROWS)
-          ldmatrix4(bf[i], st + (16 * i + 8 * (lane / 16) + lane % 8) * U::PITCH + 32 * s + 16 * (lane / 8 % 2));
-        else
-          ldmatrix4_trans(bf[i], st + (16 * s + lane % 16) * U::PITCH + 32 * i + 16 * (lane / 16));
-      }
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t f[2] = {bf[i / 2][2 * (i % 2)], bf[i / 2][2 * (i % 2) + 1]};
-          mma_16816(acc[i], part ? q.hi[s] : q.lo[s], f);
-        }
-    }
-    __syncwarp();                        // the lanes have read the block before
-    if (!res) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<uint32_t*>(turn_half + (g + 8 * h) * U::T_PITCH + 8 * i + 2 * t) =
-              h2_as_u32(__floats2half2_rn(q.back[h] * acc[i][2 * h], q.back[h] * acc[i][2 * h + 1]));
-      __syncwarp();
-      const int c = 64 * b + 8 * (lane % 8);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (to[k] >= 0 && c < C)
-          *reinterpret_cast<uint4*>(out + (size_t)to[k] * C + c) =
-              *reinterpret_cast<const uint4*>(turn_half + (4 * k + lane / 8) * U::T_PITCH + 8 * (lane % 8));
-      continue;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(turn + (g + 8 * h) * U::T_PITCH + 8 * i + 2 * t) =
-            make_float2(q.back[h] * acc[i][2 * h], q.back[h] * acc[i][2 * h + 1]);
-    __syncwarp();
-    write(b, true);
-  }
-  cp_async_wait<0>();                      // no thread leaves with copies in flight
-}
-
-// ---------------------------------------------------------------- down and up in one
-// For few tiles: a cluster of KS CTAs has one tile.  Its CTAs split the contraction of
-// `down`, each gets the sums of all of them (every CTA writes its own to every other's
-// shared memory, added in rank order), and they split the columns of `up`.  One launch
-// and one exchange in place of two launches and a trip through memory; `inter` is
-// written for the backward pass.  FWD: x, A, B; else d_y, B, A.
-//
-// 512 tokens of 8 adapters, rank 16, 2048 <-> 8192: 8.7 us, of which the launch, the plan
-// and the exchange are five; bound by latency (a chain of loads, the exchange, loads).
-// W warps: eight, or four beside the product of up to 16 tokens (launch_adapters_low).
-template <bool FWD, int RJ, int U, int W>
+// W warps: eight, or four beside the product of up to 16 tokens (launch_adapters_few).
+template <bool BY_ROWS, int RJ, int U, int W>
 __global__ void __launch_bounds__(32 * W, W == 4 && RJ <= 2 ? (U == 1 ? 6 : 4) : U == 1 && RJ <= 2 ? 3 : 1)
-q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __half* mat_up, const float* scale,
-                          const int32_t* plan, float* inter, const __half* res, __half* out, int M, int L, int C_down,
-                          int C_up, unsigned int* error) {
+q4gsw_adapters_few_kernel(const __half* act, const __half* proj, const float* scale, const int32_t* plan, float* out,
+                          int M, int L, int C, unsigned int* error) {
   constexpr int R = 8 * RJ;
-  extern __shared__ __align__(16) float low_smem[];
-  auto red = reinterpret_cast<float (*)[kTileRows][R]>(low_smem);                       // [W]
-  auto recv = reinterpret_cast<float (*)[kTileRows][R]>(low_smem + W * kTileRows * R);   // [KS], by sender
+  extern __shared__ __align__(16) float few_smem[];
+  auto red = reinterpret_cast<float (*)[kTileRows][R]>(few_smem);                       // [W]
+  auto recv = reinterpret_cast<float (*)[R]>(few_smem + W * kTileRows * R);             // [KS][owned rows], by sender
   griddep_wait();
   griddep_launch_dependents();     // behind the wait: what ran before has been written when the next kernel starts
   const PlanView P = plan_view(const_cast<int32_t*>(plan), M, L);
@@ -766,74 +446,55 @@ q4gsw_adapters_low_kernel(const __half* act, const __half* mat_down, const __hal
   const int32_t* rows = P.rows + (size_t)blockIdx.x * kTileRows;
   const int m[2] = {ld_int(rows + g), ld_int(rows + g + 8)};
   if (adapter == kNoTile) return;
-  UpTile<RJ> q;
-  const __half* up = mat_up + (size_t)(adapter < 0 ? 0 : adapter) * R * C_up;
-  const int blocks = out ? (C_up + 63) / 64 : 0;      // without an output: the intermediate alone
-  if (adapter >= 0) {
-    if (KS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    // the first block's part of `up`'s matrix on its way to L2 meanwhile
-    const int b0 = ks * W + warp;
-    if (b0 < blocks) {
-      const int cols = min(64, C_up - 64 * b0);
-      if (FWD) {
-        for (int e = lane; e < cols * R / 64; e += 32) prefetch_l2(up + (size_t)(64 * b0) * R + 64 * e);
-      } else {
-        for (int e = lane; e < R; e += 32) prefetch_l2(up + (size_t)e * C_up + 64 * b0);
-      }
-    }
-    const int r0 = ld_int(rows);
-    const __half* a0 = act + (size_t)(m[0] < 0 ? r0 : m[0]) * C_down;
-    const __half* a1 = act + (size_t)(m[1] < 0 ? r0 : m[1]) * C_down;
-    const int chunks = (C_down + 63) / 64, parts = KS * W, part = ks * W + warp;
-    const int s_begin = (int)((long long)part * chunks / parts), s_end = (int)((long long)(part + 1) * chunks / parts);
-    float acc[RJ][4];
-#pragma unroll
-    for (int j = 0; j < RJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    down_chunks<FWD, RJ, U>(mat_down + (size_t)adapter * R * C_down, a0, a1, C_down, s_begin, s_end, g, t, acc);
-    down_park<FWD, RJ>(acc, red[warp], g, t);
-    __syncthreads();
-    if (KS > 1) {
-      // every CTA of the cluster has started (arrived above): remote stores are safe
-      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-      cg::cluster_group cluster = cg::this_cluster();
-      for (int e = threadIdx.x; e < kTileRows * R; e += 32 * W) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) s += red[w][e / R][e % R];
-        for (int k = 0; k < KS; ++k) *cluster.map_shared_rank(&recv[ks][e / R][e % R], k) = s;
-      }
-      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    }
-    const float f = scale ? ld_f32(scale + adapter) : 1.f;
-    for (int e = threadIdx.x; e < kTileRows * R; e += 32 * W) {
-      float s = 0.f;
-      if (KS > 1) {
-        for (int k = 0; k < KS; ++k) s += recv[k][e / R][e % R];
-      } else {
-#pragma unroll
-        for (int w = 0; w < W; ++w) s += red[w][e / R][e % R];
-      }
-      if (!FWD) s *= f;
-      red[0][e / R][e % R] = s;      // (each element is read and written by one thread)
+  if (adapter < 0) {               // the whole cluster
+    for (int e = threadIdx.x + 32 * W * ks; e < kTileRows * R; e += 32 * W * KS) {
       const int to = ld_int(rows + e / R);
-      if (ks == 0 && to >= 0) inter[(size_t)to * R + e % R] = s;
+      if (to >= 0) out[(size_t)to * R + e % R] = 0.f;
     }
-    __syncthreads();
-    q.fill(FWD ? f : 1.f, [&](int h, int e, float& v0, float& v1) {
-      const float* v = &red[0][g + 8 * h][UpTile<RJ>::rank_of(e, t)];
-      v0 = v[0];
-      v1 = v[1];
-    });
-  } else if (ks == 0) {
-    for (int e = threadIdx.x; e < kTileRows * R; e += 32 * W) {
-      const int to = ld_int(rows + e / R);
-      if (to >= 0) inter[(size_t)to * R + e % R] = 0.f;
-    }
+    return;
   }
-  for (int b = ks * W + warp; b < blocks; b += KS * W)
-    up_block<FWD, RJ>(up, q, adapter >= 0, m, 64 * b, C_up, res, out, g, t);
+  if (KS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int r0 = ld_int(rows);
+  const __half* a0 = act + (size_t)(m[0] < 0 ? r0 : m[0]) * C;
+  const __half* a1 = act + (size_t)(m[1] < 0 ? r0 : m[1]) * C;
+  const int chunks = (C + 63) / 64, parts = KS * W, part = ks * W + warp;
+  const int s_begin = (int)((long long)part * chunks / parts), s_end = (int)((long long)(part + 1) * chunks / parts);
+  float acc[RJ][4];
+#pragma unroll
+  for (int j = 0; j < RJ; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+  down_chunks<BY_ROWS, RJ, U>(proj + (size_t)adapter * R * C, a0, a1, C, s_begin, s_end, g, t, acc);
+  down_park<BY_ROWS, RJ>(acc, red[warp], g, t);
+  __syncthreads();
+  auto own = [&](int row, int j) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) s += red[w][row][j];
+    return s;
+  };
+  const int owned = kTileRows / KS;      // rows that this CTA writes (KS is a power of two)
+  if (KS > 1) {
+    // every CTA of the cluster has started (arrived above): remote stores are safe
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    cg::cluster_group cluster = cg::this_cluster();
+    for (int e = threadIdx.x; e < kTileRows * R; e += 32 * W) {
+      const int row = e / R, j = e % R;
+      *cluster.map_shared_rank(&recv[ks * owned + row % owned][j], row / owned) = own(row, j);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  for (int e = threadIdx.x; e < owned * R; e += 32 * W) {
+    const int row = e / R, j = e % R, to = ld_int(rows + ks * owned + row);
+    if (to < 0) continue;
+    float v = 0.f;
+    if (KS > 1) {
+      for (int q = 0; q < KS; ++q) v += recv[q * owned + row][j];
+    } else {
+      v = own(row, j);
+    }
+    out[(size_t)to * R + j] = scale ? ld_f32(scale + adapter) * v : v;
+  }
 }
 
 // ---------------------------------------------------------------- grad
@@ -1148,8 +809,73 @@ static cudaError_t down_form(cudaLaunchConfig_t& cfg, const __half* a, const __h
   return cudaLaunchKernelEx(&cfg, kernel, a, p, scale, ad.plan, out, M, ad.L, C, error);
 }
 
+bool adapters_few(const AdaptersRef& ad, int M) { return ma::plan_slots(M, ad.L) <= 64; }
+
+template <bool BY_ROWS, int RJ, int U, int W>
+static cudaError_t few_form(cudaLaunchConfig_t& cfg, const __half* act, const __half* proj, const float* scale,
+                            const AdaptersRef& ad, float* out, int M, int C) {
+  constexpr int kTile = (int)sizeof(float) * ma::kTileRows * 8 * RJ;
+  constexpr int kBytes = (W + 1) * kTile;      // the warps' sums, and those that the cluster sends
+  auto kernel = ma::q4gsw_adapters_few_kernel<BY_ROWS, RJ, U, W>;
+  static PerDeviceOnce once;
+  const cudaError_t e = once_per_device(once, current_device(), [&] {
+    if (W == 4) {      // runs beside the product's CTAs: with their division of shared memory
+      const cudaError_t c =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+      if (c != cudaSuccess) return c;
+    }
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  cfg.dynamicSmemBytes = kBytes;
+  cfg.blockDim = dim3(32 * W, 1, 1);
+  unsigned int* error = nullptr;
+  const cudaError_t w = device_error_word(&error);
+  if (w != cudaSuccess) return w;
+  return cudaLaunchKernelEx(&cfg, kernel, act, proj, scale, ad.plan, out, M, ad.L, C, error);
+}
+
+static cudaError_t launch_adapters_few(const AdaptersRef& ad, const __half* x, bool by_rows, const __half* p,
+                                       const float* scale, int M, int C, float* out, cudaStream_t stream) {
+  const int KS = 8;
+  const bool deep = (C + 63) / 64 > KS * ma::kWarps;      // more than a chunk a warp
+  // The forward product of up to 16 tokens has two or four CTAs on every SM at once, and one
+  // that starts late ends late.  CTAs of four warps leave them room and run beside them
+  // (four and eight warps, us of a whole call, rank 16): 16 tokens of as many adapters on 4096
+  // x 14336 17.7 and 20.4, on 8192 x 2048 11.2 and 13.2; of one adapter 17.3 and 17.7, 10.8 and
+  // 10.9; 8 tokens 16.3 and 15.7, 9.7 and 10.5.
+  const bool slim = by_rows && M <= ma::kTileRows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ma::plan_slots(M, ad.L), KS, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  serialize(attr[0]);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = KS;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+#define Q4_FEW(RJ_)                                                                              \
+  {                                                                                              \
+    constexpr int U = RJ_ <= 2 ? 4 : RJ_ <= 4 ? 2 : 1;                                           \
+    if constexpr (RJ_ <= 2) {                                                                    \
+      if (slim) return few_form<true, RJ_, 2, 4>(cfg, x, p, scale, ad, out, M, C);               \
+    }                                                                                            \
+    return by_rows ? (deep ? few_form<true, RJ_, U, 8>(cfg, x, p, scale, ad, out, M, C)          \
+                           : few_form<true, RJ_, 1, 8>(cfg, x, p, scale, ad, out, M, C))         \
+                   : (deep ? few_form<false, RJ_, U, 8>(cfg, x, p, scale, ad, out, M, C)         \
+                           : few_form<false, RJ_, 1, 8>(cfg, x, p, scale, ad, out, M, C));       \
+  }
+  Q4_RANKS(ad.r / 8, Q4_FEW)
+#undef Q4_FEW
+}
+
 cudaError_t launch_adapters_down(const AdaptersRef& ad, const uint16_t* act, bool by_rows, const uint16_t* proj,
                                  const float* scale, int M, int C, float* out, cudaStream_t stream) {
+  const __half* a = reinterpret_cast<const __half*>(act);
+  const __half* p = reinterpret_cast<const __half*>(proj);
+  if (adapters_few(ad, M)) return launch_adapters_few(ad, a, by_rows, p, scale, M, C, out, stream);
   const int groups = ma::plan_pairs(M, ad.L), sms = sm_count(current_device());
   // contraction splits: about two CTAs per SM, two stages each at least, clusters of at most
   // 8, by the pairs that are likely to be in use, half of the adapters' last ones (by all
@@ -1171,134 +897,11 @@ cudaError_t launch_adapters_down(const AdaptersRef& ad, const uint16_t* act, boo
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const __half* a = reinterpret_cast<const __half*>(act);
-  const __half* p = reinterpret_cast<const __half*>(proj);
 #define Q4_DOWN(RJ_)                                                            \
   return by_rows ? down_form<true, RJ_>(cfg, a, p, scale, ad, out, M, C)        \
                  : down_form<false, RJ_>(cfg, a, p, scale, ad, out, M, C)
   Q4_RANKS(ad.r / 8, Q4_DOWN)
 #undef Q4_DOWN
-}
-
-template <bool BY_ROWS, int RJ>
-static cudaError_t up_form(cudaLaunchConfig_t& cfg, const float* inter, const __half* p, const float* scale,
-                           const AdaptersRef& ad, const __half* res, __half* out, int M, int C, int per) {
-  using U = ma::UpRing<BY_ROWS, RJ>;
-  auto kernel = ma::q4gsw_adapters_up_kernel<BY_ROWS, RJ>;
-  static PerDeviceOnce once;
-  const cudaError_t e = once_per_device(once, current_device(), [&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, U::BYTES_RES);
-  });
-  if (e != cudaSuccess) return e;
-  cfg.dynamicSmemBytes = res ? U::BYTES_RES : U::BYTES;
-  return cudaLaunchKernelEx(&cfg, kernel, inter, p, scale, ad.plan, res, out, M, ad.L, C, per);
-}
-
-cudaError_t launch_adapters_up(const AdaptersRef& ad, const float* inter, bool by_rows, const uint16_t* proj,
-                               const float* scale, int M, int C, const uint16_t* res, uint16_t* out,
-                               cudaStream_t stream) {
-  const int groups = (ma::plan_pairs(M, ad.L) + 1) / 2;
-  const int blocks = (C + 63) / 64;
-  // runs of two blocks or more: up to 16 CTAs per SM, so that those without an adapter
-  // leave room (4096 x 14336, rank 64: 49.5 us, 51.3 with eight, 55.8 with four; 1021 x
-  // 4096: 8.8 with single blocks, 7.3 with two)
-  int runs = 16 * sm_count(current_device()) / groups;
-  runs = runs < 1 ? 1 : runs > (blocks + 1) / 2 ? (blocks + 1) / 2 : runs;
-  const int per = (blocks + runs - 1) / runs;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(groups, (blocks + per - 1) / per, 1);
-  cfg.blockDim = dim3(ma::kUpThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  serialize(attr[0]);
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const __half* p = reinterpret_cast<const __half*>(proj);
-  const __half* rs = reinterpret_cast<const __half*>(res);
-  __half* o = reinterpret_cast<__half*>(out);
-#define Q4_UP(RJ_)                                                              \
-  return by_rows ? up_form<true, RJ_>(cfg, inter, p, scale, ad, rs, o, M, C, per)  \
-                 : up_form<false, RJ_>(cfg, inter, p, scale, ad, rs, o, M, C, per)
-  Q4_RANKS(ad.r / 8, Q4_UP)
-#undef Q4_UP
-}
-
-template <bool FWD, int RJ, int U, int W>
-static cudaError_t low_form(cudaLaunchConfig_t& cfg, int KS, const __half* act, const __half* down, const __half* up,
-                            const float* scale, const AdaptersRef& ad, float* inter, const __half* res, __half* out,
-                            int M, int C_down, int C_up) {
-  constexpr int kTile = (int)sizeof(float) * ma::kTileRows * 8 * RJ;
-  auto kernel = ma::q4gsw_adapters_low_kernel<FWD, RJ, U, W>;
-  static PerDeviceOnce once;
-  const cudaError_t e = once_per_device(once, current_device(), [&] {
-    if (W == 4) {      // runs beside the product's CTAs: with their division of shared memory
-      const cudaError_t c =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-      if (c != cudaSuccess) return c;
-    }
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (W + 8) * kTile);
-  });
-  if (e != cudaSuccess) return e;
-  cfg.dynamicSmemBytes = (W + (KS > 1 ? KS : 0)) * kTile;
-  cfg.blockDim = dim3(32 * W, 1, 1);
-  unsigned int* error = nullptr;
-  const cudaError_t w = device_error_word(&error);
-  if (w != cudaSuccess) return w;
-  return cudaLaunchKernelEx(&cfg, kernel, act, down, up, scale, ad.plan, inter, res, out, M, ad.L, C_down, C_up, error);
-}
-
-bool adapters_low_fits(const AdaptersRef& ad, int M) {
-  return ma::plan_slots(M, ad.L) <= 64;
-}
-
-cudaError_t launch_adapters_low(const AdaptersRef& ad, bool fwd, const uint16_t* act, const uint16_t* a,
-                                const uint16_t* b, const float* scale, int M, int K, int N, float* inter,
-                                const uint16_t* res, uint16_t* out, cudaStream_t stream) {
-  const int slots = ma::plan_slots(M, ad.L);
-  const int KS = 8;
-  const bool deep = ((fwd ? K : N) + 63) / 64 > KS * ma::kWarps;      // more than a chunk a warp
-  // The forward product of 9 to 16 tokens has two CTAs of 288 threads on every SM at once,
-  // and one that starts late ends late.  CTAs of four warps with 80 registers a thread leave
-  // them room (10240 of 65536) and run beside them, where the product is long enough for
-  // their own pace: 16 tokens on 4096 x 14336 22.5 -> 18.1 us, on 14336 x 4096 23.2 -> 18.8
-  // (9 tokens 17.6 -> 18.4), on 4096 x 4096 13.3 -> 11.0; but on 8192 x 2048 14.1 -> 15.5.
-  // (Backward: 30.7 -> 25.6, 29.4 -> 31.6, 17.0 -> 19.3 and 20.7 -> 17.0: eight warps.)
-  const bool beside = fwd && M > 8 && M <= 16 && (long long)N * K >= 2048LL * (N + K);
-  // Up to 8 tokens the product's CTAs are smaller and leave a few places free: four warps
-  // with two chunks in flight, where `down` is at least as long as `up` (4 and 6 tokens on
-  // 4096 x 14336 17.8 -> 14.3 and 18.3 -> 14.8, on 4096 x 4096 9.4 -> 9.4 and 11.9 -> 9.7; but
-  // on 8192 x 2048 10.5 -> 11.2 and 12.7 -> 11.4, on 14336 x 4096 15.4 -> 16.0 and 15.5 -> 16.4).
-  const bool slim = fwd && M <= 8 && K >= N;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(slots, KS, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  serialize(attr[0]);
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1;
-  attr[1].val.clusterDim.y = KS;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const __half* x = reinterpret_cast<const __half*>(act);
-  const __half* pa = reinterpret_cast<const __half*>(a);
-  const __half* pb = reinterpret_cast<const __half*>(b);
-  const __half* rs = reinterpret_cast<const __half*>(res);
-  __half* o = reinterpret_cast<__half*>(out);
-#define Q4_LOW(RJ_)                                                                                                   \
-  {                                                                                                                   \
-    constexpr int U = RJ_ <= 2 ? 4 : RJ_ <= 4 ? 2 : 1;                                                                \
-    if constexpr (RJ_ <= 2) {                                                                                         \
-      if (beside) return low_form<true, RJ_, 1, 4>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N);             \
-      if (slim) return low_form<true, RJ_, 2, 4>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N);               \
-    }                                                                                                                 \
-    return fwd ? (deep ? low_form<true, RJ_, U, 8>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N)              \
-                       : low_form<true, RJ_, 1, 8>(cfg, KS, x, pa, pb, scale, ad, inter, rs, o, M, K, N))             \
-               : (deep ? low_form<false, RJ_, U, 8>(cfg, KS, x, pb, pa, scale, ad, inter, rs, o, M, N, K)             \
-                       : low_form<false, RJ_, 1, 8>(cfg, KS, x, pb, pa, scale, ad, inter, rs, o, M, N, K));           \
-  }
-  Q4_RANKS(ad.r / 8, Q4_LOW)
-#undef Q4_LOW
 }
 
 template <int RJ>

@@ -58,22 +58,15 @@ q4gsw_status adapters_fwd_impl(const void* packed, int N, int K, int gs, bool f3
   if (!aligned16(packed) || !aligned16(plan) || !aligned16(a) || !aligned16(b) || !aligned16(x) || !aligned16(bias) ||
       !aligned16(residual) || !aligned16(y) || !aligned16(u) || !word(scale))
     return Q4GSW_ERR_ALIGN;
-  if (y == x) return Q4GSW_ERR_UNSUPPORTED;      // the term is there before the product reads x
+  if (y == x) return Q4GSW_ERR_UNSUPPORTED;      // tiles of y are written while others are computed from x
   const AdaptersRef ad{static_cast<const int32_t*>(plan), L, r};
-  const bool low = adapters_low_fits(ad, M);
-  cudaError_t e;
-  if (low) {
-    e = launch_adapters_low(ad, true, x, a, b, scale, M, K, N, u, residual, y, stream);
-  } else {
-    e = launch_adapters_down(ad, x, true, a, nullptr, M, K, u, stream);
-    if (e == cudaSuccess) e = launch_adapters_up(ad, u, true, b, scale, M, N, residual, y, stream);
-  }
+  cudaError_t e = launch_adapters_down(ad, x, true, a, nullptr, M, K, u, stream);
   char inner[128] = "", route[160];
   if (e == cudaSuccess) {
-    const Epi out{h(y), nullptr, h(bias), h(y), N, kActNone, 0, 1};
-    e = launch_product_epi(false, packed, N, K, gs, f32s, x, M, out, stream, inner, sizeof(inner));
+    const EpiLow out{h(y), h(bias), h(residual), N, u, h(b), scale, ad.plan, M, L, r};   // its epilogue adds the term
+    e = launch_product_low(false, packed, N, K, gs, f32s, x, M, out, stream, inner, sizeof(inner));
   }
-  snprintf(route, sizeof(route), "adapters %s + %s", low ? "low launches=1" : "down launches=1 + up launches=1", inner);
+  snprintf(route, sizeof(route), "adapters %s launches=1 + %s", adapters_few(ad, M) ? "few" : "down", inner);
   set_route(route);
   return from_cuda(e);
 }
@@ -99,25 +92,18 @@ q4gsw_status adapters_bwd_impl(const void* packed, int N, int K, int gs, bool f3
   if (!aligned16(packed) || !aligned16(plan) || !aligned16(a) || !aligned16(b) || !aligned16(x) || !aligned16(u) ||
       !aligned16(d_y) || !aligned16(v) || !aligned16(d_x) || !word(scale))
     return Q4GSW_ERR_ALIGN;
-  // d_x has v A before the product reads d_y and the gradients read x
+  // tiles of d_x are written while others are computed from d_y; v is there before the gradients read u
   if (d_x == d_y || (grads && ((d_x && d_x == x) || v == u))) return Q4GSW_ERR_UNSUPPORTED;
   const AdaptersRef ad{static_cast<const int32_t*>(plan), L, r};
   char inner[128] = "", route[160];
-  const bool low = adapters_low_fits(ad, M);
-  cudaError_t e;
-  if (low) {
-    e = launch_adapters_low(ad, false, d_y, a, b, scale, M, K, N, v, nullptr, d_x, stream);
-  } else {
-    e = launch_adapters_down(ad, d_y, false, b, scale, M, N, v, stream);
-    if (e == cudaSuccess && d_x) e = launch_adapters_up(ad, v, false, a, nullptr, M, K, nullptr, d_x, stream);
-  }
+  cudaError_t e = launch_adapters_down(ad, d_y, false, b, scale, M, N, v, stream);
   if (e == cudaSuccess && grads)
     e = launch_adapters_grad(ad, x, v, d_a, K, d_y, u, scale, d_b, N, M, accumulate != 0, stream);
   if (e == cudaSuccess && d_x) {
-    const Epi out{h(d_x), nullptr, nullptr, h(d_x), K, kActNone, 0, 1};
-    e = launch_product_epi(true, packed, N, K, gs, f32s, d_y, M, out, stream, inner, sizeof(inner));
+    const EpiLow out{h(d_x), nullptr, nullptr, K, v, h(a), nullptr, ad.plan, M, L, r};
+    e = launch_product_low(true, packed, N, K, gs, f32s, d_y, M, out, stream, inner, sizeof(inner));
   }
-  snprintf(route, sizeof(route), "adapters %s%s%s%s", low ? "low launches=1" : d_x ? "down launches=1 + up launches=1" : "down launches=1",
+  snprintf(route, sizeof(route), "adapters %s launches=1%s%s%s", adapters_few(ad, M) ? "few" : "down",
            grads ? " + grad launches=1" : "", d_x ? " + " : "", inner);
   set_route(route);
   return from_cuda(e);

@@ -5,7 +5,9 @@
 //   OutSplit  fp32 rows, split over up to three buffers (the plain forward,
 //             the fused Q/K/V projection, the input gradient);
 //   Epi       fp16 rows, with the epilogue of a projection or of the gated
-//             feed-forward block applied to the fp32 sums in registers.
+//             feed-forward block applied to the fp32 sums in registers;
+//   EpiLow    fp16 rows of a projection with an adapter for every token
+//             (q4gsw_lowrank.cuh).
 // The epilogue adds no pass over memory: a projection followed by separate
 // bias, activation and residual passes writes and re-reads its fp32 result
 // (8 bytes an element) per pass; here each element is written once, in 2 bytes.
@@ -22,6 +24,8 @@
 #pragma once
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "q4gsw_common.cuh"
 #include "q4gsw_internal.h"
@@ -74,9 +78,11 @@ __device__ __forceinline__ float act_value_slope(float z, int act, float& slope)
 }
 
 // Whether a product reads its activations before it waits for the kernel in front.
-__device__ __forceinline__ bool reads_early(const OutSplit&) { return false; }
-__device__ __forceinline__ bool reads_early(const float*) { return false; }
-__device__ __forceinline__ bool reads_early(const Epi& o) { return o.early; }
+template <typename Out>
+constexpr bool kReadsEarly = std::is_same_v<Out, EpiLow>;
+// Whether its outputs are fp16.
+template <typename Out>
+constexpr bool kHalfOut = std::is_same_v<Out, Epi> || std::is_same_v<Out, EpiLow>;
 
 // ---------------------------------------------------------------- OutSplit
 // What an epilogue reads before it stores: nothing here.
@@ -152,6 +158,20 @@ __device__ __forceinline__ void epi_store2(const Epi& o, size_t m, int n, float 
     v1 += r.y;
   }
   *reinterpret_cast<uint32_t*>(o.y + at) = h2_as_u32(__floats2half2_rn(v0, v1));
+}
+
+// ---------------------------------------------------------------- EpiLow
+// (the term is in the sums by then)
+__device__ __forceinline__ EpiOperand epi_load4(const EpiLow& o, size_t m, int n) {
+  EpiOperand q{make_uint2(0u, 0u), make_uint2(0u, 0u)};
+  if (o.bias) q.bias = *reinterpret_cast<const uint2*>(o.bias + n);
+  if (o.res) q.res = *reinterpret_cast<const uint2*>(o.res + m * o.N + n);
+  return q;
+}
+__device__ __forceinline__ void epi_store4(const EpiLow& o, size_t m, int n, float4 v, const EpiOperand& q) {
+  const float4 b = half4_f32(q.bias), r = half4_f32(q.res);
+  *reinterpret_cast<uint2*>(o.y + m * o.N + n) =
+      f32_half4(make_float4(v.x + b.x + r.x, v.y + b.y + r.y, v.z + b.z + r.z, v.w + b.w + r.w));
 }
 
 }  // namespace q4gsw

@@ -40,6 +40,7 @@
 #include "q4gsw_common.cuh"
 #include "q4gsw_epilogue.cuh"
 #include "q4gsw_internal.h"
+#include "q4gsw_lowrank.cuh"
 #include "q4gsw_sm100.cuh"
 
 namespace cg = cooperative_groups;
@@ -80,10 +81,12 @@ struct Smem {
   static constexpr int OFF_W = OFF_P + ST * P_BYTES;
   static constexpr int OFF_SC = OFF_W + WST * W_BYTES;
   static constexpr int OFF_CTL = OFF_SC + ST * SCB;
-  static constexpr int BYTES = OFF_CTL + CTL_BYTES + 1024;
+  static constexpr int OFF_GROUPS = OFF_CTL + CTL_BYTES;
+  static constexpr int BYTES = OFF_GROUPS + (int)sizeof(lr::Groups) + 1024;
   static constexpr int TMEM_COLS = 256 * MSUB;
   static_assert(OFF_P % 1024 == 0 && OFF_W % 1024 == 0 && OFF_SC % 1024 == 0, "1024-byte aligned regions");
-  static_assert(BM * BN * 4 <= OFF_SC, "split-K staging of one sub-tile must fit below the scale buffers");
+  static constexpr int OFF_LOW = BM * BN * 4;   // behind the staging of one sub-tile
+  static_assert(OFF_LOW + (int)sizeof(lr::Scratch) <= OFF_SC, "what the epilogue has must fit below the scale buffers");
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -119,6 +122,10 @@ struct SmemCtl {
   int abort;
 };
 static_assert(sizeof(SmemCtl) <= CTL_BYTES, "control block");
+
+// With the low-rank epilogue two more warps look its groups of tokens up.
+template <typename Out>
+constexpr int kThreadsOf = kThreads + (std::is_same_v<Out, EpiLow> ? 32 * lr::kFindWarps : 0);
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -272,7 +279,7 @@ __device__ __forceinline__ void epi_tiles(const Epi& o, const OutMaps<Epi>& maps
 }
 
 template <bool BWD, int ST, int SCB, int MSUB, bool F32S, typename Out>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<Out>, 1)
 q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_constant__ CUtensorMap map_pk,
                   const __grid_constant__ CUtensorMap map_sc, const __grid_constant__ OutMaps<Out> out_maps,
                   const Args<Out> args) {
@@ -286,11 +293,12 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   SmemCtl* ctl = reinterpret_cast<SmemCtl*>(smem + OFF_CTL);
   volatile int* abort_flag = &ctl->abort;
+  [[maybe_unused]] lr::Groups* groups = reinterpret_cast<lr::Groups*>(smem + SM::OFF_GROUPS);
   const uint32_t sbase = smem_u32(smem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int tile_n = blockIdx.x, tile_m = blockIdx.y;
-  if constexpr (std::is_same_v<Out, Epi>) {   // a range of the tiles (gemm_variant)
+  if constexpr (kHalfOut<Out>) {   // a range of the tiles (gemm_variant)
     tile_m = (args.tile0 + blockIdx.x) / args.tiles_n;
     tile_n = args.tile0 + blockIdx.x - tile_m * args.tiles_n;
   }
@@ -314,6 +322,7 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
     mbar_init(&ctl->drain, 1);
     mbar_init(&ctl->res[0], 1);
     mbar_init(&ctl->res[1], 1);
+    if constexpr (std::is_same_v<Out, EpiLow>) groups->count[0] = groups->count[1] = groups->fits = 0;
     ctl->abort = 0;
     fence_mbar_init();
     prefetch_tmap(&map_act);
@@ -358,7 +367,7 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
         mbar_arrive_expect_tx(&ctl->full[it], A_STAGE + P_BYTES + args.sc_bytes);
         load_weights(it);
       }
-      if (!reads_early(args.out)) griddep_wait();
+      if (!kReadsEarly<Out>) griddep_wait();
       for (int it = 0; it < pre; ++it) load_act(it);
       int issued = pre;
       for (int it = pre; it < nit; ++it) {
@@ -404,6 +413,18 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
       mma_commit(&ctl->accfull);
       mma_commit(&ctl->drain);
       mbar_wait_teardown(&ctl->drain, 0);
+    }
+  } else if (std::is_same_v<Out, EpiLow> && warp >= 2 + kDequantWarps) {
+    // ------------------------------------------------------------ adapters
+    if constexpr (std::is_same_v<Out, EpiLow>) {
+      const int r = S > 1 ? split : 0;      // this CTA's rows of each sub-tile, as below
+      lr::Ranges range;
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        range.begin[l] = l < MSUB ? min(args.M, m0 + l * BM + r * BM / S) : 0;
+        range.end[l] = l < MSUB ? min(args.M, m0 + l * BM + (r + 1) * BM / S) : 0;
+      }
+      lr::find(args.out, groups, range, threadIdx.x - 32 * (2 + kDequantWarps));
     }
   } else {
     // ------------------------------------------------------------ dequantisation
@@ -494,7 +515,8 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
   // then copy whole rows out, so each warp store covers 512 contiguous bytes
   // of one output row; with split-K the copy-out also sums the S partial
   // tiles of the cluster.
-  const bool epi = warp >= 2;
+  const bool epi = warp >= 2 && warp < 2 + kDequantWarps;
+  constexpr int kThreads = kThreadsOf<Out>;
   float* stage_f32 = reinterpret_cast<float*>(smem);   // staging [128][256] fp32, 16-byte chunks swizzled
   griddep_wait();   // outputs may still be read by the previous kernel of the stream
   bool have_acc = false;
@@ -508,9 +530,17 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
 #pragma unroll 1
   for (int ms = 0; ms < (by_tensor ? 0 : MSUB); ++ms) {
     const int mb = m0 + ms * BM;
+    int tid = threadIdx.x;
+    // (what the epilogues of both sub-tiles share is not worth registers around this loop)
+    if constexpr (std::is_same_v<Out, EpiLow>) asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
     if (epi && have_acc) {
-      const int q = warp & 3, h = (warp - 2) >> 2;
-      const int row = 32 * q + lane;
+      if constexpr (std::is_same_v<Out, EpiLow>) {   // the operand rings are idle
+        const int row_b = split * BM / S;
+        lr::stage(args.out, reinterpret_cast<lr::Scratch*>(smem + SM::OFF_LOW), mb + row_b,
+                  min((split + 1) * BM / S, args.M - mb) - row_b, tid - 64, 32 * kDequantWarps);
+      }
+      const int q = tid >> 5 & 3, h = ((tid >> 5) - 2) >> 2;
+      const int row = 32 * q + (tid & 31);
 #pragma unroll 1
       for (int c32 = 0; c32 < 2; ++c32) {
         const int col = 64 * h + 32 * c32;
@@ -526,7 +556,38 @@ q4gsw_gemm_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_cons
         }
       }
     }
-    if (S == 1) {   // fp32 rows (fp16 ones went by tensor)
+    if constexpr (std::is_same_v<Out, EpiLow>) {
+      // The low-rank term, to this CTA's own sums, or partial sums, of the rows that it writes
+      // (all threads, aborted or not), then those rows.
+      cg::cluster_group cluster = cg::this_cluster();
+      if (S > 1) cluster.sync();
+      else __syncthreads();
+      const int row_b = split * BM / S, n = min((split + 1) * BM / S, args.M - mb) - row_b;
+      const uint32_t parked = smem_u32(stage_f32);
+      auto at = [&](int row, int chunk) {
+        const int r = row_b + row;
+        return parked + 4u * (uint32_t)(r * 256 + 4 * (chunk ^ (r & 7)));
+      };
+      if (n > 0)
+        lr::add_terms<!BWD, BN, kThreads>(args.out, groups, ms, false, reinterpret_cast<lr::Scratch*>(smem + SM::OFF_LOW),
+                                          n, n0, [&](int row, int col) { return at(row, col >> 2); });
+      const bool aborted = S > 1 ? cluster_any_abort(cluster, &ctl->abort, S) : *abort_flag != 0;
+      if (!aborted && groups->fits) {
+#pragma unroll 2
+        for (int idx = tid; idx < n * 64; idx += kThreads) {
+          const int row = idx >> 6, c = n0 + 4 * (idx & 63);
+          if (c >= args.out_cols) continue;
+          const size_t m = (size_t)(mb + row_b + row);
+          const uint32_t from = at(row, idx & 63);
+          const EpiOperand operand = epi_load4(args.out, m, c);
+          const float4 v = S == 1 ? ld_shared_f4(from)
+                                  : lr::add_parts<4>(S, [&](int k) { return ld_dsmem_v4(mapa_u32(from, (uint32_t)k)); });
+          epi_store4(args.out, m, c, v, operand);
+        }
+      }
+      if (S > 1) cluster.sync();
+      else __syncthreads();
+    } else if (S == 1) {   // (Epi: by tensor)
       __syncthreads();
       const int rows = args.M - mb < BM ? args.M - mb : BM;
       if constexpr (std::is_same_v<Out, OutSplit>) {
@@ -649,7 +710,7 @@ static cudaError_t gemm_variant(const CUtensorMap& map_act, const CUtensorMap& m
   }
   const int tiles_m = (a.M + BM * MSUB - 1) / (BM * MSUB);
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kThreadsOf<Out>, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -682,7 +743,7 @@ static cudaError_t gemm_variant(const CUtensorMap& map_act, const CUtensorMap& m
       best_S = S;
     }
   }
-  if constexpr (std::is_same_v<Out, Epi>) {
+  if constexpr (kHalfOut<Out>) {
     // Whole waves of unsplit tiles, and what is left over in a second launch
     // that splits the contraction so that it fills the SMs, too: a launch's gap
     // and a shorter wave instead of a whole one.  (The fp32 products keep one
@@ -822,7 +883,7 @@ static cudaError_t launch_gemm_impl(const void* packed, int N, int K, int gs, co
   if (route)
     snprintf(route, route_len, "tcgen05_gemm_%s launches=%d tile=%dx%dx%d stages=%d+%d grid=%dx%dx%d",
              BWD ? "bwd" : "fwd", S < 0 ? 2 : 1, BM * msub, BN, TK, st, WST, tiles_n, tiles_m, S < 0 ? 1 : S);
-  if (route && std::is_same_v<Out, Epi>) {
+  if (route && kHalfOut<Out>) {
     size_t len = strlen(route);
     if (S < 0) {
       snprintf(route + len, route_len - len, " rest_splits=%d", -S);
@@ -904,25 +965,36 @@ static bool epi_on_ss_route(int M, int rows, int contraction) {
 
 // The products with fp16 outputs through an epilogue (any M): the same routes,
 // but for the register-fed GEMVs, which have none (their pin is passed over).
-template <bool BWD, bool F32S>
-static cudaError_t product_epi(const void* packed, int N, int K, int gs, const uint16_t* act, int M, const Epi& out,
+template <bool BWD, bool F32S, typename Out>
+static cudaError_t product_epi(const void* packed, int N, int K, int gs, const uint16_t* act, int M, const Out& out,
                                cudaStream_t stream, char* route, int route_len) {
   if (M <= kGemvMaxM) {
     return BWD ? gemv_tma_bwd_impl(packed, N, K, gs, F32S, act, M, out, stream, route, route_len)
                : gemv_tma_fwd_impl(packed, N, K, gs, F32S, act, M, out, stream, route, route_len);
   }
   return epi_on_ss_route(M, BWD ? K : N, BWD ? N : K)
-             ? launch_gemm_impl<BWD, F32S>(packed, N, K, gs, act, M, out, stream, route, route_len)
-             : launch_gemm_ts_impl<BWD, F32S>(packed, N, K, gs, act, M, out, stream, route, route_len);
+             ? launch_gemm_impl<BWD, F32S, Out>(packed, N, K, gs, act, M, out, stream, route, route_len)
+             : launch_gemm_ts_impl<BWD, F32S, Out>(packed, N, K, gs, act, M, out, stream, route, route_len);
 }
 
-cudaError_t launch_product_epi(bool bwd, const void* packed, int N, int K, int gs, bool f32s, const uint16_t* act,
-                               int M, const Epi& out, cudaStream_t stream, char* route, int route_len) {
+template <typename Out>
+static cudaError_t product_half(bool bwd, const void* packed, int N, int K, int gs, bool f32s, const uint16_t* act,
+                                int M, const Out& out, cudaStream_t stream, char* route, int route_len) {
   if (bwd)
     return f32s ? product_epi<true, true>(packed, N, K, gs, act, M, out, stream, route, route_len)
                 : product_epi<true, false>(packed, N, K, gs, act, M, out, stream, route, route_len);
   return f32s ? product_epi<false, true>(packed, N, K, gs, act, M, out, stream, route, route_len)
               : product_epi<false, false>(packed, N, K, gs, act, M, out, stream, route, route_len);
+}
+
+cudaError_t launch_product_epi(bool bwd, const void* packed, int N, int K, int gs, bool f32s, const uint16_t* act,
+                               int M, const Epi& out, cudaStream_t stream, char* route, int route_len) {
+  return product_half(bwd, packed, N, K, gs, f32s, act, M, out, stream, route, route_len);
+}
+
+cudaError_t launch_product_low(bool bwd, const void* packed, int N, int K, int gs, bool f32s, const uint16_t* act,
+                               int M, const EpiLow& out, cudaStream_t stream, char* route, int route_len) {
+  return product_half(bwd, packed, N, K, gs, f32s, act, M, out, stream, route, route_len);
 }
 
 __global__ void q4gsw_error_exchange_kernel(unsigned int slot) {

@@ -59,9 +59,11 @@ struct Smem {
   static constexpr int OFF_P = OFF_X + ST * X_BYTES;
   static constexpr int OFF_SC = OFF_P + ST * P_BYTES;
   static constexpr int OFF_CTL = OFF_SC + ST * SCB;
-  static constexpr int BYTES = OFF_CTL + CTL_BYTES + 1024;
+  static constexpr int OFF_GROUPS = OFF_CTL + CTL_BYTES;
+  static constexpr int BYTES = OFF_GROUPS + (int)sizeof(lr::Groups) + 1024;
   static_assert(OFF_P % 1024 == 0 && OFF_SC % 1024 == 0, "1024-byte aligned regions");
-  static_assert((BT_MAX + 7) * BW * 4 <= OFF_SC, "split-K receive slots must fit below the scale slots");
+  static constexpr int OFF_LOW = (BT_MAX + 7) * BW * 4;   // behind the split-K receive slots, or the parked tile
+  static_assert(OFF_LOW + (int)sizeof(lr::Scratch) <= OFF_SC, "what the epilogue has must fit below the scale slots");
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -93,6 +95,10 @@ struct Ctl {
   int abort;
 };
 static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
+
+// With the low-rank epilogue two more warps look its groups of tokens up.
+template <typename Out>
+constexpr int kThreadsOf = kThreads + (std::is_same_v<Out, EpiLow> ? 32 * lr::kFindWarps : 0);
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -133,8 +139,8 @@ __device__ __forceinline__ void copy_out(const float* stage_f32, bool pushed, in
   // at most 12 float4 in flight (8 with an epilogue, whose operands take
   // registers too: with 12 they spilled, and a 512-token gated forward of 16384
   // rows took 44.3 us instead of 38.1)
-  constexpr int kMost = std::is_same_v<Out, Epi> ? 8 : 12;
-  constexpr int kPer = S == 1 ? (std::is_same_v<Out, Epi> ? 4 : 8) : (kMost / S > 0 ? kMost / S : 1);
+  constexpr int kMost = kHalfOut<Out> ? 8 : 12;
+  constexpr int kPer = S == 1 ? (kHalfOut<Out> ? 4 : 8) : (kMost / S > 0 ? kMost / S : 1);
   using Operand = decltype(epi_load4(args.out, size_t(0), 0));   // what the epilogue reads (nothing for fp32 rows)
   uint32_t src[S];   // rank qq's partial rows, in the cluster's shared window
 #pragma unroll
@@ -143,6 +149,7 @@ __device__ __forceinline__ void copy_out(const float* stage_f32, bool pushed, in
                      : (S == 1 ? smem_u32(stage_f32) : mapa_u32(smem_u32(stage_f32), (uint32_t)qq));
   const int r0 = pushed ? 0 : row_b;   // row of row_b in the source layout
   const int total = (row_e - row_b) * (BW / 4);
+  constexpr int kThreads = kThreadsOf<Out>;
   for (int base = threadIdx.x; base < total; base += kThreads * kPer) {
     float4 part[kPer][S];
     Operand opd[kPer];
@@ -181,7 +188,7 @@ __device__ __forceinline__ void copy_out(const float* stage_f32, bool pushed, in
 }
 
 template <bool BWD, int ST, bool F32S, typename Out>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<Out>, 1)
 q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_constant__ CUtensorMap map_pk,
                      const __grid_constant__ CUtensorMap map_sc, const __grid_constant__ CUtensorMap map_y0,
                      const __grid_constant__ CUtensorMap map_y1, const __grid_constant__ CUtensorMap map_y2,
@@ -195,6 +202,7 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + SM::OFF_CTL);
   volatile int* abort_flag = &ctl->abort;
+  [[maybe_unused]] lr::Groups* groups = reinterpret_cast<lr::Groups*>(smem + SM::OFF_GROUPS);
   const uint32_t sbase = smem_u32(smem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -217,6 +225,7 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
     mbar_init(&ctl->accfull, 1);
     mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
+    if constexpr (std::is_same_v<Out, EpiLow>) groups->count[0] = groups->count[1] = groups->fits = 0;
     fence_mbar_init();
     prefetch_tmap(&map_act);
     prefetch_tmap(&map_pk);
@@ -264,7 +273,7 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
         mbar_arrive_expect_tx(&ctl->full[it], it < nit ? tx : tx_ad);
         if (it < nit) load_weights(it);
       }
-      if (!reads_early(args.out)) griddep_wait();
+      if (!kReadsEarly<Out>) griddep_wait();
       for (int it = 0; it < pre; ++it) load_act(it);
       int issued = pre;
       for (int it = pre; it < nitx; ++it) {
@@ -332,6 +341,19 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
       mma_commit(&ctl->accfull);
       mma_commit(&ctl->drain);
       mbar_wait_teardown(&ctl->drain, 0);
+    }
+  } else if (std::is_same_v<Out, EpiLow> && warp >= 2 + kDequantWarps) {
+    // ------------------------------------------------------------ adapters
+    if constexpr (std::is_same_v<Out, EpiLow>) {
+      const int me = S > 1 ? split : 0;      // this CTA's token rows, as below
+      const int row_b = me * args.bt / S, row_e = min((me + 1) * args.bt / S, args.M - t0);
+      lr::Ranges range;
+#pragma unroll
+      for (int l = 0; l < 2; ++l) {
+        range.begin[l] = t0 + min(row_b + l * lr::kChunk, max(row_b, row_e));
+        range.end[l] = t0 + min(row_b + (l + 1) * lr::kChunk, max(row_b, row_e));
+      }
+      lr::find(args.out, groups, range, threadIdx.x - 32 * (2 + kDequantWarps));
     }
   } else {
     // ------------------------------------------------------------ dequantisation
@@ -473,13 +495,20 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
   // Warp w (2..17) reads TMEM lanes 32 (w % 4) .. +31 (weight rows) and the
   // token columns [64 c, 64 c + 64) with c = (w - 2) / 4, and parks them in
   // shared memory (the operand ring is idle by now) as [token][128 features].
-  const bool epi = warp >= 2;
+  const bool epi = warp >= 2 && warp < 2 + kDequantWarps;
   griddep_wait();   // outputs may still be read by the previous kernel of the stream
+  [[maybe_unused]] lr::Scratch* scratch = reinterpret_cast<lr::Scratch*>(smem + SM::OFF_LOW);
   bool have_acc = false;
   if (epi) {
     have_acc = mbar_wait(&ctl->accfull, 0, abort_flag, &g_device_error, 16u);
     have_acc = __all_sync(0xffffffffu, have_acc);
     if (have_acc) tc_fence_after();
+    if constexpr (std::is_same_v<Out, EpiLow>) {   // the operand ring is idle
+      const int row_b = split * args.bt / S, row_e = min((split + 1) * args.bt / S, args.M - t0);
+      if (have_acc)
+        lr::stage(args.out, scratch, t0 + row_b, min(lr::both_lists(args.out.r) ? 2 * lr::kChunk : lr::kChunk, row_e - row_b),
+                  threadIdx.x - 64, 32 * kDequantWarps);
+    }
   }
   float* stage_f32 = reinterpret_cast<float*>(smem);   // the operand ring, idle by now
   // Park the tile in this CTA's shared memory as [token][128 features].
@@ -496,6 +525,24 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 32; ++j) stage_f32[(col + j) * BW + r] = __uint_as_float(v[j]);
+    }
+  };
+  // EpiLow: the term of tokens [row_b, row_e) of the tile, whose sums stand at `sums`, and
+  // whether anything is written at all.  All threads.
+  bool writes = true;
+  auto add_low = [&](float* sums, int row_b, int row_e) {
+    if constexpr (std::is_same_v<Out, EpiLow>) {
+      row_e = min(row_e, args.M - t0);
+      const int rows = lr::both_lists(args.out.r) ? 2 * lr::kChunk : lr::kChunk;   // at a time
+#pragma unroll 1
+      for (int b = row_b; b < row_e; b += rows) {
+        if (b > row_b) lr::stage(args.out, scratch, t0 + b, min(rows, row_e - b), threadIdx.x, kThreadsOf<Out>);
+        const uint32_t from = smem_u32(sums + (b - row_b) * BW);
+        lr::add_terms<!BWD, BW, kThreadsOf<Out>>(args.out, groups, (b - row_b) / lr::kChunk,
+                                                 row_e - b > lr::kChunk && rows > lr::kChunk, scratch, min(rows, row_e - b), f0,
+                                                 [&](int row, int col) { return from + 4u * (uint32_t)(row * BW + col); });
+      }
+      writes = groups->fits;
     }
   };
   if (S == 1) {
@@ -520,7 +567,8 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
     }
     if (!by_tma) {
       __syncthreads();
-      if (!*abort_flag) copy_out<1>(stage_f32, false, 0, 0, args.bt, t0, f0, args);
+      add_low(stage_f32, 0, args.bt);
+      if (!*abort_flag && writes) copy_out<1>(stage_f32, false, 0, 0, args.bt, t0, f0, args);
     }
   } else {
     // Split-K: rank rk owns token rows [rk bt / S, (rk + 1) bt / S) and adds
@@ -578,7 +626,8 @@ q4gsw_gemm_ts_kernel(const __grid_constant__ CUtensorMap map_act, const __grid_c
       }
       cluster_barrier();   // every partial row delivered
     }
-    if (!aborted) {
+    add_low(stage_f32 + (push ? me * rmax : row_b) * BW, row_b, row_e);   // to this CTA's own partial sums of its rows
+    if (!aborted && writes) {
       switch (S) {
         case 2: copy_out<2>(stage_f32, push, rmax * BW, row_b, row_e, t0, f0, args); break;
         case 3: copy_out<3>(stage_f32, push, rmax * BW, row_b, row_e, t0, f0, args); break;
@@ -706,7 +755,7 @@ static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs,
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kThreadsOf<Out>, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -772,7 +821,7 @@ static cudaError_t launch_gemm_ts_impl(const void* packed, int N, int K, int gs,
   if (route)
     snprintf(route, route_len, "tcgen05_ts_gemm_%s launches=1 tile=%dx%dx%d stages=%d+%d grid=%dx%dx%d out=%s%s",
              BWD ? "bwd" : "fwd", BW, a.bt, TK, ST, ST, tiles_f, tiles_t, best_S,
-             std::is_same_v<Out, Epi> ? "epi" : a.tma_out ? "tma" : "st", ad ? " adapter_stage=1" : "");
+             kHalfOut<Out> ? "epi" : a.tma_out ? "tma" : "st", ad ? " adapter_stage=1" : "");
   return cudaLaunchKernelEx(&cfg, kern, map_act, map_pk, map_sc, map_y[0], map_y[1], map_y[2], map_ad, a);
 }
 

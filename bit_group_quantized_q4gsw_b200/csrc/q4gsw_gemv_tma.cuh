@@ -75,6 +75,7 @@ struct Ctl {
   uint64_t full[12];
   uint64_t empty[12];
   int abort;
+  int16_t adapter[16];   // of each token (EpiLow; at most 16 tokens, one z-slice)
 };
 static_assert(sizeof(Ctl) <= CTL_BYTES, "control block");
 
@@ -158,7 +159,7 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
 
   if (warp == C::CW) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    {
       auto load_weights = [&](int it) {
         const int s = it % C::ST;
         const int kc = (st_begin + it) * SK;
@@ -177,32 +178,42 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
       // the packed weight is constant: the ring is filled before (and while)
       // the consumers wait for the kernel that produces x
       const int pre = nit < C::ST ? nit : C::ST;
-      for (int it = 0; it < pre; ++it) {
-        mbar_arrive_expect_tx(&ctl->full[it], tx);
-        load_weights(it);
+      if (lane == 0) {
+        for (int it = 0; it < pre; ++it) {
+          mbar_arrive_expect_tx(&ctl->full[it], tx);
+          load_weights(it);
+        }
+        if (XS) {
+          if (!kReadsEarly<Out>) griddep_wait();
+          for (int it = 0; it < pre; ++it) load_x(it);
+        }
       }
-      if (XS) {
-        if (!reads_early(out)) griddep_wait();
-        for (int it = 0; it < pre; ++it) load_x(it);
+      if constexpr (std::is_same_v<Out, EpiLow>) {   // the whole warp, while the first stages are on their way
+        __syncwarp();
+        lr::few_adapters(out, ctl->adapter);
+        const int rk = blockIdx.y;                   // the rank in the cluster, which is a column of the grid
+        lr::few_prefetch<true>(out, ctl->adapter, rk * Mz / S, (rk + 1) * Mz / S, n0, min(64, N - n0));
       }
-      int issued = pre;
-      for (int it = pre; it < nit; ++it) {
-        const int s = it % C::ST;
-        if (!mbar_wait(&ctl->empty[s], ((it / C::ST) - 1) & 1, abort_flag, &g_device_error, 64u)) break;
-        mbar_arrive_expect_tx(&ctl->full[s], tx);
-        load_weights(it);
-        if (XS) load_x(it);
-        issued = it + 1;
+      if (lane == 0) {
+        int issued = pre;
+        for (int it = pre; it < nit; ++it) {
+          const int s = it % C::ST;
+          if (!mbar_wait(&ctl->empty[s], ((it / C::ST) - 1) & 1, abort_flag, &g_device_error, 64u)) break;
+          mbar_arrive_expect_tx(&ctl->full[s], tx);
+          load_weights(it);
+          if (XS) load_x(it);
+          issued = it + 1;
+        }
+        for (int it = (issued > C::ST ? issued - C::ST : 0); it < issued; ++it)
+          mbar_wait_teardown(&ctl->full[it % C::ST], (it / C::ST) & 1);
       }
-      for (int it = (issued > C::ST ? issued - C::ST : 0); it < issued; ++it)
-        mbar_wait_teardown(&ctl->full[it % C::ST], (it / C::ST) & 1);
     }
   } else {
     // ------------------------------------------------------------ consumers
     // outputs of this kernel may still be read by the previous one; a product that reads
     // early waits in its epilogue, and makes sure here that no older line of x is in L1
     // (x by TMA comes from L2)
-    if (!reads_early(out)) griddep_wait();
+    if (!kReadsEarly<Out>) griddep_wait();
     else if (!XS) __threadfence();
     const int w = warp & 3;             // 64-column block of every stage
     const int rt0 = (warp >> 2) * RTW;  // first row tile of this warp
@@ -405,7 +416,7 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
         else out.y2[m * (out.N - out.n2) + (n - out.n2)] = v;
       }
     } else {
-      if (reads_early(out)) griddep_wait();   // the residual
+      if (kReadsEarly<Out>) griddep_wait();   // the low-rank intermediate; what y held may be read until then
       // pairs of features (N % 8 == 0: a pair is wholly inside or outside)
       for (int e = threadIdx.x; e < (te - tb) * 32; e += C::THREADS) {
         const int tok = tb + (e >> 5), nl = 2 * (e & 31);
@@ -416,7 +427,8 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
           v.x += p.x;
           v.y += p.y;
         }
-        epi_store2(out, (size_t)(tok0 + tok), n0 + nl, v.x, v.y);
+        if constexpr (std::is_same_v<Out, EpiLow>) lr::finish_pair<true>(out, ctl->adapter[tok], tok, n0 + nl, v);
+        else epi_store2(out, (size_t)(tok0 + tok), n0 + nl, v.x, v.y);
       }
     }
   }
@@ -508,7 +520,7 @@ q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    {
       auto load_weights = [&](int it) {
         const int s = it % C::ST;
         const int n0 = (st_begin + it) * 128;
@@ -524,27 +536,37 @@ q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
         tma_load_2d(ds + C::DBOX, &map_d, &ctl->full[s], n0 + 64, tok0);
       };
       const int pre = nit < C::ST ? nit : C::ST;
-      for (int it = 0; it < pre; ++it) {
-        mbar_arrive_expect_tx(&ctl->full[it], tx);
-        load_weights(it);
+      if (lane == 0) {
+        for (int it = 0; it < pre; ++it) {
+          mbar_arrive_expect_tx(&ctl->full[it], tx);
+          load_weights(it);
+        }
+        if (!kReadsEarly<Out>) griddep_wait();   // d_out may come from the previous kernel of the stream
+        for (int it = 0; it < pre; ++it) load_d(it);
       }
-      if (!reads_early(dx)) griddep_wait();   // d_out may come from the previous kernel of the stream
-      for (int it = 0; it < pre; ++it) load_d(it);
-      int issued = pre;
-      for (int it = pre; it < nit; ++it) {
-        const int s = it % C::ST;
-        if (!mbar_wait(&ctl->empty[s], ((it / C::ST) - 1) & 1, abort_flag, &g_device_error, 64u)) break;
-        mbar_arrive_expect_tx(&ctl->full[s], tx);
-        load_weights(it);
-        load_d(it);
-        issued = it + 1;
+      if constexpr (std::is_same_v<Out, EpiLow>) {   // the whole warp, while the first stages are on their way
+        __syncwarp();
+        lr::few_adapters(dx, ctl->adapter);
+        const int rk = blockIdx.y;
+        lr::few_prefetch<false>(dx, ctl->adapter, rk * Mz / S, (rk + 1) * Mz / S, kbase, min(128, K - kbase));
       }
-      for (int it = (issued > C::ST ? issued - C::ST : 0); it < issued; ++it)
-        mbar_wait_teardown(&ctl->full[it % C::ST], (it / C::ST) & 1);
+      if (lane == 0) {
+        int issued = pre;
+        for (int it = pre; it < nit; ++it) {
+          const int s = it % C::ST;
+          if (!mbar_wait(&ctl->empty[s], ((it / C::ST) - 1) & 1, abort_flag, &g_device_error, 64u)) break;
+          mbar_arrive_expect_tx(&ctl->full[s], tx);
+          load_weights(it);
+          load_d(it);
+          issued = it + 1;
+        }
+        for (int it = (issued > C::ST ? issued - C::ST : 0); it < issued; ++it)
+          mbar_wait_teardown(&ctl->full[it % C::ST], (it / C::ST) & 1);
+      }
     }
   } else {
     // ------------------------------------------------------------ consumers
-    if (!reads_early(dx)) griddep_wait();   // outputs may still be read by the previous kernel
+    if (!kReadsEarly<Out>) griddep_wait();   // outputs may still be read by the previous kernel
     const int c = warp - 1;
     const int rowA = 8 * c + t, rowB = rowA + 4;   // pair rows of the stage
     const int J = g >> 2;                          // 64-column block of this lane
@@ -664,7 +686,7 @@ q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
         dx[(size_t)(tok0 + tok) * K + kbase + kl] = v;
       }
     } else {
-      if (reads_early(dx)) griddep_wait();   // the residual
+      if (kReadsEarly<Out>) griddep_wait();   // the low-rank intermediate; what d_x held may be read until then
       for (int e = tb * 128 + 2 * threadIdx.x; e < te * 128; e += 2 * kBwdThreads) {
         const int tok = e >> 7, kl = e & 127;
         if (kl >= kw) continue;   // kw is a multiple of 64
@@ -674,7 +696,8 @@ q4gsw_gemv_bwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
           v.x += p.x;
           v.y += p.y;
         }
-        epi_store2(dx, (size_t)(tok0 + tok), kbase + kl, v.x, v.y);
+        if constexpr (std::is_same_v<Out, EpiLow>) lr::finish_pair<false>(dx, ctl->adapter[tok], tok, kbase + kl, v);
+        else epi_store2(dx, (size_t)(tok0 + tok), kbase + kl, v.x, v.y);
       }
     }
   }
@@ -770,7 +793,7 @@ static cudaError_t gemv_tma_fwd_impl(const void* packed, int N, int K, int gs, b
 #undef Q4_TMA_FWD_X
   if (route)
     snprintf(route, route_len, "gemv_tma_fwd launches=1 nt=%d tiles=%d splits=%d zslices=%d stages=%d%s%s", NT, tiles,
-             S, zs, stages_total, xs ? " x=staged" : "", std::is_same_v<Out, Epi> ? " out=epi" : "");
+             S, zs, stages_total, xs ? " x=staged" : "", kHalfOut<Out> ? " out=epi" : "");
   return e;
 }
 
@@ -779,7 +802,7 @@ cudaError_t launch_gemv_tma_fwd(const void* packed, int N, int K, int gs, bool f
   return gemv_tma_fwd_impl(packed, N, K, gs, f32s, x, M, out, stream, route, route_len);
 }
 
-// Out: float* (fp32 rows) or Epi (fp16 rows)
+// Out: float* (fp32 rows), Epi or EpiLow (fp16 rows)
 template <typename Out>
 static cudaError_t gemv_tma_bwd_impl(const void* packed, int N, int K, int gs, bool f32s, const uint16_t* d_out, int M,
                                      Out d_x, cudaStream_t stream, char* route, int route_len) {
@@ -838,7 +861,7 @@ static cudaError_t gemv_tma_bwd_impl(const void* packed, int N, int K, int gs, b
 #undef Q4_TMA_BWD
   if (route)
     snprintf(route, route_len, "gemv_tma_bwd launches=1 nt=%d tiles=%d splits=%d zslices=%d stages=%d%s", NT, tiles, S,
-             zs, stages_total, std::is_same_v<Out, Epi> ? " out=epi" : "");
+             zs, stages_total, kHalfOut<Out> ? " out=epi" : "");
   return e;
 }
 

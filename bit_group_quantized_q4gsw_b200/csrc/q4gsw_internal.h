@@ -70,10 +70,7 @@ __host__ __device__ inline OutSplit single_output(float* y, int N) { return OutS
 //   gated   v = (g, u) pairs (weight rows interleaved): y[m, j] = act(g_j) u_j,
 //           z[m, 2 j] = g_j, z[m, 2 j + 1] = u_j
 //   else    z[m, n] = v + bias[n],  y[m, n] = act(z) + res[m, n]
-// bias, res and z may be null; y may be res.  early: the product's activations were
-// complete before the kernel in front of it could start (the first kernel behind them
-// lets its successors start only behind its own wait), so they are read at once and only
-// the epilogue waits for that kernel, which may still be writing the residual.
+// bias, res and z may be null; y may be res.
 enum ActKind { kActNone = 0, kActSilu = 1, kActGelu = 2 };
 struct Epi {
   __half* y;
@@ -83,7 +80,25 @@ struct Epi {
   int N;
   int act;
   int gated;
-  int early = 0;
+};
+
+// The same of a product with an adapter for every token (q4gsw_lowrank.cuh):
+//   y[m, n] = v + scale[a] sum_j inter[m, j] P_a(n, j) + bias[n] + res[m, n]
+// for the tokens with an adapter a in the plan.  mat: [L, N, r], or [L, r, N] for the
+// input gradient; scale may be null.  The product's activations were complete before the
+// kernel in front of it could start (that kernel lets its successors start only behind
+// its own wait), so they are read at once, and only the epilogue waits for that
+// kernel, which writes inter.
+struct EpiLow {
+  __half* y;
+  const __half* bias;
+  const __half* res;
+  int N;
+  const float* inter;
+  const __half* mat;
+  const float* scale;
+  const int32_t* plan;
+  int M, L, r;
 };
 
 // The compute launchers take f32s = the packed blob has fp32 scales (layout
@@ -97,6 +112,8 @@ cudaError_t launch_gemv_bwd(const void* packed, int N, int K, int gs, bool f32s,
 
 // The same products with fp16 outputs through an epilogue: any M >= 1, the
 // GEMV up to kGemvMaxM tokens, the GEMMs above.
+cudaError_t launch_product_low(bool bwd, const void* packed, int N, int K, int gs, bool f32s, const uint16_t* act,
+                               int M, const EpiLow& out, cudaStream_t stream, char* route, int route_len);
 cudaError_t launch_product_epi(bool bwd, const void* packed, int N, int K, int gs, bool f32s, const uint16_t* act,
                                int M, const Epi& out, cudaStream_t stream, char* route, int route_len);
 
@@ -176,9 +193,9 @@ cudaError_t launch_distill_bwd(const DistillArgs& a, bool half_logits, cudaStrea
 cudaError_t device_error_word(unsigned int** word);
 
 // Adapters of many requests (q4gsw_adapters.cu; the plan: q4gsw_adapters.cuh).
-// down: out fp32 [M][r] = (scale) act P;  up: out fp16 [M][C] = res + scale inter P;
+// down: out fp32 [M][r] = (scale) act P, the adapters' matrices [r, C] (by_rows: A) or
+// [C, r] (B), by one kernel for few tiles (adapters_few) and another for many;
 // grad: d_a = sums over each adapter's tokens of v^T x, d_b of scale d_y^T u, fp32.
-// by_rows: the adapters' matrices are [r, C] for down (A) and [C, r] for up (B).
 struct AdaptersRef {
   const int32_t* plan;
   int L, r;
@@ -187,14 +204,7 @@ constexpr int kMaxAdapterFeatures = 64 * 65535;
 cudaError_t launch_adapters_plan(const int32_t* ids, int M, int L, void* plan, cudaStream_t stream);
 cudaError_t launch_adapters_down(const AdaptersRef& ad, const uint16_t* act, bool by_rows, const uint16_t* proj,
                                  const float* scale, int M, int C, float* out, cudaStream_t stream);
-cudaError_t launch_adapters_up(const AdaptersRef& ad, const float* inter, bool by_rows, const uint16_t* proj,
-                               const float* scale, int M, int C, const uint16_t* res, uint16_t* out,
-                               cudaStream_t stream);
-// down and up in one launch, for few tiles (adapters_low_fits)
-bool adapters_low_fits(const AdaptersRef& ad, int M);
-cudaError_t launch_adapters_low(const AdaptersRef& ad, bool fwd, const uint16_t* act, const uint16_t* a,
-                                const uint16_t* b, const float* scale, int M, int K, int N, float* inter,
-                                const uint16_t* res, uint16_t* out, cudaStream_t stream);
+bool adapters_few(const AdaptersRef& ad, int M);
 cudaError_t launch_adapters_grad(const AdaptersRef& ad, const uint16_t* x, const float* v, float* d_a, int K,
                                  const uint16_t* d_y, const float* u, const float* scale, float* d_b, int N, int M,
                                  bool accumulate, cudaStream_t stream);

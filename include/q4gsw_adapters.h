@@ -57,7 +57,7 @@ Q4GSW_API q4gsw_status q4gsw_adapters_plan(const int32_t *ids, int M, int L, voi
                                  q4gsw_stream_t stream);
 
 /*
- * Forward, two launches (three, or four, for many tokens): x fp16 [M, K], a fp16 [L, r, K], b fp16 [L, N, r] ->
+ * Forward, two launches (three for some numbers of tokens): x fp16 [M, K], a fp16 [L, r, K], b fp16 [L, N, r] ->
  * y fp16 [M, N], u fp32 [M, r] (what the backward pass reads; always written).
  *   plan      of the same M and L; with another one nothing is computed, and
  *             q4gsw_device_error_check returns Q4GSW_ERR_INDEX
@@ -65,9 +65,9 @@ Q4GSW_API q4gsw_status q4gsw_adapters_plan(const int32_t *ids, int M, int L, voi
  *   bias      fp16 [N] or NULL
  *   residual  fp16 [M, N] or NULL; y may be the residual's buffer (but not x's, also
  *             where the residual is x: Q4GSW_ERR_UNSUPPORTED)
- * The low-rank term, with the residual, is rounded to fp16 once before the base
- * product is added to it and the sum rounded: y is off by at most half a unit in
- * the last place of each beside the error of q4gsw_linear_act_fwd.
+ * The base product, the low-rank term, bias and residual are added in fp32 and y is
+ * rounded once: the term, or its sum with the residual, may pass fp16's range where
+ * the base product brings it back.
  */
 Q4GSW_API q4gsw_status q4gsw_adapters_fwd(const void *packed, int N, int K, int group_size, const void *plan,
                                 const uint16_t *a, const uint16_t *b, const float *scale, int L, int r,
@@ -81,8 +81,8 @@ Q4GSW_API q4gsw_status q4gsw_adapters_fwd_f32s(const void *packed, int N, int K,
 /*
  * Backward: d_y fp16 [M, N], x and u as in and of the forward ->
  *   v    fp32 [M, r], a workspace that is written; always needed
- *   d_x  fp16 [M, K] or NULL (the first layer needs none).  v A is rounded to
- *        fp16 once before the base's gradient is added, as in the forward.
+ *   d_x  fp16 [M, K] or NULL (the first layer needs none), rounded once, as in the
+ *        forward.
  *   d_a  fp32 [L, r, K] and d_b fp32 [L, N, r], both or neither (NULL).  The
  *        gradients of an adapter without tokens are zero.  With accumulate != 0
  *        the sums are added to what the buffers hold (micro-batches; an adapter

@@ -1,4 +1,5 @@
-"""Adapters of many requests at the edges of what a call allows: plans that are shorter than the call's."""
+"""Adapters of many requests at the edges of what a call allows: plans that are shorter than the call's, terms that
+pass fp16's range or nearly cancel the base product."""
 import numpy as np
 import pytest
 import torch
@@ -40,3 +41,58 @@ def test_a_plan_that_ends_before_the_calls_is_not_read_past_its_head(M):
     assert (v == 7).all() and (d_a == 5).all() and (d_b == 5).all()
     m.q4gsw_adapters_fwd(*head(c), x)                              # the right plan still serves
     m.q4gsw_device_error_check()
+
+
+def exact_case(M, f32s, L=3, N=136, K=128, r=16):
+    """A base product of -8 times the first activation (forward) or gradient (backward), for every output, and adapters
+    whose terms are picked by the next two: integers, exact in every sum."""
+    m = q()
+    codes = np.full((N, K), 8, np.uint8)
+    codes[:, 0], codes[0, :] = 0, 0
+    scales = np.ones((K // 32, N), np.float32 if f32s else np.float16)
+    a, b = np.zeros((L, r, K), np.float16), np.zeros((L, N, r), np.float16)
+    ids = (np.arange(M) % (L + 1) - 1).astype(np.int32)
+    return m, m.q4gsw_prepack(cuda(codes), cuda(scales), 32), a, b, ids
+
+
+@pytest.mark.parametrize("f32s", [False, True])
+@pytest.mark.parametrize("M,gemm", [(M, None) for M in (1, 3, 8, 13, 16)] +
+                         [(M, g) for M in (17, 40, 300, 513, 700, 1100) for g in (None, "ts", "ss1", "ss2")])
+def test_a_term_that_leaves_the_range_of_fp16_or_cancels_the_base(M, gemm, f32s):
+    # every sum is exact in fp32 and every output an fp16 value, so that outputs are equal: 60000 + 8000 - 20000 = 48000
+    # (the residual with the term is 68000), and 40001 - 40000 = 1 (the term has 16 bits)
+    m, blob, a, b, ids = exact_case(M, f32s)
+    N, K, L, r = 136, 128, 3, 16
+    with_adapter = torch.from_numpy(ids >= 0).cuda()[:, None]
+    plan = m.q4gsw_adapters_plan(cuda(ids), L)
+    m.q4gsw_debug_pin_routes(gemm=gemm) if gemm else m.q4gsw_debug_pin_routes()
+    try:
+        # forward: rank 0 has the activation 1, rank 1 the activation 2
+        a[:, 0, 1], a[:, 1, 2] = 1, 1
+        for base, first, second, res, want, alone in ((2500, 200, 0, 60000, 48000, 40000), (5000, 1000, 1, None, 1, -40000)):
+            b[:, :, 0], b[:, :, 1] = 40, 1
+            x = np.zeros((M, K), np.float16)
+            x[:, 0], x[:, 1], x[:, 2] = base, first, second
+            rest = None if res is None else torch.full((M, N), float(res), device="cuda").half()
+            for y in (None, rest):       # and in the residual's own buffer
+                y = m.q4gsw_adapters_fwd(blob, N, K, 32, plan, cuda(a), cuda(b), cuda(x), residual=rest, y=y, f32s=f32s)
+                expect = torch.where(with_adapter, float(want), float(alone)).expand(M, N).clone()
+                expect[:, 0] = torch.where(with_adapter[:, 0], want, alone) - 8 * (first + second)     # (row 0 of the weight is -8 everywhere)
+                assert torch.equal(y.float(), expect.half().float()), (base, y[:, :3])
+                if res is None:
+                    break
+        # backward: rank 0 has the gradient 1, rank 1 the gradient 2
+        a[:], b[:] = 0, 0
+        b[:, 1, 0], b[:, 2, 1] = 1, 1
+        for base, first, second, want, alone in ((5000, 1000, 1, 1, -40000), (10000, 3000, 0, 40000, None)):
+            a[:, 0, :], a[:, 1, :] = 40, 1
+            d_y = np.zeros((M, N), np.float16)
+            d_y[:, 0], d_y[:, 1], d_y[:, 2] = base, first, second
+            d_x = m.q4gsw_adapters_bwd(blob, N, K, 32, plan, cuda(a), cuda(b), None, None, cuda(d_y), want_adapters=False, f32s=f32s)[0]
+            got = d_x[ids >= 0][:, 1:]           # (column 0 of the weight is -8 in every row)
+            assert torch.equal(got.float(), torch.full_like(got, want).float()), (base, d_x[:, :3])
+            if alone is not None:
+                got = d_x[ids < 0][:, 1:]
+                assert torch.equal(got.float(), torch.full_like(got, alone).float())
+    finally:
+        m.q4gsw_debug_pin_routes()

@@ -809,7 +809,12 @@ static cudaError_t down_form(cudaLaunchConfig_t& cfg, const __half* a, const __h
   return cudaLaunchKernelEx(&cfg, kernel, a, p, scale, ad.plan, out, M, ad.L, C, error);
 }
 
-bool adapters_few(const AdaptersRef& ad, int M) { return ma::plan_slots(M, ad.L) <= 64; }
+// Up to 256 tokens in at most 48 tiles.  On both sides (us of a whole call, few and down): 128
+// tokens of one adapter of 32, 4096 x 14336, rank 64 36.3 and 44.5, 256 46.6 and 49.7, 8192 x
+// 2048, rank 16 25.3 and 24.8; 512 tokens of eight adapters there 28.9 and 28.5, backward 35.6
+// and 33.1, 700 tokens 53.6 and 50.1; 96 tokens of as many adapters on 4096 x 14336, rank 64
+// 115 and 86, 48 75.6 and 62.1, 16 of 32 26.3 and 31.8.
+bool adapters_few(const AdaptersRef& ad, int M) { return M <= 256 && ma::plan_slots(M, ad.L) <= 48; }
 
 template <bool BY_ROWS, int RJ, int U, int W>
 static cudaError_t few_form(cudaLaunchConfig_t& cfg, const __half* act, const __half* proj, const float* scale,
@@ -877,14 +882,15 @@ cudaError_t launch_adapters_down(const AdaptersRef& ad, const uint16_t* act, boo
   const __half* p = reinterpret_cast<const __half*>(proj);
   if (adapters_few(ad, M)) return launch_adapters_few(ad, a, by_rows, p, scale, M, C, out, stream);
   const int groups = ma::plan_pairs(M, ad.L), sms = sm_count(current_device());
-  // contraction splits: about two CTAs per SM, two stages each at least, clusters of at most
-  // 8, by the pairs that are likely to be in use, half of the adapters' last ones (by all
-  // that may be: 1024 tokens over 64 adapters 23.3 us, 17.9 now; 256 over 6 of them 11.9 and 8.5)
-  const int last = ad.L + 1 < M / 16 ? ad.L + 1 : M / 16;
-  const int likely = M / 32 + last / 2 < groups ? M / 32 + last / 2 : groups;
+  // Contraction splits: two stages each at least, clusters of at most 8.  The pairs in use
+  // are at least M / 32 and at most `groups`, which of the two the host does not know: no
+  // more than two CTAs per SM by the least and four by the most.  Calls with 1, 2, 4, 8 splits (us,
+  // the choice in brackets), rank 64, 4096 x 4096: 128 tokens of as many adapters 67.7, 56.4,
+  // [54.1], 66.2, 256 of as many 77.9, [82.8], 92.6, 113, 256 of six of 64 adapters 41.0, 39.0,
+  // 32.3, [29.4], 1024 of 64 84.5, 74.6, [68.8], 75.5, 4096 of 16 191, [177], 184, 194.
   const int stages = (C + 127) / 128;
   int KS = 1;
-  while (KS < 8 && 2 * likely * KS <= 2 * sms && stages / (2 * KS) >= 2) KS *= 2;
+  while (KS < 8 && 2LL * KS * groups <= 4 * sms && 2LL * KS * (M / 32) <= 2 * sms && stages / (2 * KS) >= 2) KS *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(groups, KS, 1);
   cfg.blockDim = dim3(ma::kThreads, 1, 1);

@@ -222,7 +222,7 @@ const char* q4gsw_status_str(q4gsw_status s) {
     case Q4GSW_ERR_CUDA: return "CUDA runtime error";
     case Q4GSW_ERR_SIZE: return "buffer too small";
     case Q4GSW_ERR_TIMEOUT: return "a kernel wait ran out (results of the calls since the last check are invalid)";
-    case Q4GSW_ERR_INDEX: return "an embedding index was outside [0, N) (its row was written as zeros), or a teacher's token id outside [0, V) (taken as padding), or a token's adapter outside [-1, L) (taken as none), or a plan was of another batch size (nothing was computed)";
+    case Q4GSW_ERR_INDEX: return "an embedding index was outside [0, N) (its row was written as zeros), or a teacher's token id outside [0, V) (taken as padding), or a token's adapter outside [-1, L) (taken as none), or a plan was of another batch size (nothing was written)";
   }
   return "unknown status";
 }

@@ -59,14 +59,16 @@ __device__ __forceinline__ int ld_l2(const int32_t* p) {
   return v;
 }
 
-// The adapters of tokens 0 .. 15 (-1: none), by one warp, before griddepcontrol.wait: the plan
-// was complete before the kernel in front could start, as the activations were.
+// The adapters of tokens 0 .. 15 (-1: none; -2: the plan is not the call's, and nothing is
+// written), by one warp, before griddepcontrol.wait: the plan was complete before the
+// kernel in front could start, as the activations were.
 __device__ __forceinline__ void few_adapters(const EpiLow& o, int16_t* adapter) {
   const int lane = threadIdx.x & 31;
-  if (lane < 16) adapter[lane] = -1;
-  __syncwarp();
   const int head = ld_l2(o.plan + 1 + lane % 3);
-  if (__all_sync(0xffffffffu, head == (lane % 3 == 0 ? o.M : lane % 3 == 1 ? o.L : ma::kPlanMark))) {
+  const bool fits = __all_sync(0xffffffffu, head == (lane % 3 == 0 ? o.M : lane % 3 == 1 ? o.L : ma::kPlanMark));
+  if (lane < 16) adapter[lane] = fits ? -1 : -2;
+  __syncwarp();
+  if (fits) {
     const PlanView P = plan_view(const_cast<int32_t*>(o.plan), o.M, o.L);
     const int n = ma::kTileRows * ma::plan_slots(o.M, o.L);
 #pragma unroll 4
@@ -97,9 +99,10 @@ __device__ __forceinline__ void few_prefetch(const EpiLow& o, const int16_t* ada
 }
 
 // Columns c, c + 1 (c even; N % 8 == 0: both or neither are there) of token m with adapter
-// a (-1: none), whose sums are v.  What is read is on its way before the first use.
+// a (few_adapters), whose sums are v.  What is read is on its way before the first use.
 template <bool BY_ROWS>
 __device__ __forceinline__ void finish_pair(const EpiLow& o, int a, int m, int c, float2 v) {
+  if (a < -1) return;
   const size_t at = (size_t)m * o.N + c;
   const uint32_t bias = o.bias ? ld_u32(o.bias + c) : 0u, res = o.res ? ld_u32(o.res + at) : 0u;
   if (a >= 0) {

@@ -59,8 +59,8 @@ Q4GSW_API q4gsw_status q4gsw_adapters_plan(const int32_t *ids, int M, int L, voi
 /*
  * Forward, two launches (three for some numbers of tokens): x fp16 [M, K], a fp16 [L, r, K], b fp16 [L, N, r] ->
  * y fp16 [M, N], u fp32 [M, r] (what the backward pass reads; always written).
- *   plan      of the same M and L; with another one nothing is computed, and
- *             q4gsw_device_error_check returns Q4GSW_ERR_INDEX
+ *   plan      of the same M and L; with another one, also a shorter one, nothing is
+ *             written, and q4gsw_device_error_check returns Q4GSW_ERR_INDEX
  *   scale     fp32 [L] (4-byte aligned) or NULL (1 for every adapter)
  *   bias      fp16 [N] or NULL
  *   residual  fp16 [M, N] or NULL; y may be the residual's buffer (but not x's, also

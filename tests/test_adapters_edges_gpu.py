@@ -1,11 +1,11 @@
 """Adapters of many requests at the edges of what a call allows: plans that are shorter than the call's, terms that
-pass fp16's range or nearly cancel the base product."""
+pass fp16's range or nearly cancel the base product, plans of other batches."""
 import numpy as np
 import pytest
 import torch
 
 from helpers import cuda
-from test_adapters_gpu import head, make, q
+from test_adapters_gpu import check, head, make, q
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,35 @@ def test_a_term_that_leaves_the_range_of_fp16_or_cancels_the_base(M, gemm, f32s)
                 assert torch.equal(got.float(), torch.full_like(got, alone).float())
     finally:
         m.q4gsw_debug_pin_routes()
+
+
+@pytest.mark.parametrize("M,gemm", [(1, None), (5, None), (8, None), (16, None)] + [(M, g) for M in (17, 100, 600) for g in ("ts", "ss1", "ss2")])
+def test_with_the_plan_of_another_batch_no_output_is_written(M, gemm):
+    m = q()
+    N, K, gs, L, r = 136, 256, 32, 3, 16
+    c = make(M, N, K, gs, L, r, np.arange(M) % L)
+    blob, _, _, _, plan, a, b = head(c)
+    x, d_y, s = cuda(c["x"]), cuda(c["d_y"]), cuda(c["scale"])
+    u = m.q4gsw_adapters_fwd(blob, N, K, gs, plan, a, b, x, scale=s, save_u=True)[1]
+    res = torch.randn(M, N, device="cuda").half()
+    for other, its in ((M + 1, L), (M, L + 1)):
+        wrong = m.q4gsw_adapters_plan(torch.zeros(other, dtype=torch.int32, device="cuda"), its,
+                                      plan=torch.zeros(1 << 14, dtype=torch.int32, device="cuda"))
+        m.q4gsw_device_error_check()
+        m.q4gsw_debug_pin_routes(gemm=gemm) if gemm else m.q4gsw_debug_pin_routes()
+        try:
+            y = torch.full((M, N), 3.0, device="cuda").half()
+            for residual, out, before in ((None, y, y.clone()), (res, y, y.clone()), (res, res, res.clone())):
+                m.q4gsw_adapters_fwd(blob, N, K, gs, wrong, a, b, x, scale=s, residual=residual, y=out)
+                with pytest.raises(m.Q4gswError, match="INDEX"):
+                    m.q4gsw_device_error_check()
+                assert torch.equal(out, before)
+            d_x, v = torch.full((M, K), 3.0, device="cuda").half(), torch.full((M, r), 7.0, device="cuda")
+            d_a, d_b = torch.full((L, r, K), 5.0, device="cuda"), torch.full((L, N, r), 5.0, device="cuda")
+            m.q4gsw_adapters_bwd(blob, N, K, gs, wrong, a, b, x, u, d_y, scale=s, d_x=d_x, d_a=d_a, d_b=d_b, v=v)
+            with pytest.raises(m.Q4gswError, match="INDEX"):
+                m.q4gsw_device_error_check()
+            assert (d_x == 3).all() and (v == 7).all() and (d_a == 5).all() and (d_b == 5).all()
+        finally:
+            m.q4gsw_debug_pin_routes()
+    check(c, residual=res.cpu().numpy())                           # and the right plan still serves

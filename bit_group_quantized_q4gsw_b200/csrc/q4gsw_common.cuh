@@ -159,12 +159,30 @@ __device__ __forceinline__ uint4 lds128_u32addr(uint32_t addr) {
   return v;
 }
 
+// Coherent loads from L2, where all that earlier kernels wrote is once they are done, whatever
+// this SM's L1 holds: for what is read before griddep_wait.
+__device__ __forceinline__ uint2 ld_l2_v2(const void* p) {
+  uint2 v;
+  asm volatile("ld.relaxed.gpu.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_l2_u32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialization may start while the previous kernel of the stream drains.
 // `griddep_wait` blocks until that kernel has completed and its memory is
 // visible; everything a kernel reads that an earlier kernel may have written
 // (activations) or writes that an earlier kernel may read (outputs) comes
-// after it.  The packed weight is constant and may be read before it.
+// after it.  The packed weight is constant and may be read before it.  One
+// exception: a product behind an adapters' `few` or `down` kernel (EpiLow) reads its
+// activations and the plan before it.  That kernel calls griddep_launch_dependents
+// only behind its own wait, so that the kernels which wrote them were complete,
+// and their writes in L2, before the product started; it reads them from L2, by
+// TMA or ld_l2_*, never by the non-coherent path or from an L1 that may have older lines.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -211,10 +211,8 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
   } else {
     // ------------------------------------------------------------ consumers
     // outputs of this kernel may still be read by the previous one; a product that reads
-    // early waits in its epilogue, and makes sure here that no older line of x is in L1
-    // (x by TMA comes from L2)
+    // early waits in its epilogue
     if (!kReadsEarly<Out>) griddep_wait();
-    else if (!XS) __threadfence();
     const int w = warp & 3;             // 64-column block of every stage
     const int rt0 = (warp >> 2) * RTW;  // first row tile of this warp
     // per-thread shared-memory offsets inside a stage: 16-byte code chunk t of
@@ -245,7 +243,8 @@ q4gsw_gemv_fwd_tma_kernel(const __grid_constant__ CUtensorMap map_pk, const __gr
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[j][i] = in ? ldg_nc_v2(xrow[j] + kb + 16 * i) : make_uint2(0u, 0u);
+        for (int i = 0; i < 4; ++i)
+          d[j][i] = !in ? make_uint2(0u, 0u) : kReadsEarly<Out> ? ld_l2_v2(xrow[j] + kb + 16 * i) : ldg_nc_v2(xrow[j] + kb + 16 * i);
     };
     // scale words of block w: row (64 w + 16 SPG q) >> gsl of the stage's box
     // (stages start on multiples of 256 columns), the (even, odd) pair of pair

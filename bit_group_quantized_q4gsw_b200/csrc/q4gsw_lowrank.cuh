@@ -51,20 +51,12 @@ __device__ __forceinline__ bool plan_fits(const EpiLow& o) {
 }
 
 // ---------------------------------------------------------------- up to 16 tokens
-// A load from L2, which has what kernels that are done have written whatever this SM's L1
-// still holds: for what is read before griddepcontrol.wait.
-__device__ __forceinline__ int ld_l2(const int32_t* p) {
-  int v;
-  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-
 // The adapters of tokens 0 .. 15 (-1: none; -2: the plan is not the call's, and nothing is
 // written), by one warp, before griddepcontrol.wait: the plan was complete before the
 // kernel in front could start, as the activations were.
 __device__ __forceinline__ void few_adapters(const EpiLow& o, int16_t* adapter) {
   const int lane = threadIdx.x & 31;
-  const int head = ld_l2(o.plan + 1 + lane % 3);
+  const int head = (int)ld_l2_u32(o.plan + 1 + lane % 3);
   const bool fits = __all_sync(0xffffffffu, head == (lane % 3 == 0 ? o.M : lane % 3 == 1 ? o.L : ma::kPlanMark));
   if (lane < 16) adapter[lane] = fits ? -1 : -2;
   __syncwarp();
@@ -73,7 +65,7 @@ __device__ __forceinline__ void few_adapters(const EpiLow& o, int16_t* adapter) 
     const int n = ma::kTileRows * ma::plan_slots(o.M, o.L);
 #pragma unroll 4
     for (int i = lane; i < n; i += 32) {
-      const int m = ld_l2(P.rows + i), a = ld_l2(P.tile + i / ma::kTileRows);
+      const int m = (int)ld_l2_u32(P.rows + i), a = (int)ld_l2_u32(P.tile + i / ma::kTileRows);
       if (m >= 0) adapter[m] = (int16_t)(a >= 0 ? a : -1);
     }
   }

@@ -128,3 +128,43 @@ def test_with_the_plan_of_another_batch_no_output_is_written(M, gemm):
         finally:
             m.q4gsw_debug_pin_routes()
     check(c, residual=res.cpu().numpy())                           # and the right plan still serves
+
+
+@pytest.mark.parametrize("gemv", ["tma", "tma_xs"])
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 11, 16])
+def test_activations_and_plan_written_right_in_front_of_the_call(M, gemv):
+    # the product reads x and the plan before it waits for the kernel in front: both are rewritten, in their own buffers, by
+    # the kernels just before the call, many steps behind one another without a wait
+    m = q()
+    N, K, L, r = 520, 2048, 4, 16
+    c = make(M, N, K, 32, L, r, np.arange(M) % L)
+    blob, _, _, gs, _, a, b = head(c)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    hs = [torch.empty(M, K, device="cuda").normal_(0, 1, generator=g).half() for _ in range(5)]
+    ids = [torch.randint(-1, L, (M,), device="cuda", generator=g, dtype=torch.int32) for _ in range(7)]
+    w = torch.ones(K, device="cuda").half()
+    x, plan = torch.empty_like(hs[0]), torch.zeros_like(m.q4gsw_adapters_plan(ids[0], L))
+    m.q4gsw_debug_pin_routes(gemv=gemv)
+    try:
+        want = {}
+        for i in range(35):
+            y = m.q4gsw_adapters_fwd(blob, N, K, gs, m.q4gsw_adapters_plan(ids[i % 7], L), a, b, m.q4gsw_norms_fwd(hs[i % 5], w_pre=w)[0])
+            torch.cuda.synchronize()
+            want[i] = y
+        got = [torch.empty(M, N, device="cuda").half() for _ in range(35)]
+        wrong = torch.zeros((), device="cuda", dtype=torch.int64)
+        for _ in range(8):
+            for i in range(35):
+                if i % 2:
+                    m.q4gsw_norms_fwd(hs[i % 5], w_pre=w, x=x)
+                    m.q4gsw_adapters_plan(ids[i % 7], L, plan=plan)
+                else:
+                    m.q4gsw_adapters_plan(ids[i % 7], L, plan=plan)
+                    m.q4gsw_norms_fwd(hs[i % 5], w_pre=w, x=x)
+                m.q4gsw_adapters_fwd(blob, N, K, gs, plan, a, b, x, y=got[i])
+            for i in range(35):
+                wrong += (got[i] != want[i]).sum()
+        assert wrong.item() == 0
+    finally:
+        m.q4gsw_debug_pin_routes()
+    m.q4gsw_device_error_check()

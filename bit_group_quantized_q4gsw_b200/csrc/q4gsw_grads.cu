@@ -152,21 +152,28 @@ __device__ __forceinline__ double cta_sum(double v, double* s_part) {
   return s;
 }
 
-__device__ __forceinline__ float norm_of(double squares, float inv_scale) {
-  return (float)(fabs((double)inv_scale) * sqrt(squares));
+__device__ __forceinline__ double norm_of(double squares, float inv_scale) {
+  return fabs((double)inv_scale) * sqrt(squares);
 }
-__device__ __forceinline__ float total_norm(const double* part, int parts, float inv_scale, double* s_part) {
+__device__ __forceinline__ double total_norm(const double* part, int parts, float inv_scale, double* s_part) {
   double v = 0.;
   for (int i = threadIdx.x; i < parts; i += kThreads) v += part[i];
   return norm_of(cta_sum(v, s_part), inv_scale);
 }
 
 // inv_scale min(1, max_norm / (norm + 1e-6)), where min keeps a NaN and an infinite
-// max_norm never clips.
-__device__ __forceinline__ float clip_factor(float norm, float max_norm, float inv_scale) {
-  float clip = isinf(max_norm) && !isnan(norm) ? 1.f : max_norm / (norm + 1e-6f);
-  if (clip > 1.f) clip = 1.f;
-  return inv_scale * clip;
+// max_norm never clips: `first` times `second`, which is 1 but where the factor is near the
+// least normal fp32 number or below (it would lose its bits there, and a large gradient
+// times it is an ordinary number).
+struct Factor {
+  float first, second;
+};
+__device__ __forceinline__ Factor clip_factor(double norm, float max_norm, float inv_scale) {
+  double clip = isinf(max_norm) && !isnan(norm) ? 1. : (double)max_norm / (norm + 1e-6);
+  if (clip > 1.) clip = 1.;
+  const double f = (double)inv_scale * clip;
+  if (fabs(f) < 0x1p-100) return {(float)(f * 0x1p64), 0x1p-64f};
+  return {(float)f, 1.f};
 }
 
 // This CTA's run of pieces: its sum of squares, and its outputs.
@@ -192,9 +199,9 @@ __device__ __forceinline__ double run_squares(const Piece* table, int pieces, in
   });
   return sum;
 }
-__device__ __forceinline__ void run_scale(const Piece* table, int pieces, int run, float factor) {
+__device__ __forceinline__ void run_scale(const Piece* table, int pieces, int run, Factor factor) {
   for_pieces(table, pieces, run, [&](const Piece& e, int n) {
-    if (e.halves & 4 || (factor == 1.f && e.out == e.grad && e.halves != 1 && e.halves != 2)) return;
+    if (e.halves & 4 || (factor.first == 1.f && e.out == e.grad && e.halves != 1 && e.halves != 2)) return;
     const bool wide = (reinterpret_cast<uintptr_t>(e.out) & (e.halves & 2 ? 7u : 15u)) == 0;
     const int at = (int)threadIdx.x * kGroup;
     float v[kBatch][kGroup];
@@ -202,7 +209,7 @@ __device__ __forceinline__ void run_scale(const Piece* table, int pieces, int ru
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
 #pragma unroll
-      for (int i = 0; i < kGroup; ++i) v[k][i] *= factor;
+      for (int i = 0; i < kGroup; ++i) v[k][i] = v[k][i] * factor.first * factor.second;
       if (k < n) store_group(e, wide, at + k * kPiece, v[k]);
     }
   });
@@ -222,8 +229,8 @@ q4gsw_grad_few_kernel(const Piece* table, int pieces, float max_norm, float inv_
   cluster.sync();
   double squares = 0.;
   for (int k = 0; k < (int)gridDim.x; ++k) squares += *cluster.map_shared_rank(&s_sum, k);
-  const float n = norm_of(squares, inv_scale);
-  if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = n;
+  const double n = norm_of(squares, inv_scale);
+  if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)n;
   if (CLIP) run_scale(table, pieces, blockIdx.x, clip_factor(n, max_norm, inv_scale));
   cluster.sync();      // no CTA leaves while another reads its sum
 }
@@ -242,8 +249,8 @@ q4gsw_grad_norm_kernel(const double* part, int parts, float inv_scale, float* no
   __shared__ double s_part[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
-  const float n = total_norm(part, parts, inv_scale, s_part);
-  if (threadIdx.x == 0) norm[0] = n;
+  const double n = total_norm(part, parts, inv_scale, s_part);
+  if (threadIdx.x == 0) norm[0] = (float)n;
 }
 
 __global__ void __launch_bounds__(kThreads, 4)
@@ -252,8 +259,8 @@ q4gsw_grad_scale_kernel(const Piece* table, int pieces, const double* part, int 
   __shared__ double s_part[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
-  const float n = total_norm(part, parts, inv_scale, s_part);
-  if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = n;
+  const double n = total_norm(part, parts, inv_scale, s_part);
+  if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)n;
   run_scale(table, pieces, gridDim.x - 1 - blockIdx.x, clip_factor(n, max_norm, inv_scale));
 }
 

@@ -156,9 +156,11 @@ Q4GSW_API q4gsw_status q4gsw_norms_bwd(const uint16_t *h_out, const uint16_t *d_
  *
  *   norm = |inv_scale| sqrt(sum over all tensors and elements of g^2)
  *   out  = inv_scale min(1, max_norm / (norm + 1e-6)) g
- * inv_scale takes a loss scale out.  Squares are summed in fp64, so no finite
- * list overflows or underflows.  A norm of infinity gives factors of zero and a
- * norm of NaN factors of NaN, as the formula says: the caller looks at the norm.
+ * inv_scale takes a loss scale out.  Squares are summed in fp64 and the factor is
+ * taken from that sum, so no finite list overflows or underflows; a norm beyond fp32
+ * is returned as infinity, and its gradients are clipped all the same.  A gradient that is
+ * infinite gives factors of zero and one that is NaN factors of NaN, as the formula
+ * says: the caller looks at the norm.
  * ---------------------------------------------------------------------- */
 
 /* Bytes and host contents of the list's table: `count` tensors (1 <= count <=

@@ -56,8 +56,16 @@ def q4gsw_adapters_plan(ids, L: int, plan=None):
     nbytes = _plan_size(M, L)
     if plan is None:
         plan = _new(max(nbytes // 4, 4), _i32, index)
-    _call("q4gsw_adapters_plan", index, pi, M, L, _need(plan, "plan", _i32, (plan.numel(),), index), 4 * plan.numel())
+    pp, words = _sized(plan, "plan", _i32, index)
+    _call("q4gsw_adapters_plan", index, pi, M, L, pp, 4 * words)
     return plan
+
+
+def _sized(t, name: str, dtype, index: int):
+    """(pointer, elements) of a caller's buffer of any size."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return _need(t, name, dtype, (t.numel(),), index), t.numel()
 
 
 def _adapters(plan, a, b, scale, M: int, N: int, K: int, index: int):
@@ -249,8 +257,7 @@ def q4gsw_norms_bwd(h_out, d_x=None, d_h=None, block=None, w_post=None, gate=Non
             workspace = _new(nbytes, _u8, index)
             pws = workspace.data_ptr()
         else:
-            nbytes = workspace.numel()
-            pws = _need(workspace, "workspace", _u8, (nbytes,), index)
+            pws, nbytes = _sized(workspace, "workspace", _u8, index)
     _call("q4gsw_norms_bwd", index, ph, pdx, pdh, pblock, ppost, pgate, rows, residual_scale, ppre, weight_offset, eps, M,
           D, pr, pdb, pgr, pwe, pwo, pg, pws, nbytes)
     return NormsGrad(d_residual, d_block, d_gate, d_w_post, d_w_pre)
@@ -284,7 +291,13 @@ def _elements(t, name: str, index: int):
 
 def q4gsw_grad_set(grads, outs=None) -> GradSet:
     """A GradSet of gradients (fp32 or fp16 tensors of one device, any shapes).  `outs`, one tensor of as many elements
-    for each gradient, fp32 or fp16, receive the clipped values; without them the gradients are clipped in place."""
+    for each gradient, fp32 or fp16, receive the clipped values; without them the gradients are clipped in place, and
+    must not overlap one another, also where only their norm is asked for.
+
+    Make it once for buffers that stay where they are: it fills a record of 32 bytes for every 1024 elements on the
+    host (2 ms for 200 million elements, where a clip takes 0.1), copies them and waits for the current stream.  With
+    gradients that are allocated anew each step (zero_grad(set_to_none=True)) that is paid each step: keep the
+    buffers, or have their sums accumulated in them (set_to_none=False)."""
     grads = list(grads)
     if not grads:
         raise ValueError("grads is empty")
@@ -335,8 +348,7 @@ def _grad_call(name: str, grads: GradSet, head, norm, workspace):
     norm, pn = _out(norm, "norm", _f32, (1,), grads.index)
     pw, nbytes = None, 0
     if workspace is not None:
-        nbytes = workspace.numel()
-        pw = _need(workspace, "workspace", _u8, (nbytes,), grads.index)
+        pw, nbytes = _sized(workspace, "workspace", _u8, grads.index)
     elif grads.long:
         if _grad_bytes is None:
             _grad_bytes = int(library().q4gsw_grad_workspace_bytes())

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from helpers import cuda
-from test_adapters_gpu import check, head, make, q
+from oracle import q4gsw_adapters as oa
+from test_adapters_gpu import check, close, head, make, q
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +169,35 @@ def test_activations_and_plan_written_right_in_front_of_the_call(M, gemv):
     finally:
         m.q4gsw_debug_pin_routes()
     m.q4gsw_device_error_check()
+
+
+@pytest.mark.parametrize("M,L,N,K,r", [(1500, 1, 264, 320, 16), (3000, 2, 72, 128, 64), (2200, 3, 136, 64, 40)])
+def test_accumulate_with_the_tokens_split_over_a_cluster(M, L, N, K, r):
+    # few columns and many tokens of each adapter: the tokens' sums are added over a cluster's CTAs, then to the buffers
+    m = q()
+    c = make(M, N, K, 32, L, r, np.arange(M) * L // M)
+    args, x, d_y, s = head(c), cuda(c["x"]), cuda(c["d_y"]), cuda(c["scale"])
+    u = m.q4gsw_adapters_fwd(*args, x, scale=s, save_u=True)[1]
+    _, d_a, d_b = m.q4gsw_adapters_bwd(*args, x, u, d_y, scale=s, want_x=False)
+    want = oa.adapters_bwd(c["x"], u.cpu().numpy(), c["d_y"], c["w"], c["ids"], c["a"], c["b"], c["scale"])
+    close(d_a, want[1], "d_a")
+    close(d_b, want[2], "d_b")
+    ga, gb = torch.randn_like(d_a), torch.randn_like(d_b)
+    start = ga.clone(), gb.clone()
+    for k in range(1, 4):          # micro-batches: the same sums once more each time
+        m.q4gsw_adapters_bwd(*args, x, u, d_y, scale=s, want_x=False, d_a=ga, d_b=gb, accumulate=True)
+        for got, first, grad in ((ga, start[0], d_a), (gb, start[1], d_b)):
+            exact = first.double() + k * grad.double()
+            assert ((got - exact).abs() <= k * 2.0 ** -24 * (first.abs().double() + k * grad.abs().double())).all()
+
+
+def test_buffers_that_are_no_tensors_are_type_errors():
+    m = q()
+    ids = torch.zeros(4, dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError, match="plan"):
+        m.q4gsw_adapters_plan(ids, 2, plan=[0] * 64)
+    x = torch.ones(2, 64, device="cuda").half()
+    with pytest.raises(TypeError, match="workspace"):
+        m.q4gsw_norms_bwd(x, d_x=x, w_pre=x[0], want_weights=True, workspace=b"0" * 4096)
+    with pytest.raises(TypeError, match="workspace"):
+        m.q4gsw_grad_norm(m.q4gsw_grad_set([torch.ones(200000, device="cuda")]), workspace=np.zeros(1 << 16, np.uint8))

@@ -507,9 +507,9 @@ q4gsw_adapters_few_kernel(const __half* act, const __half* proj, const float* sc
 // rank's q of a chunk is divided by a power of two near its largest value and split
 // into two fp16 parts, once for all warps, and the chunk's sums are scaled back when
 // they are added to the fp32 registers: 2^-23 of the largest q of the chunk is lost, no
-// range, and the tensor cores' own sums are two steps long.  The Z CTAs of a cluster
-// take every Z-th chunk, and their sums are added through distributed shared memory in
-// rank order.
+// range, and the tensor cores' own sums are four products long (two steps of tokens of both
+// parts).  The Z CTAs of a cluster take every Z-th chunk, and their sums are added through
+// distributed shared memory in rank order.
 //
 // 1021 tokens of four adapters, 4096 and 14336 columns, rank 64: 24.2 us (the bytes alone
 // 8.6); 512 of eight, 8192 and 2048, rank 16: 8.7.  Bound by the steps of a chunk (three

@@ -178,11 +178,12 @@ __device__ __forceinline__ uint32_t ld_l2_u32(const void* p) {
 // visible; everything a kernel reads that an earlier kernel may have written
 // (activations) or writes that an earlier kernel may read (outputs) comes
 // after it.  The packed weight is constant and may be read before it.  One
-// exception: a product behind an adapters' `few` or `down` kernel (EpiLow) reads its
-// activations and the plan before it.  That kernel calls griddep_launch_dependents
-// only behind its own wait, so that the kernels which wrote them were complete,
-// and their writes in L2, before the product started; it reads them from L2, by
-// TMA or ld_l2_*, never by the non-coherent path or from an L1 that may have older lines.
+// exception: the product of an adapters' call (EpiLow) reads its activations and, up to 16
+// tokens, the plan before it.  The first kernel of such a call (`few` or `down`) calls
+// griddep_launch_dependents only behind its own wait, so that the kernels which wrote them
+// were complete, and their writes in L2, before the product could start; it reads them from
+// L2, by TMA or ld_l2_*, never by the non-coherent path or from an L1 that may have older
+// lines.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

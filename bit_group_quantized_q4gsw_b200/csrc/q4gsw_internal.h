@@ -85,10 +85,9 @@ struct Epi {
 // The same of a product with an adapter for every token (q4gsw_lowrank.cuh):
 //   y[m, n] = v + scale[a] sum_j inter[m, j] P_a(n, j) + bias[n] + res[m, n]
 // for the tokens with an adapter a in the plan.  mat: [L, N, r], or [L, r, N] for the
-// input gradient; scale may be null.  The product's activations were complete before the
-// kernel in front of it could start (that kernel lets its successors start only behind
-// its own wait), so they are read at once, and only the epilogue waits for that
-// kernel, which writes inter.
+// input gradient; scale may be null.  The product's activations were complete before it
+// could start (griddep_wait), so they are read at once, and only the epilogue waits for
+// the kernel in front, behind which inter has been written.
 struct EpiLow {
   __half* y;
   const __half* bias;

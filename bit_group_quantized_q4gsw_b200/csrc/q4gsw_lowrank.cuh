@@ -143,17 +143,16 @@ __device__ __forceinline__ void finish_pair(const EpiLow& o, int a, int m, int c
 // ---------------------------------------------------------------- tiles
 // A GEMM with this epilogue has two more warps than without.  While the others are in
 // the main loop they find which tokens of the CTA's output have which adapter (find); the
-// epilogue then adds the term to the parked sums of up to 128 tokens at a time, a group of
-// tokens of one adapter after the other (add_terms).
+// epilogue then adds the term to the parked sums of up to 128 or 256 tokens at a time
+// (add_terms).
 constexpr int kFindWarps = 2;
 constexpr int kChunk = 128;
-// Two lists of groups of up to 16 tokens of one adapter.
+// Two lists of tokens with an adapter, those of one side by side.
 struct Groups {
-  uint32_t count[2];                   // groups << 16 | tokens
+  int count[2];                        // tokens
   int fits;                            // the plan is the call's
+  float factor[2][kChunk];
   int16_t adapter[2][kChunk];
-  unsigned char first[2][kChunk];      // a group's first token in `row`
-  unsigned char tokens[2][kChunk];
   unsigned char row[2][kChunk];        // from the first token of the list's range on
 };
 struct Ranges {
@@ -194,12 +193,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
 
-// The groups of both ranges, by the threads `tid` = 0 .. 63 (whole warps) of a CTA that has
+// The lists of both ranges, by the threads `tid` = 0 .. 63 (whole warps) of a CTA that has
 // set count and fits to zero behind a barrier.  A plan's order has the tokens of an
 // adapter in their own order, so those of a range stand side by side: `lanes` lanes search
 // the ends of that run, each step narrows it lanes + 1 times, two adapters at once.
-// Which group stands where depends on the order of atomics, the results do not: every
-// value of the output belongs to one group.
+// Which adapter stands where depends on the order of atomics, the results do not: every
+// value of the output is one adapter's.
 __device__ __forceinline__ void find(const EpiLow& o, Groups* s, const Ranges& range, int tid) {
   constexpr int kSearch = 32 * kFindWarps, A = 2;
   griddep_wait();
@@ -247,24 +246,23 @@ __device__ __forceinline__ void find(const EpiLow& o, Groups* s, const Ranges& r
     for (int i = 0; i < A; ++i)
 #pragma unroll
       for (int l = 0; l < 2; ++l) {
-        const int from = lo[i][2 * l], tokens = max(0, lo[i][2 * l + 1] - from), groups = (tokens + 15) / 16;
-        uint32_t place = 0;
-        if (sub == 0 && tokens) {
-          place = atomicAdd(&s->count[l], (uint32_t)groups << 16 | (uint32_t)tokens);
-          for (int k = 0; k < groups; ++k) {
-            s->first[l][(place >> 16) + k] = (unsigned char)((place & 0xffffu) + 16 * k);
-            s->tokens[l][(place >> 16) + k] = (unsigned char)min(16, tokens - 16 * k);
-            s->adapter[l][(place >> 16) + k] = (int16_t)(a0 + i * step);
-          }
-        }
-        place = __shfl_sync(0xffffffffu, place, lane - sub) & 0xffffu;
+        const int from = lo[i][2 * l], tokens = max(0, lo[i][2 * l + 1] - from), a = a0 + i * step;
+        int place = 0;
+        if (sub == 0 && tokens) place = atomicAdd(&s->count[l], tokens);
+        place = __shfl_sync(0xffffffffu, place, lane - sub);
+        const float f = o.scale && tokens ? __uint_as_float(ld_u32(o.scale + a)) : 1.f;
         for (int k = sub; k < tokens; k += 4 * lanes) {
           int token[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) token[e] = k + e * lanes < tokens ? ld_int(P.order + from + k + e * lanes) : 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (k + e * lanes < tokens) s->row[l][place + k + e * lanes] = (unsigned char)(token[e] - key[2 * l]);
+            if (k + e * lanes < tokens) {
+              const int at = place + k + e * lanes;
+              s->row[l][at] = (unsigned char)(token[e] - key[2 * l]);
+              s->adapter[l][at] = (int16_t)a;
+              s->factor[l][at] = f;
+            }
         }
       }
   }
@@ -288,34 +286,40 @@ __device__ __forceinline__ float4 add_parts(int S, Part&& part) {
   return acc;
 }
 
-// Adds the low-rank term of list `l` (and, where both_lists and `two`, of the next) to the sums of
-// tokens m0 .. m0 + rows - 1 (the lists' ranges, the second kChunk behind the first), columns c0 ..
-// of COLS, in shared memory: at(row, column) is the address of four columns' sums, side by side.  All THREADS threads of the CTA, with a barrier between what they
+// Adds the low-rank term of list `l` (and, where both_lists and `two`, of the next) to the sums
+// of the `rows` tokens from the list's range on (the second range kChunk behind the first),
+// columns c0 .. of COLS, in shared memory: at(row, column) is the address of four columns'
+// sums, side by side.  All THREADS threads of the CTA, with a barrier between what they
 // parked and this (and `stage` before that); one ends it.
 //
 // inter goes to the tensor cores as two fp16 parts over a power of two with the row's
-// largest value in [1, 2): 2^-23 of that value is lost.  The rows of a group lie anywhere
-// in the chunk (ldmatrix takes each row's address).  A warp has 8 J columns and a share of
-// the groups, one behind the other: groups of one adapter share the matrix's fragments,
-// which it takes from L2 into registers.
+// largest value in [1, 2): 2^-23 of that value is lost.  A warp has 16 columns and a share
+// of the lists, 16 tokens at a time, whose rows lie anywhere in the chunk (ldmatrix takes each
+// row's address).  For each adapter of the 16 the other tokens' rows are zeros, and the
+// sums of its own rows alone are taken (an infinite matrix times zeros is none of the
+// others' business).  Adapters that follow each other share the matrix's fragments, which
+// come from L2 into registers.
 //
 // The order of the ranks in the contraction is free: lane t of a quad has the r / 4 ranks
 // from t r / 4 on, four of them in each step, so that a row of B [N, r] comes in vectors.
-// The order of the columns is, too: column n of the j-th eight is 2 J (n / 2) + 2 j + n % 2,
-// and a lane then has the sums of 2 J columns side by side.
+// The order of the columns is, too: column n of the j-th eight is 2 n + j.  A lane then
+// reads two columns of a row of A [r, K] at once, and has the sums of four columns side by
+// side.
 //
-// 512 tokens of eight adapters, rank 16, 8192 x 2048: 3 us of a call's 29; 4096 tokens of 16,
-// rank 64, 14336 x 4096: 95 of 507, of which the tensor cores' part is 60 (49 as a kernel of its
-// own, and the output through memory once more).  Bound by latency: cold code, a few loads and
-// short chains with four warps a scheduler.  So it has no long unrolled loops and no spills (what
-// the GEMM leaves of L1 does not hold them: twice as many columns a warp with 84 bytes of them
-// 531 us); outputs written from here in pieces of 32 bytes a row took 518.
+// 512 tokens of eight adapters, rank 16, 8192 x 2048: 4 us of a call's 30.5; 4096 tokens of 16,
+// rank 64, 14336 x 4096: 100 of 515, of which the tensor cores' part is 60 (49 as a kernel of its
+// own, and the output through memory once more).  Bound by issued instructions and short
+// chains: cold code, a few loads, four warps a scheduler.  So it has no long unrolled loops
+// and no spills (what the GEMM leaves of L1 does not hold them: twice as many columns a warp with
+// 84 bytes of them 531 us); outputs written from here in pieces of 32 bytes a row took 518,
+// the next adapter's matrix in registers ahead of its use 550.
+// 1024 scattered tokens of 64 adapters, some 56 to a chunk, rank 16: 97 us on 8192 x 2048, 160 on
+// 4096 x 14336, backward 93 and 330 (112, 175, 113, 392 with 16 rows for each adapter): an
+// adapter's matrix is taken again for every chunk of 128 tokens.
 template <bool BY_ROWS, int COLS, int THREADS, class At>
 __device__ __forceinline__ void add_terms(const EpiLow& o, const Groups* q, int l, bool two, Scratch* s, int rows,
                                           int c0, const At& at) {
-  constexpr int STEPS = 4, J = BY_ROWS && COLS == 128 ? 4 : 2;
-  constexpr int WARPS = THREADS / 32, BLOCKS = COLS / (8 * J), SHARES = WARPS / BLOCKS;
-  const int groups0 = (int)(q->count[l] >> 16), groups = groups0 + (two ? (int)(q->count[1] >> 16) : 0);
+  constexpr int WARPS = THREADS / 32, BLOCKS = COLS / 16, SHARES = WARPS / BLOCKS, STEPS = 4;
   // (volatile: what follows from it is computed here, not kept in registers around the loop
   // over chunks)
   int tid;
@@ -324,21 +328,21 @@ __device__ __forceinline__ void add_terms(const EpiLow& o, const Groups* q, int 
   const int g = lane >> 2, t = lane & 3;
   const int per = o.r / 4;                           // ranks of a lane
   const int block = warp % BLOCKS, share = warp / BLOCKS;
-  const int base = c0 + 8 * J * block;
+  const int base = c0 + 16 * block;
+  // batches of 16 tokens, of the first list and of the second
+  const int batches0 = (q->count[l] + 15) / 16, batches = batches0 + (two ? (q->count[1] + 15) / 16 : 0);
   const bool works = share < SHARES && base < o.N;
-  const int begin = works ? share * groups / SHARES : 0, end = works ? (share + 1) * groups / SHARES : 0;
-  uint32_t bf[STEPS][J][2];                          // the matrix
-  float f = 1.f;
+  const int begin = works ? share * batches / SHARES : 0, end = works ? (share + 1) * batches / SHARES : 0;
+  uint32_t bf[STEPS][2][2];                          // the matrix: [step of 16 ranks][eight columns]
   int mine = -1;
   auto fetch = [&](int a) {
     mine = a;
-    f = o.scale ? __uint_as_float(ld_u32(o.scale + a)) : 1.f;
     const __half* mat = o.mat + (size_t)a * o.r * o.N;
+    const int c = base + 2 * g < o.N ? base + 2 * g : base;      // N % 8 == 0: both columns or none
     if (BY_ROWS) {
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int c = base + 2 * J * (g >> 1) + 2 * j + (g & 1);
-        const __half* p = mat + (size_t)(c < o.N ? c : base) * o.r + t * per;
+      for (int j = 0; j < 2; ++j) {
+        const __half* p = mat + (size_t)(c + j) * o.r + t * per;
         uint32_t w[2 * STEPS];
         if (per % 8 == 0) {                          // vectors of what the rank's alignment allows
 #pragma unroll
@@ -360,38 +364,35 @@ __device__ __forceinline__ void add_terms(const EpiLow& o, const Groups* q, int 
         for (int k = 0; k < STEPS; ++k) bf[k][j][0] = w[2 * k], bf[k][j][1] = w[2 * k + 1];
       }
     } else {
-      const int c = base + 2 * J * (g >> 1);
-      const __half* p = mat + (size_t)(t * per) * o.N + (c < o.N ? c : base);
-      const uint32_t sel = g & 1 ? 0x7632u : 0x5410u;
+      const __half* p = mat + (size_t)(t * per) * o.N + c;
+      // ranks up to 32 and the rest, all on their way before the first is used
+      const bool rest = per > 8;
+      uint32_t w[2][8];
+      auto load = [&](int x) {
 #pragma unroll
-      for (int k = 0; k < STEPS; ++k) {
-        uint32_t w[4][J];                            // N % 8 == 0: all 2 J columns or none
+        for (int e = 0; e < 8; ++e)
+          w[x][e] = 8 * x + e < per ? *reinterpret_cast<const uint32_t*>(p + (size_t)(8 * x + e) * o.N) : 0u;
+      };
+      auto turn = [&](int x) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __half* from = p + (size_t)(4 * k + e) * o.N;
-          const bool in = 4 * k + e < per;
-          if constexpr (J == 4) {
-            const uint4 x = in ? *reinterpret_cast<const uint4*>(from) : make_uint4(0u, 0u, 0u, 0u);
-            w[e][0] = x.x, w[e][1] = x.y, w[e][2] = x.z, w[e][3] = x.w;
-          } else {
-            const uint2 x = in ? *reinterpret_cast<const uint2*>(from) : make_uint2(0u, 0u);
-            w[e][0] = x.x, w[e][1] = x.y;
-          }
-        }
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          bf[k][j][0] = prmt(w[0][j], w[1][j], sel);
-          bf[k][j][1] = prmt(w[2][j], w[3][j], sel);
-        }
-      }
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              bf[2 * x + k][j][e] = prmt(w[x][4 * k + 2 * e], w[x][4 * k + 2 * e + 1], j ? 0x7632u : 0x5410u);
+      };
+      load(0);
+      if (rest) load(1);
+      turn(0);
+      if (rest) turn(1);
     }
   };
   if (tid < kZeroBytes / 4) reinterpret_cast<uint32_t*>(s->zeros)[tid] = 0u;
   cp_async_wait<0>();
   __syncthreads();
-  if (groups == 0) return;
-  auto list_of = [&](int i) { return i < groups0 ? l : 1; };
-  if (begin < end) fetch(q->adapter[list_of(begin)][begin - (begin < groups0 ? 0 : groups0)]);
+  if (batches == 0) return;
+  if (begin < end) fetch(begin < batches0 ? q->adapter[l][16 * begin] : q->adapter[1][16 * (begin - batches0)]);
   // ranks 2 sub, 2 sub + 1 of a row in a thread, 8, 16 or 32 lanes to a row, which is replaced
   // by its parts: rank t per + e stands where step e / 4 has it, and behind the ranks zeros
   // fill the last step
@@ -422,46 +423,53 @@ __device__ __forceinline__ void add_terms(const EpiLow& o, const Groups* q, int 
   }
   __syncthreads();
   const uint32_t parts = (uint32_t)__cvta_generic_to_shared(s->inter), zeros = (uint32_t)__cvta_generic_to_shared(s->zeros);
-  constexpr int SETS = J == 2 ? 2 : 1;               // four chains of products at least
 #pragma unroll 1
   for (int i = begin; i < end; ++i) {
-    const int list = list_of(i), of = i < groups0 ? i : i - groups0;
-    const int a = q->adapter[list][of], first = q->first[list][of], tokens = q->tokens[list][of];
-    auto row_of = [&](int k) { return k < tokens ? (int)q->row[list][first + k] + (list - l) * kChunk : -1; };
-    if (a != mine) fetch(a);
-    const int theirs = row_of(lane & 15);
-    const uint32_t from = (theirs < 0 ? zeros : parts + theirs * pitch) + 16 * (lane >> 4);
-    float acc[SETS][J][4];
+    const int list = i < batches0 ? l : 1, p0 = 16 * (i < batches0 ? i : i - batches0), p = p0 + (lane & 15);
+    const bool in = p < q->count[list];
+    const int a_of = in ? q->adapter[list][p] : -1, row_of = in ? q->row[list][p] + (list - l) * kChunk : 0;
+    const uint32_t from = parts + row_of * pitch + 16 * (lane >> 4);
+    float sum[2][4];                                 // of eight columns each
+    uint32_t todo = __ballot_sync(0xffffffffu, in) & 0xffffu;
+#pragma unroll 1
+    while (todo) {
+      const int a = __shfl_sync(0xffffffffu, a_of, __ffs(todo) - 1);
+      const uint32_t theirs = __ballot_sync(0xffffffffu, a_of == a) & 0xffffu;
+      todo &= ~theirs;
+      if (a != mine) fetch(a);
+      const uint32_t rows16 = theirs >> (lane & 15) & 1u ? from : zeros;
+      float acc[2][2][4];                            // of the two parts
 #pragma unroll
-    for (int x = 0; x < SETS * J; ++x)
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[x / J][x % J][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[x / 2][x % 2][e] = 0.f;
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-      if (4 * k >= per) break;
-      uint32_t af[2][4];
-      ldmatrix4(af[1], from + lo + 32 * k);
-      ldmatrix4(af[0], from + 32 * k);
+      for (int k = 0; k < STEPS; ++k) {
+        if (4 * k >= per) break;
+        uint32_t af[2][4];
+        ldmatrix4(af[1], rows16 + lo + 32 * k);
+        ldmatrix4(af[0], rows16 + 32 * k);
 #pragma unroll
-      for (int x = 2 * J - 1; x >= 0; --x) mma_16816(acc[SETS == 2 ? x / J : 0][x % J], af[x / J], bf[k][x % J]);
+        for (int x = 3; x >= 0; --x) mma_16816(acc[x / 2][x % 2], af[x / 2], bf[k][x % 2]);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (theirs >> (g + 8 * h) & 1u) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) sum[j][2 * h + e] = acc[0][j][2 * h + e] + acc[1][j][2 * h + e];
+        }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = row_of(g + 8 * h);
-      if (row < 0) continue;
-      const float back = s->back[row];
-#pragma unroll
-      for (int x = 0; x < J / 2; ++x) {              // four columns
-        if (base + 2 * J * t + 4 * x >= o.N) break;
-        const uint32_t to = at(row, 8 * J * block + 2 * J * t + 4 * x);
-        const float4 y = sm100::ld_shared_f4(to);
-        auto term = [&](int j, int e) {
-          const float v = acc[0][2 * x + j][2 * h + e];
-          return back * (SETS == 2 ? v + acc[SETS - 1][2 * x + j][2 * h + e] : v);
-        };
-        sm100::st_shared_f4(to, make_float4(fmaf(f, term(0, 0), y.x), fmaf(f, term(0, 1), y.y),
-                                            fmaf(f, term(1, 0), y.z), fmaf(f, term(1, 1), y.w)));
-      }
+      const int row = __shfl_sync(0xffffffffu, row_of, g + 8 * h);
+      if (p0 + g + 8 * h >= q->count[list] || base + 4 * t >= o.N) continue;
+      const float back = s->back[row], f = q->factor[list][p0 + g + 8 * h];
+      const uint32_t to = at(row, 16 * block + 4 * t);
+      const float4 y = sm100::ld_shared_f4(to);
+      sm100::st_shared_f4(to, make_float4(fmaf(f, back * sum[0][2 * h], y.x), fmaf(f, back * sum[1][2 * h], y.y),
+                                          fmaf(f, back * sum[0][2 * h + 1], y.z), fmaf(f, back * sum[1][2 * h + 1], y.w)));
     }
   }
   __syncthreads();

@@ -427,8 +427,13 @@ q4gsw_adapters_down_kernel(const __half* act, const __half* proj, const float* s
 // CTA writes to every other's shared memory, added in rank order).
 //
 // W warps: eight, or four beside the product of up to 16 tokens (launch_adapters_few).
+// The registers are kept to three CTAs an SM where a warp has one chunk and the rank is at
+// most 16: with the columns of x forward that spills (100 bytes a thread of stores with rank
+// 8, 40 with 16) and is still the faster where the tiles are many (three, two, one CTA an SM,
+// us of a whole call on 8192 x 2048, rank 8: 48 tokens of as many adapters 22.9, 24.0, 27.0;
+// 256 tokens of 31 27.6, 28.3, 30.4; 256 of 8 24.7, 24.3, 25.2; 32 of 8 16.1, 16.0, 15.9).
 template <bool BY_ROWS, int RJ, int U, int W>
-__global__ void __launch_bounds__(32 * W, W == 4 && RJ <= 2 ? (U == 1 ? 6 : 4) : U == 1 && RJ <= 2 ? 3 : 1)
+__global__ void __launch_bounds__(32 * W, W == 4 ? 4 : U == 1 && RJ <= 2 ? 3 : 1)
 q4gsw_adapters_few_kernel(const __half* act, const __half* proj, const float* scale, const int32_t* plan, float* out,
                           int M, int L, int C, unsigned int* error) {
   constexpr int R = 8 * RJ;

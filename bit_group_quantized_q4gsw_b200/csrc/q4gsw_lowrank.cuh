@@ -310,8 +310,9 @@ __device__ __forceinline__ float4 add_parts(int S, Part&& part) {
 // rank 64, 14336 x 4096: 100 of 515, of which the tensor cores' part is 60 (49 as a kernel of its
 // own, and the output through memory once more).  Bound by issued instructions and short
 // chains: cold code, a few loads, four warps a scheduler.  So it has no long unrolled loops
-// and no spills (what the GEMM leaves of L1 does not hold them: twice as many columns a warp with
-// 84 bytes of them 531 us); outputs written from here in pieces of 32 bytes a row took 518,
+// and next to no spills (what the GEMM leaves of L1 does not hold them: 4 bytes a thread in the
+// forward GEMM, 72 in the backward one, which has 24 without the term; twice as many columns a
+// warp with 84 bytes of them 531 us); outputs written from here in pieces of 32 bytes a row took 518,
 // the next adapter's matrix in registers ahead of its use 550.
 // 1024 scattered tokens of 64 adapters, some 56 to a chunk, rank 16: 97 us on 8192 x 2048, 160 on
 // 4096 x 14336, backward 93 and 330 (112, 175, 113, 392 with 16 rows for each adapter): an

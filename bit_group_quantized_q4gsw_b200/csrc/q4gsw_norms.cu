@@ -473,7 +473,13 @@ constexpr int kMaxRing = 208 * 1024;
 // backward pass, whose registers hold the columns' weights then (4096 x 4096: 44.1 us,
 // 50.4 with two); two in the forward from 2^21 features on (4096 x 4096: 24.5 us, 28.4
 // with one); four beyond 8192 features (1000 x 16384: forward 27.3 us, 36.8 with two;
-// backward 61.0 and 65.7).
+// backward 60.9 and 65.7).  Beyond 8192 features the backward pass keeps four vectors of
+// three rows and their weights and spills: 152 to 172 bytes a thread of stores with 512
+// threads, 624 to 712 with 1024, and 1296 to 2692 with the sums, whose columns it holds
+// too; with the sums 1024 threads of one vector spill 208 to 220.  1000 rows, backward
+// and with all three sums (us; the floor of both in brackets): 4096 features 13.0 and
+// 19.0 (7.5), 8192 24.1 and 47.5 (15), 12288 49.6 and 88.0 (22.5), 16384 60.9 and 124
+// (30), 32768 213 and 390 (60).
 struct Shape {
   int vec, tpr;
 };
